@@ -150,7 +150,7 @@ def _quantize(x):
     """Codes, scale and lowest value (float16) of the rows of x (..., D) in fp32."""
     x = x.float().clamp(-65504.0, 65504.0)
     low, high = x.amin(-1), x.amax(-1)
-    scale = ((high - low) / 15.0).half()
+    scale = ((high - low) / torch.full_like(low, 15.0)).half()
     low = low.half()
     s = scale.float()[..., None]
     codes = torch.where(s > 0, (x - low.float()[..., None]) / s, torch.zeros_like(x))
