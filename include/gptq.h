@@ -66,8 +66,9 @@ uint64_t gptq_launch_count(void);
 
 /*
  * Synchronizes `stream`, then reads and clears the library's device error word,
- * which kernels raise when a bounded on-device wait gives up (GPTQ_ERR_TIMEOUT) or
- * when they meet a NaN or an Inf they cannot report otherwise (GPTQ_ERR_NONFINITE).
+ * which kernels raise when a bounded on-device wait gives up (GPTQ_ERR_TIMEOUT),
+ * when they meet a NaN or an Inf they cannot report otherwise (GPTQ_ERR_NONFINITE) or
+ * when an index array holds a value out of its range (GPTQ_ERR_INVALID_ARG).
  * The word is shared by all calls on the current device.
  */
 gptq_status gptq_device_check(gptq_stream_t stream);
@@ -417,6 +418,151 @@ gptq_status gptq_gemm_f32(int engine, int a_kmajor, int b_kmajor, int64_t M, int
  * return GPTQ_ERR_INVALID_ARG before any launch.
  */
 gptq_status gptq_wait_selftest(int which, int64_t limit_ns, gptq_stream_t stream);
+
+/* Element types of the serving calls below. */
+enum { GPTQ_F32 = 0, GPTQ_BF16 = 1, GPTQ_F16 = 2 };
+
+/*
+ * Serving: what a decoder block needs between and beside its packed projections
+ * (gptq_adapter_linear, gptq_qk_norm_rope, gptq_kv_append, gptq_kv_read,
+ * gptq_kv_attention). All are asynchronous on `stream`, allocate nothing and check their
+ * arguments before any launch. Index arrays live on the device, so their VALUES are
+ * checked by the kernels: a value out of its documented range is never used as an
+ * address; the kernel skips that element and gptq_device_check() then returns
+ * GPTQ_ERR_INVALID_ARG.
+ */
+
+/*
+ * A packed projection with the low-rank adapters of many requests beside it:
+ *
+ *   Y[t] = X[t] W_hat^T + alpha[a] * (X[t] A[a]^T) B[a]^T,   a = ids[t]
+ *
+ * with W_hat as in gptq_dequant_gemm (natural groups). Tokens of a decoding batch may each
+ * have their own adapter; a prompt's tokens share one.
+ *
+ *   qweight, scales, zeros, m, d, bits, group_size  the packed layer; qweight 16-byte
+ *              aligned for 4 and 8 bits, 8-byte for 2.
+ *   X          device bf16 bits, T x d, row stride ldx (ldx % 8 == 0, 16-byte aligned).
+ *   A, B       device bf16 bits, n_adapters x rank x d and n_adapters x m x rank, dense,
+ *              16-byte aligned. rank a multiple of 8 in [8, 128].
+ *   alpha      device fp32[n_adapters], or NULL for 1.
+ *   ids        device int32[T]: the token's adapter in [0, n_adapters), or negative for
+ *              none, in any order. May be NULL with n_adapters 0 (no adapters at all).
+ *   Y          device, T x m, row stride ldy >= m: fp32 (y_dtype GPTQ_F32) or bf16 rounded
+ *              to nearest even (GPTQ_BF16). Sums are fp32.
+ *   ws         device workspace of gptq_adapter_workspace_size() bytes, 256-byte aligned;
+ *              its contents on entry do not matter.
+ */
+size_t gptq_adapter_workspace_size(int64_t m, int64_t d, int bits, int group_size, int64_t T,
+                                   int rank);
+gptq_status gptq_adapter_linear(const uint32_t* qweight, const float* scales, const float* zeros,
+                                int64_t m, int64_t d, int bits, int group_size, const uint16_t* X,
+                                int64_t T, int64_t ldx, const uint16_t* A, const uint16_t* B,
+                                const float* alpha, int64_t n_adapters, int rank,
+                                const int32_t* ids, void* Y, int y_dtype, int64_t ldy, void* ws,
+                                size_t ws_bytes, gptq_stream_t stream);
+
+/*
+ * The RMS norm of every query and key head and the position rotation, in one pass:
+ *
+ *   n = x * rsqrt(mean(x^2) + eps) * w          over a head's head_dim values (w NULL: n = x)
+ *   (n_i, n_j) -> (n_i c - n_j s, n_j c + n_i s)   c, s = cos/sin_table[positions[t]][i]
+ *
+ * for i < rot_dim / 2, with j = i + rot_dim / 2, or the pairs (2 i, 2 i + 1) when
+ * `interleaved`; the values from rot_dim on are not rotated. Arithmetic is fp32, rounded
+ * once to the output's type.
+ *
+ *   Q, K       device, T x n_heads x head_dim of in_dtype (GPTQ_F32, _BF16 or _F16): heads
+ *              dense, token stride ldq / ldk elements (slices of a fused projection's
+ *              output), rows 16-byte aligned. n_k_heads may be 0 (K, Ko ignored).
+ *   head_dim   a multiple of 8 in [8, 256].
+ *   wq, wk     device fp32[head_dim], or NULL for no norm.
+ *   cos_table, sin_table  device fp32, n_positions x rot_dim / 2.
+ *   rot_dim    0 (no rotation; positions and tables ignored) or a multiple of 16, at most
+ *              head_dim.
+ *   positions  device int32[T], in [0, n_positions); a row whose position is out of range
+ *              is written without rotation and reported.
+ *   Qo, Ko     device, like Q and K but of out_dtype; may be Q and K themselves when the
+ *              types and strides are the same.
+ */
+gptq_status gptq_qk_norm_rope(const void* Q, const void* K, int in_dtype, int64_t T, int n_q_heads,
+                              int n_k_heads, int head_dim, int64_t ldq, int64_t ldk, const float* wq,
+                              const float* wk, float eps, const float* cos_table,
+                              const float* sin_table, int64_t n_positions, int rot_dim,
+                              int interleaved, const int32_t* positions, void* Qo, void* Ko,
+                              int out_dtype, int64_t ldqo, int64_t ldko, gptq_stream_t stream);
+
+/*
+ * The 4-bit paged cache. One page of one head is one block of page_size * (head_dim + 8)
+ * bytes: the K codes of its tokens (head_dim / 2 bytes each, a little-endian bitstream like
+ * qweight's), the V codes, then four fp16 per token: K scale, K lowest value, V scale, V
+ * lowest value. The pool is num_pages x n_kv_heads such blocks, 16-byte aligned.
+ *
+ *   page_size  a multiple of 16 in [16, 256].  head_dim 64, 128 or 256.
+ *   num_pages  at most 2^31 - 1.
+ *
+ * gptq_kv_append quantizes one K row and one V row per token and head:
+ *
+ *   low = fp16(min x), scale = fp16((max x - min x) / 15),
+ *   code = clamp(round((x - low) / scale), 0, 15)      (a scale of 0 gives codes of 0)
+ *
+ * in fp32, ties to even, with x limited to fp16's range (+-65504, so infinities too); a row
+ * that holds a NaN gets a NaN scale and is read back as NaN. The cached value is
+ * code * scale + low.
+ *
+ *   K, V       device, T x n_kv_heads x head_dim of kv_dtype (any of the three), heads
+ *              dense, token strides ldk / ldv elements, rows 16-byte aligned.
+ *   slots      device int64[T]: page * page_size + place of every token; negative: the
+ *              token is not stored. Tokens of one call have different slots.
+ *
+ * gptq_kv_read writes the cached values of the tokens at `slots` to K and V (same shapes
+ * and types), rounded once (and kept within fp16's range for GPTQ_F16); zeros for negative
+ * slots.
+ */
+gptq_status gptq_kv_append(const void* K, const void* V, int kv_dtype, int64_t T, int n_kv_heads,
+                           int head_dim, int64_t ldk, int64_t ldv, const int64_t* slots, void* pool,
+                           int64_t num_pages, int page_size, gptq_stream_t stream);
+gptq_status gptq_kv_read(const void* pool, int64_t num_pages, int page_size, int n_kv_heads,
+                         int head_dim, const int64_t* slots, int64_t T, void* K, void* V,
+                         int kv_dtype, int64_t ldk, int64_t ldv, gptq_stream_t stream);
+
+/*
+ * Attention over the 4-bit paged cache:
+ *
+ *   O[i] = sum_j p_ij v_j,  p_i = softmax over the seen keys j of sm_scale * q_i . k_j
+ *
+ * for a batch of sequences. Sequence b has kv_lens[b] cached keys, in pages block_table[b][0],
+ * block_table[b][1], ..., and the query tokens cu_q[b] ... cu_q[b + 1] - 1; its query token i
+ * stands at position p = kv_lens[b] - (number of its query tokens) + i. It sees keys j <= p
+ * when `causal` (all keys otherwise), and, with window > 0, only j > p - window. A query that
+ * sees no key gets zeros (and an lse of -infinity). Query head h reads cache head
+ * h / (n_q_heads / n_kv_heads).
+ *
+ *   Q, O       device, total_q x n_q_heads x head_dim of q_dtype (GPTQ_BF16 or GPTQ_F16),
+ *              heads dense, token strides ldq / ldo elements, rows 16-byte aligned.
+ *   cu_q       device int32[batch + 1], non-decreasing, within [0, total_q]; query tokens
+ *              outside every sequence get no output.
+ *   kv_lens    device int32[batch], in [0, table_width * page_size].
+ *   block_table device int32, batch x table_width, row stride ldt; entries that hold keys
+ *              are pages in [0, num_pages), later ones are not read.
+ *   batch      at most 65535.
+ *   max_q      at least every sequence's number of query tokens (1 for decoding): chooses
+ *              the kernel and its grid.
+ *   sm_scale   positive and finite (1 / sqrt(head_dim) as a rule).
+ *   lse        device fp32, total_q x n_q_heads: log of the sum of exp of the seen scores;
+ *              or NULL.
+ *   ws         device workspace of gptq_kv_attention_workspace_size() bytes, 256-byte
+ *              aligned; its contents on entry do not matter.
+ */
+size_t gptq_kv_attention_workspace_size(int64_t total_q, int n_q_heads, int n_kv_heads, int head_dim,
+                                        int64_t batch, int64_t max_q);
+gptq_status gptq_kv_attention(const void* Q, int q_dtype, int64_t total_q, int n_q_heads,
+                              int n_kv_heads, int head_dim, int64_t ldq, const int32_t* cu_q,
+                              const int32_t* kv_lens, const int32_t* block_table, int64_t ldt,
+                              int64_t table_width, int64_t batch, int64_t max_q, const void* pool,
+                              int64_t num_pages, int page_size, float sm_scale, int causal,
+                              int64_t window, void* O, int64_t ldo, float* lse, void* ws,
+                              size_t ws_bytes, gptq_stream_t stream);
 
 #ifdef __cplusplus
 }

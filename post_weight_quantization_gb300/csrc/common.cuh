@@ -53,7 +53,7 @@ int sm_count();
 int* device_error_word();   // device address of the library's error word
 
 // error bits written by kernels into the device error word
-enum : int { DEVERR_TIMEOUT = 1, DEVERR_NONFINITE = 2 };
+enum : int { DEVERR_TIMEOUT = 1, DEVERR_NONFINITE = 2, DEVERR_INDEX = 4 };
 
 // wall-clock limit of one on-device wait; every spin-wait in this library ends
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;   // 2 s

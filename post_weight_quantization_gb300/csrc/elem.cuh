@@ -1,0 +1,93 @@
+// Element types of the serving kernels: eight consecutive values of a row to and from
+// fp32 registers by 16-byte accesses (two of them for fp32), and the small helpers the
+// kernels share. Rows are 16-byte aligned.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace gptq {
+
+struct F32 { using T = float; };
+struct BF16 { using T = __nv_bfloat16; };
+struct F16 { using T = __half; };
+
+template <typename E> __device__ __forceinline__ void unpack8(const void* p, float (&v)[8]);
+template <typename E> __device__ __forceinline__ void pack8(void* p, const float (&v)[8]);
+
+template <> __device__ __forceinline__ void unpack8<F32>(const void* p, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+template <> __device__ __forceinline__ void unpack8<BF16>(const void* p, float (&v)[8]) {
+  const uint4 a = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    v[2 * k] = __uint_as_float(w[k] << 16);
+    v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+  }
+}
+template <> __device__ __forceinline__ void unpack8<F16>(const void* p, float (&v)[8]) {
+  const uint4 a = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+    v[2 * k] = f.x;
+    v[2 * k + 1] = f.y;
+  }
+}
+template <> __device__ __forceinline__ void pack8<F32>(void* p, const float (&v)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+template <> __device__ __forceinline__ void pack8<BF16>(void* p, const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+    w[k] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <> __device__ __forceinline__ void pack8<F16>(void* p, const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const __half2 h = __floats2half2_rn(v[2 * k], v[2 * k + 1]);
+    w[k] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Call f with the element type of a dtype code (checked by the caller).
+template <typename F>
+inline void with_dtype(int dtype, F&& f) {
+  if (dtype == GPTQ_F32) f(F32{});
+  else if (dtype == GPTQ_BF16) f(BF16{});
+  else f(F16{});
+}
+
+// Lanes that hold one row of head_dim values, eight each: the power of two that covers it.
+inline int lanes_per_row(int head_dim) {
+  int l = 1;
+  while (l * 8 < head_dim) l *= 2;
+  return l;
+}
+// Call f with lanes_per_row(head_dim) as a compile-time constant.
+template <typename F>
+inline void with_lanes(int head_dim, F&& f) {
+  switch (lanes_per_row(head_dim)) {
+    case 1: f(std::integral_constant<int, 1>{}); break;
+    case 2: f(std::integral_constant<int, 2>{}); break;
+    case 4: f(std::integral_constant<int, 4>{}); break;
+    case 8: f(std::integral_constant<int, 8>{}); break;
+    case 16: f(std::integral_constant<int, 16>{}); break;
+    default: f(std::integral_constant<int, 32>{}); break;
+  }
+}
+
+}  // namespace gptq

@@ -253,6 +253,8 @@ gptq_status gptq_device_check(gptq_stream_t stream) {
   }
   if (v & DEVERR_TIMEOUT) return set_error(GPTQ_ERR_TIMEOUT, "an on-device wait gave up");
   if (v & DEVERR_NONFINITE) return set_error(GPTQ_ERR_NONFINITE, "a kernel met a NaN or an Inf");
+  if (v & DEVERR_INDEX)
+    return set_error(GPTQ_ERR_INVALID_ARG, "a kernel met an index (slot, page, length, position or adapter) out of range");
   return GPTQ_OK;
 }
 

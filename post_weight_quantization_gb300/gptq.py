@@ -57,6 +57,17 @@ SIGNATURES = {
     "gptq_wait_selftest": (_c_int, [_c_int, _c_i64, _vp]),
     "gptq_dequant_gemm": (_c_int, [_vp, _vp, _vp, _c_i64, _c_i64, _c_int, _c_int, _vp, _c_i64, _c_i64, _vp, _c_int,
                                    _c_i64, _vp, _c_size, _vp]),
+    "gptq_qk_norm_rope": (_c_int, [_vp, _vp, _c_int, _c_i64, _c_int, _c_int, _c_int, _c_i64, _c_i64, _vp, _vp, _c_float,
+                                   _vp, _vp, _c_i64, _c_int, _c_int, _vp, _vp, _vp, _c_int, _c_i64, _c_i64, _vp]),
+    "gptq_kv_append": (_c_int, [_vp, _vp, _c_int, _c_i64, _c_int, _c_int, _c_i64, _c_i64, _vp, _vp, _c_i64, _c_int, _vp]),
+    "gptq_kv_read": (_c_int, [_vp, _c_i64, _c_int, _c_int, _c_int, _vp, _c_i64, _vp, _vp, _c_int, _c_i64, _c_i64, _vp]),
+    "gptq_kv_attention_workspace_size": (_c_size, [_c_i64, _c_int, _c_int, _c_int, _c_i64, _c_i64]),
+    "gptq_kv_attention": (_c_int, [_vp, _c_int, _c_i64, _c_int, _c_int, _c_int, _c_i64, _vp, _vp, _vp, _c_i64, _c_i64,
+                                   _c_i64, _c_i64, _vp, _c_i64, _c_int, _c_float, _c_int, _c_i64, _vp, _c_i64, _vp, _vp,
+                                   _c_size, _vp]),
+    "gptq_adapter_workspace_size": (_c_size, [_c_i64, _c_i64, _c_int, _c_int, _c_i64, _c_int]),
+    "gptq_adapter_linear": (_c_int, [_vp, _vp, _vp, _c_i64, _c_i64, _c_int, _c_int, _vp, _c_i64, _c_i64, _vp, _vp, _vp,
+                                     _c_i64, _c_int, _vp, _vp, _c_int, _c_i64, _vp, _c_size, _vp]),
     "gptq_pipeline_create": (_c_int, [_c_i64, _c_i64, _c_int, _c_int, _c_int, _c_int, _c_float, _c_int, _c_i64,
                                       ctypes.POINTER(_vp)]),
     "gptq_pipeline_run": (_c_int, [_vp, _vp, _c_i64, _vp, _c_i64, _c_i64, _vp, _vp, _vp, _vp, _vp, _vp]),
@@ -411,6 +422,232 @@ def gptq_gemm_f32(A: torch.Tensor, B: torch.Tensor, C: torch.Tensor, a_kmajor: b
                               B.stride(0), _ptr(C), C.stride(0), float(alpha), float(beta), int(lower_tiles),
                               _stream(stream)), "gptq_gemm_f32")
     return C
+
+
+# ----------------------------------------------------------------------------------
+# Serving: adapters beside a packed layer, head norms with the rotation, the 4-bit cache
+# and the attention that reads it.
+_DTYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_ALL = tuple(_DTYPE)
+
+
+def _heads(t: torch.Tensor, name: str, dtypes, T: int = -1, heads: int = -1, dim: int = -1) -> None:
+    """A (tokens, heads, head_dim) tensor whose heads lie densely in each token's row (the
+    token stride is free), with the given sizes where they are not -1."""
+    _need_cuda(t, name, dtypes)
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be (tokens, heads, head_dim), got {tuple(t.shape)}")
+    n, h, d = t.shape
+    if (T >= 0 and n != T) or (heads >= 0 and h != heads) or (dim >= 0 and d != dim):
+        raise ValueError(f"{name} must have shape ({T}, {heads}, {dim}), got {tuple(t.shape)}")
+    if n and h and (t.stride(2) != 1 or (h > 1 and t.stride(1) != d)):
+        raise ValueError(f"{name} must hold each token's heads densely")
+
+
+def _ld(t: torch.Tensor) -> int:
+    """The token stride of a (tokens, heads, head_dim) tensor (dense for a single token)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def gptq_adapter_linear(q: "QuantizedLayer", X: torch.Tensor, m: int, A: Optional[torch.Tensor] = None,
+                        B: Optional[torch.Tensor] = None, ids: Optional[torch.Tensor] = None,
+                        alpha: Optional[torch.Tensor] = None, Y: Optional[torch.Tensor] = None, out_bf16: bool = False,
+                        ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Y[t] = X[t] W_hat^T + alpha[a] (X[t] A[a]^T) B[a]^T with a = ids[t] (negative: no
+    adapter), from the packed layer q and bf16 tokens X (T x d). A: (n, rank, d), B: (n, m,
+    rank) bf16, ids: (T,) int32, alpha: (n,) float32 or None for 1. fp32 output, or bf16 with
+    out_bf16. Without A, B and ids it is the packed layer alone."""
+    _need_cuda(X, "X", (torch.bfloat16, torch.int16))
+    d, T = q.d, X.shape[0]
+    if X.dim() != 2 or X.stride(1) != 1 or X.shape[1] != d:
+        raise ValueError("X must be T x d with unit column stride")
+    G = 1 if q.group_size == -1 else (d // q.group_size if q.group_size > 0 else 1)
+    _need_rows(q.qweight, "q.qweight", m, (d * q.bits + 31) // 32, (torch.int32,))
+    _need_rows(q.scales, "q.scales", m, G, (torch.float32,))
+    _need_rows(q.zeros, "q.zeros", m, G, (torch.float32,))
+    n, rank = 0, 8
+    if A is not None:
+        if B is None or ids is None:
+            raise ValueError("A needs B and ids")
+        if A.dim() != 3:
+            raise ValueError(f"A must be (adapters, rank, d), got {tuple(A.shape)}")
+        n, rank = A.shape[0], A.shape[1]
+        _need_buffer(A, "A", (n, rank, d), (torch.bfloat16,))
+        _need_buffer(B, "B", (n, m, rank), (torch.bfloat16,))
+        _need_buffer(ids, "ids", (T,), (torch.int32,))
+        if alpha is not None:
+            _need_buffer(alpha, "alpha", (n,), (torch.float32,))
+    elif B is not None or ids is not None or alpha is not None:
+        raise ValueError("B, ids and alpha need A")
+    ydt = torch.bfloat16 if out_bf16 else torch.float32
+    if Y is None:
+        Y = torch.empty((T, m), dtype=ydt, device=X.device)
+    else:
+        _need_cuda(Y, "Y", (ydt,))
+        if Y.dim() != 2 or tuple(Y.shape) != (T, m) or Y.stride(1) != 1:
+            raise ValueError(f"Y must be ({T}, {m}) with unit column stride, got {tuple(Y.shape)}")
+    need = int(_lib.gptq_adapter_workspace_size(m, d, q.bits, q.group_size, T, rank))
+    if ws is None:
+        ws = _workspace(need, X.device)
+    ws_bytes = _need_workspace(ws, need)
+    _one_device(q.qweight, q.scales, q.zeros, X, A, B, ids, alpha, Y, ws)
+    st = _lib.gptq_adapter_linear(_ptr(q.qweight), _ptr(q.scales), _ptr(q.zeros), m, d, q.bits, q.group_size, _ptr(X), T,
+                                  X.stride(0) if T > 1 else d, _ptr(A), _ptr(B), _ptr(alpha), n, rank, _ptr(ids),
+                                  _ptr(Y), 1 if out_bf16 else 0, Y.stride(0) if T > 1 else m, _ptr(ws), ws_bytes,
+                                  _stream(stream))
+    _check(st, "gptq_adapter_linear")
+    return Y
+
+
+def gptq_qk_norm_rope(Q: torch.Tensor, K: Optional[torch.Tensor], positions: Optional[torch.Tensor] = None,
+                      cos: Optional[torch.Tensor] = None, sin: Optional[torch.Tensor] = None,
+                      wq: Optional[torch.Tensor] = None, wk: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                      interleaved: bool = False, Q_out: Optional[torch.Tensor] = None,
+                      K_out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None, stream=None):
+    """The RMS norm of every query and key head (weights wq, wk: (head_dim,) float32, None for
+    no norm) and the rotation by cos/sin[positions] (tables (n_positions, rot_dim / 2) float32;
+    None for no rotation), in one pass. Q, K: (T, heads, head_dim) float32, bfloat16 or
+    float16; K may be None. Returns (Q_out, K_out) of out_dtype (default: Q's type); Q_out and
+    K_out may be Q and K themselves."""
+    _heads(Q, "Q", _ALL)
+    T, hq, dim = Q.shape
+    hk = 0
+    if K is not None:
+        _heads(K, "K", (Q.dtype,), T, -1, dim)
+        hk = K.shape[1]
+    elif K_out is not None or wk is not None:
+        raise ValueError("K_out and wk need K")
+    odt = out_dtype or (Q_out.dtype if Q_out is not None else Q.dtype)
+    if odt not in _DTYPE:
+        raise TypeError(f"out_dtype must be one of {_ALL}, got {odt}")
+    if Q_out is None:
+        Q_out = torch.empty((T, hq, dim), dtype=odt, device=Q.device)
+    else:
+        _heads(Q_out, "Q_out", (odt,), T, hq, dim)
+    if K is not None:
+        if K_out is None:
+            K_out = torch.empty((T, hk, dim), dtype=odt, device=Q.device)
+        else:
+            _heads(K_out, "K_out", (odt,), T, hk, dim)
+    rot = n_pos = 0
+    if cos is not None:
+        if sin is None or positions is None or cos.dim() != 2:
+            raise ValueError("a rotation needs positions and 2-D tables cos and sin")
+        n_pos, rot = cos.shape[0], 2 * cos.shape[1]
+        _need_buffer(cos, "cos", (n_pos, rot // 2), (torch.float32,))
+        _need_buffer(sin, "sin", (n_pos, rot // 2), (torch.float32,))
+        _need_buffer(positions, "positions", (T,), (torch.int32,))
+    elif sin is not None or positions is not None:
+        raise ValueError("sin and positions need cos")
+    for w, name in ((wq, "wq"), (wk, "wk")):
+        if w is not None:
+            _need_buffer(w, name, (dim,), (torch.float32,))
+    _one_device(Q, K, positions, cos, sin, wq, wk, Q_out, K_out)
+    st = _lib.gptq_qk_norm_rope(_ptr(Q), _ptr(K), _DTYPE[Q.dtype], T, hq, hk, dim, _ld(Q), _ld(K) if hk else 0, _ptr(wq),
+                                _ptr(wk), float(eps), _ptr(cos), _ptr(sin), n_pos, rot, int(bool(interleaved)),
+                                _ptr(positions), _ptr(Q_out), _ptr(K_out), _DTYPE[odt], _ld(Q_out),
+                                _ld(K_out) if hk else 0, _stream(stream))
+    _check(st, "gptq_qk_norm_rope")
+    return Q_out, K_out
+
+
+@dataclass
+class KVCache:
+    """The 4-bit paged cache of one layer: pool is (num_pages, n_kv_heads, page_size *
+    (head_dim + 8)) uint8; a page of a head holds its tokens' K codes, their V codes, then
+    four float16 per token (K scale, K lowest value, V scale, V lowest value)."""
+    pool: torch.Tensor
+    page_size: int
+    n_kv_heads: int
+    head_dim: int
+
+    @classmethod
+    def empty(cls, num_pages: int, page_size: int, n_kv_heads: int, head_dim: int, device="cuda") -> "KVCache":
+        pool = torch.empty((num_pages, n_kv_heads, page_size * (head_dim + 8)), dtype=torch.uint8, device=device)
+        return cls(pool, page_size, n_kv_heads, head_dim)
+
+    def check(self) -> int:
+        """Raise if the pool does not have the layout; returns the number of pages."""
+        _need_buffer(self.pool, "cache.pool", (self.pool.shape[0], self.n_kv_heads,
+                                               self.page_size * (self.head_dim + 8)), (torch.uint8,))
+        return self.pool.shape[0]
+
+
+def gptq_kv_append(cache: KVCache, K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
+    """Quantize K and V rows (T, n_kv_heads, head_dim; float32, bfloat16 or float16) to 4 bits
+    into the cache at slots (T,) int64 = page * page_size + place; negative slots are skipped."""
+    pages = cache.check()
+    _heads(K, "K", _ALL, -1, cache.n_kv_heads, cache.head_dim)
+    T = K.shape[0]
+    _heads(V, "V", (K.dtype,), T, cache.n_kv_heads, cache.head_dim)
+    _need_buffer(slots, "slots", (T,), (torch.int64,))
+    _one_device(cache.pool, K, V, slots)
+    st = _lib.gptq_kv_append(_ptr(K), _ptr(V), _DTYPE[K.dtype], T, cache.n_kv_heads, cache.head_dim, _ld(K), _ld(V),
+                             _ptr(slots), _ptr(cache.pool), pages, cache.page_size, _stream(stream))
+    _check(st, "gptq_kv_append")
+
+
+def gptq_kv_read(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
+                 K: Optional[torch.Tensor] = None, V: Optional[torch.Tensor] = None, stream=None):
+    """The cached values at slots (T,) int64 as (K, V), each (T, n_kv_heads, head_dim) of
+    dtype; zeros for negative slots."""
+    pages = cache.check()
+    T = slots.shape[0]
+    _need_buffer(slots, "slots", (T,), (torch.int64,))
+    if dtype not in _DTYPE:
+        raise TypeError(f"dtype must be one of {_ALL}, got {dtype}")
+    if K is None:
+        K = torch.empty((T, cache.n_kv_heads, cache.head_dim), dtype=dtype, device=cache.pool.device)
+    if V is None:
+        V = torch.empty((T, cache.n_kv_heads, cache.head_dim), dtype=dtype, device=cache.pool.device)
+    for t, name in ((K, "K"), (V, "V")):
+        _heads(t, name, (dtype,), T, cache.n_kv_heads, cache.head_dim)
+    _one_device(cache.pool, slots, K, V)
+    st = _lib.gptq_kv_read(_ptr(cache.pool), pages, cache.page_size, cache.n_kv_heads, cache.head_dim, _ptr(slots), T,
+                           _ptr(K), _ptr(V), _DTYPE[dtype], _ld(K), _ld(V), _stream(stream))
+    _check(st, "gptq_kv_read")
+    return K, V
+
+
+def gptq_kv_attention(cache: KVCache, Q: torch.Tensor, cu_q: torch.Tensor, kv_lens: torch.Tensor,
+                      block_table: torch.Tensor, max_q: int, sm_scale: Optional[float] = None, causal: bool = True,
+                      window: int = 0, O: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                      ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention of the query tokens Q (total_q, n_q_heads, head_dim; bfloat16 or float16) of a
+    batch over its cached keys and values. Sequence b has the query tokens cu_q[b] ... cu_q[b +
+    1] - 1 (int32), kv_lens[b] cached keys (int32) in pages block_table[b] (int32); its query
+    tokens are the last ones of those kv_lens[b]. max_q: the most query tokens of a sequence.
+    sm_scale defaults to head_dim ** -0.5; window > 0 sees only the last `window` keys up to
+    the query's own. lse, when given, is (total_q, n_q_heads) float32. Returns O."""
+    pages = cache.check()
+    _heads(Q, "Q", (torch.bfloat16, torch.float16), -1, -1, cache.head_dim)
+    total, hq, dim = Q.shape
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be (batch, pages)")
+    batch, width = block_table.shape
+    _need_cuda(block_table, "block_table", (torch.int32,))
+    if batch and width and block_table.stride(1) != 1:
+        raise ValueError("block_table must have unit column stride")
+    _need_buffer(cu_q, "cu_q", (batch + 1,), (torch.int32,))
+    _need_buffer(kv_lens, "kv_lens", (batch,), (torch.int32,))
+    if O is None:
+        O = torch.empty((total, hq, dim), dtype=Q.dtype, device=Q.device)
+    else:
+        _heads(O, "O", (Q.dtype,), total, hq, dim)
+    if lse is not None:
+        _need_buffer(lse, "lse", (total, hq), (torch.float32,))
+    need = int(_lib.gptq_kv_attention_workspace_size(total, hq, cache.n_kv_heads, dim, batch, max_q))
+    if ws is None:
+        ws = _workspace(need, Q.device)
+    ws_bytes = _need_workspace(ws, need)
+    _one_device(cache.pool, Q, cu_q, kv_lens, block_table, O, lse, ws)
+    st = _lib.gptq_kv_attention(_ptr(Q), _DTYPE[Q.dtype], total, hq, cache.n_kv_heads, dim, _ld(Q), _ptr(cu_q),
+                                _ptr(kv_lens), _ptr(block_table), block_table.stride(0) if batch > 1 else width, width,
+                                batch, max_q, _ptr(cache.pool), pages, cache.page_size,
+                                float(dim ** -0.5 if sm_scale is None else sm_scale), int(bool(causal)), int(window),
+                                _ptr(O), _ld(O), _ptr(lse), _ptr(ws), ws_bytes, _stream(stream))
+    _check(st, "gptq_kv_attention")
+    return O
 
 
 # ----------------------------------------------------------------------------------

@@ -1,0 +1,501 @@
+"""The serving operators against the float64 oracle: head norms with the rotation, rows of
+the 4-bit cache, attention over the cache, adapters beside a packed layer. Inputs are made
+on the CPU; the cache that attention reads is written by the oracle, so each operator is
+checked on its own.
+
+Tolerances (u: half a unit in the last place, relative: 2^-8 bf16, 2^-11 fp16, 2^-24 fp32):
+  norm_rope   a head's mean of squares is a sum of D positive terms in at most 8 + 5 steps
+              and enters as its square root, the norm, weight and rotation add at most 8
+              roundings: 16 * 2^-24 * (|n_i c| + |n_j s|) + u |y|
+  cache rows  bit-equal codes, scales and lowest values
+  attention   a score is a sum of D exact products in fp32 (tensor-core accumulation may
+              truncate: 2^-22 a step), scaled: d_s = (D + 8) 2^-22 sm_scale sum |q| (15 scale +
+              |low|); the probabilities' product with the codes may round them to fp16
+              (2^-11): (2^-11 + 2 max d_s + 2^-18) sum_j p_j (|v_j| + 2 |low_j|) + u |o|
+  adapters    the packed layer as its own tests have it, (unit + G + 2) 2^-23 sum |x w|; the
+              low-rank part in fp32 with the inner product carried as two bf16 parts:
+              ((d + rank) 2^-23 + 2^-16) |alpha| |B| (|A| |x|); + u |y|
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import gptq_oracle as orc
+from oracle import serving_oracle as so
+
+pytestmark = pytest.mark.gpu
+
+HALF_ULP = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
+TINY = {torch.float32: 1e-37, torch.bfloat16: 1e-37, torch.float16: 2.0 ** -25}
+
+
+@pytest.fixture(scope="module")
+def g():
+    from post_weight_quantization_gb300 import build as b
+    b.build()
+    from post_weight_quantization_gb300 import gptq
+    return gptq
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def randn(rng, shape, dtype, scale=1.0):
+    return torch.from_numpy(scale * rng.standard_normal(shape)).to(dtype)
+
+
+def done(g):
+    torch.cuda.synchronize()
+    g.gptq_device_check()
+
+
+# ------------------------------------------------------------------ norm and rotation
+def _tables(n, rot):
+    freq = 10000.0 ** (-np.arange(0, rot, 2) / rot)
+    a = np.arange(n)[:, None] * freq
+    return np.cos(a).astype(np.float32), np.sin(a).astype(np.float32)
+
+
+def _check_norm_rope(x, got, positions, cos, sin, w, eps, interleaved):
+    ref = so.norm_rope(f64(x), positions, cos, sin, w, eps, interleaved)
+    n = np.abs(so.norm_rope(f64(x), w=w, eps=eps))
+    mag = n.copy()
+    if cos is not None:
+        mag = so.norm_rope(n, positions, np.abs(cos), -np.abs(sin), None, eps, interleaved)
+        half = cos.shape[1]
+        pairs = [(2 * i, 2 * i + 1) if interleaved else (i, i + half) for i in range(half)]
+        for i, (a, b) in enumerate(pairs):          # |n_j c| + |n_i s| for the second of a pair
+            c, s = np.abs(cos)[positions, i][:, None], np.abs(sin)[positions, i][:, None]
+            mag[..., b] = n[..., b] * c + n[..., a] * s
+    bound = 16 * 2.0 ** -24 * mag + HALF_ULP[got.dtype] * np.abs(ref) * (1 + 2.0 ** -8) + TINY[got.dtype]
+    assert np.all(np.abs(f64(got) - ref) <= bound), float(np.max(np.abs(f64(got) - ref) / bound))
+
+
+@pytest.mark.parametrize("T,hq,hk,D,rot", [(1, 32, 32, 128, 128), (7, 64, 8, 128, 64), (33, 5, 1, 64, 64),
+                                           (3, 28, 4, 256, 64), (2, 3, 2, 80, 80), (5, 2, 0, 8, 0),
+                                           (4, 9, 3, 96, 32), (130, 8, 1, 16, 16), (19, 1, 1, 248, 240)])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("din,dout", [(torch.bfloat16, torch.bfloat16), (torch.float16, torch.float16),
+                                      (torch.float32, torch.bfloat16), (torch.float32, torch.float32),
+                                      (torch.bfloat16, torch.float16)])
+def test_norm_rope(g, T, hq, hk, D, rot, interleaved, din, dout):
+    rng = np.random.default_rng(T * 1000 + D + rot)
+    pad = 16
+    qkv = randn(rng, (T, (hq + 2 * hk) * D + pad), din, 2.0).cuda()         # a fused projection's rows
+    Q, K = qkv[:, :hq * D].view(T, hq, D), qkv[:, hq * D:(hq + hk) * D].view(T, hk, D)
+    wq, wk = (1 + 0.2 * rng.standard_normal((2, D))).astype(np.float32)
+    n_pos = 300
+    pos = rng.integers(0, n_pos, T).astype(np.int32)
+    cos, sin = _tables(n_pos, rot) if rot else (None, None)
+    dev = lambda a: None if a is None else torch.from_numpy(a).cuda()
+    Qo, Ko = g.gptq_qk_norm_rope(Q, K if hk else None, dev(pos) if rot else None, dev(cos), dev(sin), wq=dev(wq),
+                                 wk=dev(wk) if hk else None, eps=1e-5, interleaved=interleaved, out_dtype=dout)
+    done(g)
+    _check_norm_rope(Q, Qo, pos, cos, sin, wq, 1e-5, interleaved)
+    if hk:
+        _check_norm_rope(K, Ko, pos, cos, sin, wk, 1e-5, interleaved)
+
+
+@pytest.mark.parametrize("D,rot,interleaved", [(128, 128, False), (64, 32, True), (256, 256, False)])
+def test_norm_rope_in_place_and_without_norm(g, D, rot, interleaved):
+    rng = np.random.default_rng(D)
+    T, hq, hk = 11, 6, 2
+    cos, sin = _tables(64, rot)
+    pos = rng.integers(0, 64, T).astype(np.int32)
+    args = [torch.from_numpy(a).cuda() for a in (pos, cos, sin)]
+    Q, K = randn(rng, (T, hq, D), torch.bfloat16).cuda(), randn(rng, (T, hk, D), torch.bfloat16).cuda()
+    want = g.gptq_qk_norm_rope(Q, K, *args, interleaved=interleaved)
+    _check_norm_rope(Q, want[0], pos, cos, sin, None, 1e-6, interleaved)
+    qkv = torch.cat([Q.reshape(T, -1), K.reshape(T, -1)], dim=1).contiguous()
+    q, k = qkv[:, :hq * D].view(T, hq, D), qkv[:, hq * D:].view(T, hk, D)
+    g.gptq_qk_norm_rope(q, k, *args, interleaved=interleaved, Q_out=q, K_out=k)
+    done(g)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+
+
+def test_norm_rope_zero_rows_nan_and_bad_position(g):
+    T, h, D = 4, 2, 128
+    x = torch.zeros((T, h, D), dtype=torch.bfloat16)
+    x[1] = 3.0
+    x[2, 0, 5] = float("nan")
+    x[3] = 1.0
+    cos, sin = (torch.from_numpy(a).cuda() for a in _tables(8, D))
+    w = torch.ones(D, device="cuda")
+    pos = torch.tensor([0, 7, 3, 8], dtype=torch.int32, device="cuda")          # 8 is out of range
+    y, _ = g.gptq_qk_norm_rope(x.cuda(), None, pos, cos, sin, wq=w)
+    torch.cuda.synchronize()
+    with pytest.raises(g.GPTQError) as e:
+        g.gptq_device_check()
+    assert e.value.status == g.GPTQ_ERR_INVALID_ARG
+    g.gptq_device_check()                                                        # read once, then clear
+    y = y.float().cpu()
+    assert torch.all(y[0] == 0) and torch.isnan(y[2, 0]).all() and torch.isfinite(y[2, 1]).all()
+    assert torch.allclose(y[3], torch.ones(h, D), atol=2.0 ** -8)                # written without rotation
+
+
+# ------------------------------------------------------------------ cache rows
+def _rows(rng, shape, dtype, kind):
+    x = rng.standard_normal(shape)
+    if kind == "offset":
+        x = 0.01 * x + 5.0 * rng.standard_normal(shape[:-1])[..., None]
+    elif kind == "wide":
+        x = x * np.exp(8 * rng.standard_normal(shape))
+    elif kind == "steps":                                                        # quotients on ties
+        x = rng.integers(0, 31, shape) * 0.25 - 2.0
+    x = torch.from_numpy(x).to(dtype)
+    if kind == "special":
+        x.view(-1, shape[-1])[0] = 0.0
+        x.view(-1, shape[-1])[1] = 7.25
+        x.view(-1, shape[-1])[2, 3] = float("inf")
+        x.view(-1, shape[-1])[3, 1] = -float("inf")
+        x.view(-1, shape[-1])[4, 0] = float("nan")
+        x.view(-1, shape[-1])[5] = 1e-7
+        x.view(-1, shape[-1])[6] *= 1e-6
+        if dtype != torch.float16:
+            x.view(-1, shape[-1])[7] *= 1e7
+    return x
+
+
+@pytest.mark.parametrize("kind", ["normal", "offset", "wide", "steps", "special"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("H,D,page", [(8, 128, 64), (3, 64, 16), (1, 256, 48)])
+def test_kv_append_and_read(g, kind, dtype, H, D, page):
+    rng = np.random.default_rng(D + page)
+    T, pages = 29, 7
+    K, V = _rows(rng, (T, H, D), dtype, kind), _rows(rng, (T, H, D), dtype, kind)
+    slots = rng.choice(pages * page, T, replace=False).astype(np.int64)
+    slots[[4, 20]] = -1
+    pool = rng.integers(0, 256, (pages, H, so.block_bytes(page, D))).astype(np.uint8)
+    want = pool.copy()
+    for t in range(T):
+        if slots[t] >= 0:
+            for h in range(H):
+                so.write_slot(want, page, D, slots[t], h, f64(K[t, h]), f64(V[t, h]))
+    kv = torch.stack([K, V], dim=1).reshape(T, 2 * H * D).cuda()                 # side by side, strided
+    k, v = kv[:, :H * D].view(T, H, D), kv[:, H * D:].view(T, H, D)
+    cache = g.KVCache(torch.from_numpy(pool.copy()).cuda(), page, H, D)
+    g.gptq_kv_append(cache, k, v, torch.from_numpy(slots).cuda())
+    done(g)
+    got = cache.pool.cpu().numpy()
+    if kind == "special":                       # a NaN scale's payload is free
+        half = got[..., page * D:].copy().view(np.float16), want[..., page * D:].copy().view(np.float16)
+        same = (half[0] == half[1]) | (np.isnan(half[0]) & np.isnan(half[1]))
+        assert same.all() and np.array_equal(got[..., :page * D], want[..., :page * D])
+    else:
+        assert np.array_equal(got, want)
+    for out in (torch.float32, torch.bfloat16, torch.float16):
+        rk, rv = g.gptq_kv_read(cache, torch.from_numpy(slots).cuda(), dtype=out)
+        for t in range(T):
+            for h in range(H):
+                ref = so.read_slot(got, page, D, slots[t], h) if slots[t] >= 0 else (np.zeros(D), np.zeros(D))
+                for r, x in zip(ref, (rk, rv)):
+                    assert torch.allclose(x[t, h].cpu().double(), torch.from_numpy(r), rtol=2 * HALF_ULP[out],
+                                          atol=2 * TINY[out], equal_nan=True), (t, h)
+    done(g)
+
+
+def test_kv_append_out_of_range_slots(g):
+    H, D, page, pages = 2, 64, 16, 3
+    cache = g.KVCache(torch.zeros((pages, H, so.block_bytes(page, D)), dtype=torch.uint8, device="cuda"), page, H, D)
+    K = torch.randn((2, H, D), device="cuda")
+    slots = torch.tensor([pages * page, 1 << 40], dtype=torch.int64, device="cuda")
+    g.gptq_kv_append(cache, K, K, slots)
+    torch.cuda.synchronize()
+    with pytest.raises(g.GPTQError):
+        g.gptq_device_check()
+    assert not cache.pool.any()
+    k, v = g.gptq_kv_read(cache, slots)
+    torch.cuda.synchronize()
+    with pytest.raises(g.GPTQError):
+        g.gptq_device_check()
+    assert not k.any() and not v.any()
+
+
+# ------------------------------------------------------------------ attention
+class Batch:
+    """Sequences of the given lengths and numbers of query tokens over one random cache whose
+    unused places hold NaN scales."""
+
+    def __init__(self, lens, new, hq, h, D, page, dtype, seed, q_scale=1.5, v_scale=1.0):
+        rng = np.random.default_rng(seed)
+        self.lens, self.new, self.hq, self.h, self.D, self.page = lens, new, hq, h, D, page
+        per = [-(-n // page) for n in lens]
+        pages = sum(per) + 2
+        self.pool = np.full((pages, h, so.block_bytes(page, D)), 0xFF, dtype=np.uint8)   # fp16 0xFFFF is NaN
+        width = max(per + [1]) + 1
+        order = rng.permutation(pages)
+        self.table = np.full((len(lens), width), pages + 9, dtype=np.int32)              # never read
+        at = 0
+        for b, n in enumerate(per):
+            self.table[b, :n] = order[at:at + n]
+            at += n
+            for j in range(lens[b]):
+                slot = int(self.table[b, j // page]) * page + j % page
+                for x in range(h):
+                    so.write_slot(self.pool, page, D, slot, x, rng.standard_normal(D) + 0.5,
+                                  v_scale * np.exp(rng.standard_normal()) * rng.standard_normal(D))
+        self.cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        self.Q = randn(rng, (int(self.cu[-1]), hq, D), dtype, q_scale)
+
+    def gpu(self, g):
+        self.cache = g.KVCache(torch.from_numpy(self.pool).cuda(), self.page, self.h, self.D)
+        dev = [torch.from_numpy(a).cuda() for a in (self.cu, np.array(self.lens, np.int32), self.table)]
+        return self.cache, self.Q.cuda(), *dev
+
+    def check(self, O, lse=None, sm=None, causal=True, window=0, heads=None):
+        sm = self.D ** -0.5 if sm is None else sm
+        G = self.hq // self.h
+        for b, n in enumerate(self.lens):
+            for x in range(self.h):
+                k, v = so.read_sequence(self.pool, self.page, self.D, self.table[b], n, x)
+                ks, kl, vs, vl = self._numbers(b, n, x)
+                for y in range(x * G, (x + 1) * G):
+                    if heads is not None and y not in heads:
+                        continue
+                    q = f64(self.Q[self.cu[b]:self.cu[b + 1], y])
+                    first = n - self.new[b]
+                    o, l = so.attention(q, k, v, first, sm, causal, window)
+                    got = f64(O[self.cu[b]:self.cu[b + 1], y])
+                    for i in range(q.shape[0]):
+                        d_s = ((self.D + 8) * 2.0 ** -22 * sm * np.abs(q[i]).sum() * np.max(15 * ks + np.abs(kl))) if n else 0.0
+                        mag, _ = so.attention(q[i:i + 1], k, np.abs(v) + 2 * np.abs(vl)[:, None], first + i, sm, causal, window)
+                        bound = ((2.0 ** -11 + 2 * d_s + 2.0 ** -18) * mag[0]
+                                 + HALF_ULP[O.dtype] * np.abs(o[i]) * (1 + 2.0 ** -6) + TINY[O.dtype])
+                        err = np.abs(got[i] - o[i])
+                        assert np.all(err <= bound), (b, y, i, float(np.max(err / bound)))
+                        if lse is not None:
+                            a = float(lse[self.cu[b] + i, y])
+                            assert a == l[i] or abs(a - l[i]) <= d_s + 2.0 ** -18 + 2.0 ** -22 * abs(l[i]), (a, l[i])
+
+    def _numbers(self, b, n, x):
+        out = np.zeros((4, n))
+        for j in range(n):
+            page, at = int(self.table[b][j // self.page]), j % self.page
+            s = self.page * self.D + 8 * at
+            out[:, j] = self.pool[page, x, s:s + 8].copy().view(np.float16)
+        return out
+
+
+@pytest.mark.parametrize("hq,h,D,page", [(4, 4, 128, 16), (8, 1, 128, 64), (7, 1, 64, 32), (16, 2, 256, 48),
+                                         (40, 1, 128, 16), (6, 2, 64, 256)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_attention_one_token(g, hq, h, D, page, dtype):
+    """Decoding: lengths of zero, one, around a page and around the tiles, and several tiles."""
+    lens = [0, 1, 15, 16, 17, 63, 64, 65, 127, 129, 300]
+    t = Batch(lens, [1] * len(lens), hq, h, D, page, dtype, seed=hq + D)
+    lse = torch.full((len(lens), hq), 7.0, device="cuda")
+    O = g.gptq_kv_attention(*t.gpu(g), 1, lse=lse)
+    done(g)
+    assert not O[0].any() and torch.isinf(lse[0]).all()
+    t.check(O, lse)
+
+
+@pytest.mark.parametrize("hq,h,D,page", [(8, 1, 128, 16), (3, 3, 64, 32), (4, 2, 256, 16)])
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 5), (False, 0), (False, 9), (True, 1)])
+def test_attention_several_tokens(g, hq, h, D, page, causal, window):
+    """A few new tokens each (none for one sequence), some of them more than the cache holds
+    (rows that see nothing)."""
+    lens, new = [70, 2, 33, 9, 0], [5, 4, 0, 9, 2]
+    t = Batch(lens, new, hq, h, D, page, torch.bfloat16, seed=D + window)
+    lse = torch.empty((sum(new), hq), device="cuda")
+    O = g.gptq_kv_attention(*t.gpu(g), max(new), causal=causal, window=window, lse=lse)
+    done(g)
+    t.check(O, lse, causal=causal, window=window)
+
+
+@pytest.mark.parametrize("hq,h,D,page,dtype", [(8, 2, 128, 64, torch.bfloat16), (2, 2, 64, 16, torch.float16),
+                                               (3, 1, 256, 32, torch.bfloat16), (16, 1, 128, 128, torch.bfloat16)])
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 100), (False, 0)])
+def test_attention_piece_of_a_prompt(g, hq, h, D, page, dtype, causal, window):
+    """Many new tokens over a longer cache, ragged, one sequence shorter than its new tokens."""
+    lens, new = [331, 140, 100], [150, 140, 130]
+    t = Batch(lens, new, hq, h, D, page, dtype, seed=D + page)
+    lse = torch.empty((sum(new), hq), device="cuda")
+    O = g.gptq_kv_attention(*t.gpu(g), max(new), causal=causal, window=window, lse=lse)
+    done(g)
+    t.check(O, lse, causal=causal, window=window, heads=(0, hq - 1))
+
+
+@pytest.mark.parametrize("new", [1, 3, 70])
+def test_attention_scales_of_every_size(g, new):
+    """Large and tiny queries (fp16's whole range and beyond it in bf16) and values."""
+    for q_scale, v_scale, dtype in ((1e-6, 1e-4, torch.bfloat16), (300.0, 2e3, torch.float16), (1e6, 1.0, torch.bfloat16),
+                                    (1e-30, 1.0, torch.bfloat16)):
+        t = Batch([150, 80], [new, new], 4, 2, 128, 16, dtype, seed=5, q_scale=q_scale, v_scale=v_scale)
+        sm = 128 ** -0.5 if q_scale < 1 else 128 ** -0.5 / q_scale
+        O = g.gptq_kv_attention(*t.gpu(g), new, sm_scale=sm)
+        done(g)
+        t.check(O, sm=sm)
+
+
+@pytest.mark.parametrize("new", [2, 40])
+def test_attention_nan_in_unseen_keys(g, new):
+    """A NaN in a key that only later tokens see leaves the earlier ones as they are."""
+    t = Batch([90], [new], 8, 1, 128, 16, torch.bfloat16, seed=3)
+    clean = g.gptq_kv_attention(*t.gpu(g), new)
+    slot = int(t.table[0, 89 // 16]) * 16 + 89 % 16
+    so.write_slot(t.pool, 16, 128, slot, 0, np.full(128, np.nan), np.full(128, np.nan))
+    O = g.gptq_kv_attention(*t.gpu(g), new)
+    done(g)
+    assert torch.equal(O[:-1], clean[:-1]) and torch.isnan(O[-1]).all()
+
+
+def test_attention_long_split_cache(g):
+    """A length that is split over many blocks and joined, with a flat and a peaked row."""
+    page, D, h, hq, n = 64, 128, 2, 16, 20011
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    pages = -(-n // page)
+    cache = g.KVCache.empty(pages, page, h, D)
+    K = torch.randn((n, h, D), device="cuda", generator=gen)
+    V = torch.randn((n, h, D), device="cuda", generator=gen) + 0.3
+    order = torch.randperm(pages, device="cuda", generator=gen)
+    at = torch.arange(n, device="cuda")
+    slots = order[at // page] * page + at % page
+    g.gptq_kv_append(cache, K, V, slots)
+    k, v = (x.double() for x in g.gptq_kv_read(cache, slots, dtype=torch.float32))
+    Q = torch.randn((1, hq, D), device="cuda", generator=gen).to(torch.bfloat16)
+    Q[0, 0] = 0.0
+    Q[0, 1] *= 12.0
+    for new_lens in (n, 7777):
+        O = g.gptq_kv_attention(cache, Q, torch.tensor([0, 1], dtype=torch.int32, device="cuda"),
+                                torch.tensor([new_lens], dtype=torch.int32, device="cuda"),
+                                order.to(torch.int32)[None], 1)
+        done(g)
+        for x in range(hq):
+            p = torch.softmax(k[:new_lens, x // 8] @ Q[0, x].double() * D ** -0.5, 0)
+            ref = p @ v[:new_lens, x // 8]
+            # the bound of the other tests with every |v| + 2 |low| below 3 * 6
+            mag = p @ (v[:new_lens, x // 8].abs() + 12.0)
+            assert torch.all((O[0, x].double() - ref).abs() <= (2.0 ** -11 + 2.0 ** -12) * mag + 2.0 ** -8 * ref.abs())
+
+
+def test_attention_query_strides_and_uncovered_tokens(g):
+    """Queries inside wider rows, outputs too; tokens outside every sequence keep what was there."""
+    t = Batch([40, 9], [2, 1], 4, 2, 64, 16, torch.bfloat16, seed=11)
+    cache, Q, cu, lens, table = t.gpu(g)
+    cu = cu + 1
+    wide = torch.zeros((6, 5 * 64 + 8), dtype=torch.bfloat16, device="cuda")
+    wide[1:4, :256] = Q.reshape(3, 256)
+    out = torch.full((6, 4 * 64 + 16), 3.0, dtype=torch.bfloat16, device="cuda")
+    g.gptq_kv_attention(cache, wide[:, :256].view(6, 4, 64), cu, lens, table, 2, O=out[:, :256].view(6, 4, 64))
+    done(g)
+    t.check(out[1:4, :256].reshape(3, 4, 64))
+    assert torch.all(out[:, 256:] == 3) and torch.all(out[0] == 3) and torch.all(out[4:] == 3)
+
+
+def test_attention_bad_lengths_and_pages_are_reported(g):
+    for new in (1, 40):
+        t = Batch([64, 64], [new, new], 4, 2, 64, 16, torch.bfloat16, seed=12)
+        for bad in ("length", "page"):
+            cache, Q, cu, lens, table = t.gpu(g)
+            if bad == "length":
+                lens[1] = table.shape[1] * 16 + 5
+                table[1, 4:] = table[1, 0]
+            else:
+                table[1, 1] = cache.pool.shape[0]
+            O = g.gptq_kv_attention(cache, Q, cu, lens, table, new)
+            torch.cuda.synchronize()
+            with pytest.raises(g.GPTQError) as e:
+                g.gptq_device_check()
+            assert e.value.status == g.GPTQ_ERR_INVALID_ARG
+            assert torch.isfinite(O[:new].float()).all()             # the other sequence is untouched
+
+
+# ------------------------------------------------------------------ adapters
+def _layer(rng, m, d, bits, gs):
+    G = 1 if gs == -1 else d // gs
+    codes = rng.integers(0, 2 ** bits, size=(m, d))
+    zeros = rng.integers(0, 2 ** bits, size=(m, G)).astype(np.float32)
+    scales = (0.02 * (0.5 + rng.random((m, G)))).astype(np.float32)
+    return orc.pack_codes(codes, bits), scales, zeros
+
+
+def _check_adapter(g, m, d, bits, gs, T, n, rank, ids, out_bf16, seed, alpha=True, ldx=0):
+    rng = np.random.default_rng(seed)
+    words, sc, ze = _layer(rng, m, d, bits, gs)
+    q = g.QuantizedLayer(torch.from_numpy(words.view(np.int32)).cuda(), torch.from_numpy(sc).cuda(),
+                         torch.from_numpy(ze).cuda(), None, bits, gs, d)
+    X = randn(rng, (T, d + ldx), torch.bfloat16)[:, :d]
+    A, B = randn(rng, (n, rank, d), torch.bfloat16, d ** -0.5), randn(rng, (n, m, rank), torch.bfloat16)
+    al = (0.5 + rng.random(n)).astype(np.float32) if alpha else None
+    ids = np.asarray(ids, dtype=np.int32)
+    Y = g.gptq_adapter_linear(q, X.cuda(), m, A.cuda(), B.cuda(), torch.from_numpy(ids).cuda(),
+                              alpha=None if al is None else torch.from_numpy(al).cuda(), out_bf16=out_bf16)
+    done(g)
+    ref = so.adapter_linear(f64(X), words, sc, ze, bits, gs, f64(A), f64(B), ids, al)
+    W = np.abs(orc.dequantize_packed(words, sc, ze, bits, d, gs, None))
+    G = 1 if gs == -1 else d // gs
+    unit = min(256, d if gs == -1 else gs)
+    bound = (unit + G + 2) * 2.0 ** -23 * (np.abs(f64(X)) @ W.T)
+    for t, a in enumerate(ids):
+        if a >= 0:
+            low = np.abs(f64(B[a])) @ (np.abs(f64(A[a])) @ np.abs(f64(X[t])))
+            bound[t] += ((d + rank) * 2.0 ** -23 + 2.0 ** -16) * (1.0 if al is None else al[a]) * low
+    bound += HALF_ULP[Y.dtype] * np.abs(ref) * (1 + 2.0 ** -7) + 1e-30
+    err = np.abs(f64(Y) - ref)
+    assert np.all(err <= bound), float(np.max(err / bound))
+
+
+@pytest.mark.parametrize("bits,gs", [(4, 128), (4, 32), (4, -1), (2, 64), (2, 32), (3, 128), (3, 64), (8, 128), (8, 32)])
+@pytest.mark.parametrize("T", [1, 2, 9, 17, 40])
+@pytest.mark.parametrize("out_bf16", [False, True])
+def test_adapter_linear_decoding(g, bits, gs, T, out_bf16):
+    """Each token its own adapter, some none, out of order."""
+    rng = np.random.default_rng(T)
+    _check_adapter(g, 200, 768, bits, gs, T, 6, 16, rng.integers(-1, 6, T), out_bf16, seed=bits * 100 + T)
+
+
+@pytest.mark.parametrize("rank", [8, 24, 64, 128])
+@pytest.mark.parametrize("T", [1, 5, 70, 150])
+def test_adapter_linear_ranks(g, rank, T):
+    rng = np.random.default_rng(rank + T)
+    _check_adapter(g, 136, 512, 4, 128, T, 5, rank, np.sort(rng.integers(-1, 5, T)), T % 2 == 0, seed=rank, alpha=T > 1,
+                   ldx=8)
+
+
+@pytest.mark.parametrize("T,ids", [(300, "runs"), (129, "one"), (257, "mixed"), (140, "none")])
+@pytest.mark.parametrize("m,d,bits,gs", [(300, 512, 4, 128), (64, 1056, 8, 32), (257, 768, 2, 64), (520, 640, 3, -1)])
+def test_adapter_linear_prompts(g, T, ids, m, d, bits, gs):
+    rng = np.random.default_rng(T + m)
+    ids = {"runs": np.sort(rng.integers(-1, 7, T)), "one": np.full(T, 3), "mixed": rng.integers(-1, 7, T),
+           "none": np.full(T, -1)}[ids]
+    _check_adapter(g, m, d, bits, gs, T, 7, 16, ids, T % 2 == 0, seed=T)
+
+
+def test_adapter_linear_without_adapters_and_bad_ids(g):
+    rng = np.random.default_rng(1)
+    m, d, T = 100, 256, 7
+    words, sc, ze = _layer(rng, m, d, 4, 128)
+    q = g.QuantizedLayer(torch.from_numpy(words.view(np.int32)).cuda(), torch.from_numpy(sc).cuda(),
+                         torch.from_numpy(ze).cuda(), None, 4, 128, d)
+    for T in (7, 200):
+        X = randn(rng, (T, d), torch.bfloat16).cuda()
+        plain = g.gptq_adapter_linear(q, X, m)
+        A, B = randn(rng, (2, 16, d), torch.bfloat16).cuda(), randn(rng, (2, m, 16), torch.bfloat16).cuda()
+        none = g.gptq_adapter_linear(q, X, m, A, B, torch.full((T,), -1, dtype=torch.int32, device="cuda"))
+        done(g)
+        assert torch.equal(plain, none)
+        ids = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+        ids[3] = 2                                                     # out of range: no adapter, reported
+        bad = g.gptq_adapter_linear(q, X, m, A, B, ids)
+        torch.cuda.synchronize()
+        with pytest.raises(g.GPTQError) as e:
+            g.gptq_device_check()
+        assert e.value.status == g.GPTQ_ERR_INVALID_ARG
+        assert torch.equal(bad, plain)
+
+
+def test_serving_on_another_stream(g):
+    """Every call goes to the stream it is given, behind the work queued there."""
+    s = torch.cuda.Stream()
+    t = Batch([200], [1], 8, 1, 128, 16, torch.bfloat16, seed=21)
+    cache, Q, cu, lens, table = t.gpu(g)
+    torch.cuda.synchronize()
+    late = torch.zeros_like(Q)
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+        late.copy_(Q)
+    O = g.gptq_kv_attention(cache, late, cu, lens, table, 1, stream=s)
+    s.synchronize()
+    t.check(O)
