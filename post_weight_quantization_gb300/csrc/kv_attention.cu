@@ -1,12 +1,39 @@
-// Attention over the 4-bit paged cache.
+// Attention of a few query tokens per sequence over the 4-bit paged cache (decoding).
 //
-//   o_i = sum_j p_ij v_j,   p_i = softmax over the seen j of sm_scale * q_i . k_j,
-//   k_j = code * scale_j + low_j (and v_j alike), one (scale, low) per token and head
+//   o_i = sum_j p_ij v_j,   p_i = softmax over the seen j of sm_scale * q_i . k_j
+//   k_j = kc_j ks_j + kl_j (codes, scale, lowest value; v_j alike), so
+//   q_i . k_j = ks_j (q_i . kc_j) + kl_j sum(q_i),    o_i = sum_j (p_ij vs_j) vc_j + sum_j p_ij vl_j
 //
-// One warp per query token and head: a lane holds D / 32 values of q and of the running
-// output, the scores' maximum and sum run along (one pass over the cache), everything fp32.
+// One pass over the cache with a running maximum and sum; both products run on the tensor
+// cores with the codes themselves as an operand, taken from the packed words in registers:
+//   * A pair of codes masked out of a word (0x000F000F) IS a pair of fp16 numbers, code *
+//     2^-24 (subnormal), and 0x00F000F0 is the pair code * 2^-20: no conversion, two
+//     logic instructions per four codes. The powers of two leave with the scale (K: into
+//     the query; V: at the end). Products with the fp16 query are exact in fp32.
+//   * Each query row is scaled by the power of two that brings its largest value to
+//     [2^14, 2^15), so a bf16 query is exact in fp16 too.
+//   * S^T = K Q^T: A = 16 keys x 16 dims of codes, B = the query rows (N = 8). The fp32
+//     scores leave with their key on the lane row; one movmatrix per 8 x 8 tile brings
+//     the probabilities to the B layout of O^T = V^T P^T (A = 16 dims x 16 keys of codes).
+//   * The probabilities times the key's V scale are rounded to fp16 for the second product:
+//     2^-11 of each, random in sign, against the output's own 2^-8 or 2^-11. They are
+//     brought to the top of fp16's range by a power of two that follows the largest V scale
+//     seen, so small probabilities keep their bits down to 2^-24 of the largest.
+//   Why mma.sync and not tcgen05: the product is bound by HBM bandwidth (one pass over the
+//   cache for at most 32 rows), and tcgen05 would need the codes unpacked to 16 bits in
+//   shared memory, four times the bytes that come from HBM, where here they go from the
+//   packed words to the tensor core through registers.
+//
+// Work: a sequence's (kv head, 8 NT query rows) is an item of tiles of 128 keys; the tiles of
+// all items form one line that is cut into equal pieces, one per CTA, from the lengths on the
+// device. A CTA's four warps take the tile's four 32-key chunks, each through its own ring
+// of bulk copies (page blocks are contiguous: K codes, V codes and numbers of 16 or 32
+// keys are one copy each) and its own running maximum, and meet at the item's end. An item
+// that is cut between CTAs leaves unnormalised parts in the workspace, which
+// kv_combine_kernel joins in a fixed order.
 #include <math_constants.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "elem.cuh"
@@ -14,7 +41,11 @@
 namespace gptq {
 namespace kva {
 
-constexpr int WARPS = 4;
+constexpr int WARPS = 4, THREADS = WARPS * 32;
+constexpr int KC = 32;                          // keys of a warp's chunk
+constexpr int TILE = WARPS * KC;                // keys of a tile
+constexpr float kSlack = 6.0f;                  // a row's maximum may lag by 2^6 before it is moved
+constexpr int kVExp = 8;                        // V scales are brought below 2^(kVExp + 1)
 
 struct Params {
   const void* Q;
@@ -25,86 +56,720 @@ struct Params {
   const int* table;
   const uint8_t* pool;
   long long ldq, ldo, ldt, total_q, table_width, num_pages;
-  int Hq, H, page, batch, causal;
+  int Hq, H, G, page, batch, causal, q_f16;
+  uint32_t page_mul;                            // ceil(2^32 / (page / 16)); 0 when page is 16
   long long window;
-  float scale_log2;            // sm_scale * log2(e)
+  float scale_log2;                             // sm_scale * log2(e)
+  long long* offs;                              // workspace: batch + 1 sums of units, then the unit count per CTA
+  float* part;                                  // workspace: 2 x CTAs x (R x D values, R maxima, R sums)
 };
 
-template <typename E, int D>
-__global__ void __launch_bounds__(WARPS * 32) kv_attention_kernel(Params p, int* __restrict__ err) {
-  constexpr int VPL = D / 32;                            // values per lane
+template <int D, int NT>
+struct Cfg {
+  static constexpr int R = 8 * NT;
+  static constexpr int STAGE = KC * D + KC * 8;
+  static constexpr int NS = D == 256 ? 2 : 3;
+  static constexpr int RED_LD = D + 4;
+  static constexpr int RED = WARPS * R * RED_LD * 4;
+  static constexpr int RING = WARPS * NS * STAGE;
+  static constexpr int BIG = RING > RED ? RING : RED;
+  static constexpr int SMEM = BIG + WARPS * NS * 8 + 3 * WARPS * R * 4 + 64 + 128;
+  static constexpr int OCC = D == 256 ? (NT == 1 ? 3 : 2) : NT == 4 ? 2 : NT == 2 ? (D == 64 ? 3 : 2) : 4;
+  static constexpr int PART = R * D + 2 * R;    // floats of one part
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+  return d;
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }   // -126 ... 127
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[N]) {
+  if constexpr (N == 1) {
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
+  } else if constexpr (N == 2) {
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+      asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                   : "r"(addr + 4 * i));
+  }
+}
+
+// One sequence of the batch, as the line of tiles sees it.
+struct Seq {
+  long long tok0;                // its first query token
+  int nq, len;                   // query tokens, cached keys
+  int t0, tiles, nrt;            // first tile, tiles of an item, row tiles of a head
+  long long units;               // H * nrt * tiles
+};
+
+__device__ __forceinline__ Seq load_seq(const Params& p, int b, int R, int* err) {
+  Seq s;
+  long long a = p.cu_q[b], z = p.cu_q[b + 1], len = p.kv_lens[b];
+  const long long cap = p.table_width * p.page;
+  if (a < 0 || z > p.total_q || len < 0 || len > cap) {
+    report_device_error(err, DEVERR_INDEX);
+    a = a < 0 ? 0 : a;
+    z = z > p.total_q ? p.total_q : z;
+    len = len < 0 ? 0 : (len > cap ? cap : len);
+  }
+  s.tok0 = a;
+  s.nq = z > a ? (int)(z - a) : 0;
+  s.len = (int)len;
+  const long long lo = p.window > 0 ? len - s.nq - p.window + 1 : 0;
+  s.t0 = lo > 0 ? (int)(lo / TILE) : 0;
+  const int n = (s.len + TILE - 1) / TILE - s.t0;
+  s.tiles = n > 0 ? n : 1;
+  s.nrt = (int)(((long long)s.nq * p.G + R - 1) / R);
+  s.units = (long long)p.H * s.nrt * s.tiles;
+  return s;
+}
+
+__device__ __forceinline__ void store_out(const Params& p, long long at, float4 v) {
+  if (p.q_f16) {
+    const float lim = 65504.0f;
+    v.x = v.x == v.x ? fminf(fmaxf(v.x, -lim), lim) : v.x;
+    v.y = v.y == v.y ? fminf(fmaxf(v.y, -lim), lim) : v.y;
+    v.z = v.z == v.z ? fminf(fmaxf(v.z, -lim), lim) : v.z;
+    v.w = v.w == v.w ? fminf(fmaxf(v.w, -lim), lim) : v.w;
+    *reinterpret_cast<uint2*>(reinterpret_cast<__half*>(p.O) + at) = make_uint2(pack_half2(v.x, v.y), pack_half2(v.z, v.w));
+  } else {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.O) + at) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  }
+}
+
+// A warp's running state over an item's keys. In the scores' C layout a lane (g = lane / 4,
+// t = lane % 4) holds keys g and g + 8 of a 16-key tile for rows 2t and 2t + 1 of each n-tile;
+// in the output's, dims of its V words for the same two rows.
+template <int D, int NT>
+struct State {
+  float o[D / 16][NT][4];
+  float mrc[NT][2];              // running maximum in log2 units (0 while there is none)
+  float thr[NT][2];              // mrc + kSlack (-inf while there is none)
+  float l[NT][2], low[NT][2];    // this lane's part of sum p and sum p * vl
+  uint32_t q[NT][D / 8];         // B fragments: 4 registers per word of the lane's K words
+  float rowc[NT][2], rq[NT][2];  // log2 units per inner score; the scaled query's sum
+  int lo[NT][2], hi[NT][2];      // the keys the row sees: lo ... hi
+  float vlim, vinv;              // V scales below vlim = 2^(x+1) are multiplied by vinv = 2^(kVExp - x)
+};
+
+template <int D, int NT, bool MASK>
+__device__ __forceinline__ void chunk(State<D, NT>& st, uint32_t base, int key0, int g, int t) {
+  constexpr int KW = D / 32;                     // K words of a key per lane, words KW t ...
+  constexpr int VW = D / 64;                     // V words of a key per lane, words VW g ...
+  constexpr int RB = D / 2;                      // bytes of a row of codes
+  const uint32_t kb = base, vb = base + KC * RB, nb = base + KC * D;
+  const int sw = (g >> 1) & 1;                   // tile row r holds key r ^ ((r >> 1) & 1): fewer bank conflicts in V
+  const int kr = g ^ sw;
+
+  float s[2][NT][4];
+  float vs[2][2], vl[2][2];
+#pragma unroll
+  for (int mt = 0; mt < 2; ++mt) {
+    uint32_t wa[KW], wb[KW];
+    lds_words<KW>(kb + (16 * mt + kr) * RB + t * KW * 4, wa);
+    lds_words<KW>(kb + (16 * mt + kr + 8) * RB + t * KW * 4, wb);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[mt][n][i] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < KW; ++w) {
+      const uint32_t a8 = wa[w] >> 8, b8 = wb[w] >> 8;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        mma_f16(s[mt][n], wa[w] & 0x000F000Fu, wb[w] & 0x000F000Fu, wa[w] & 0x00F000F0u, wb[w] & 0x00F000F0u,
+                st.q[n][4 * w], st.q[n][4 * w + 1]);
+        mma_f16(s[mt][n], a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u, b8 & 0x00F000F0u, st.q[n][4 * w + 2],
+                st.q[n][4 * w + 3]);
+      }
+    }
+    // numbers of the lane's two keys; inner = ks 2^24 acc + kl sum(q)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      uint32_t num[2];
+      const int r = 16 * mt + kr + 8 * e;
+      lds_words<2>(nb + r * 8, num);
+      float2 kn = __half22float2(*reinterpret_cast<const __half2*>(&num[0]));
+      float2 vn = __half22float2(*reinterpret_cast<const __half2*>(&num[1]));
+      const float ks = kn.x * 16777216.0f;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float x = fmaf(kn.y, st.rq[n][i], s[mt][n][2 * e + i] * ks);
+          if (MASK && (key0 + r > st.hi[n][i] || key0 + r < st.lo[n][i])) x = -CUDART_INF_F;
+          s[mt][n][2 * e + i] = x;
+        }
+      vs[mt][e] = vn.x;
+      vl[mt][e] = vn.y;
+    }
+  }
+  // V scales above the range in use move it (a power of two: exact)
+  {
+    float vm = fmaxf(fmaxf(vs[0][0], vs[0][1]), fmaxf(vs[1][0], vs[1][1]));
+    if (MASK) {                                  // places past the keys may hold anything: rows decide
+      vm = 0.0f;
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          bool any = false;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) any |= s[mt][n][2 * e + i] != -CUDART_INF_F;
+          if (any) vm = fmaxf(vm, vs[mt][e]);
+        }
+    }
+    if (__any_sync(0xffffffffu, vm >= st.vlim)) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
+      const int x = (int)(__float_as_uint(vm) >> 23) - 127;          // a finite fp16 value: -24 ... 15
+      const float vinv = pow2(kVExp - x), f = vinv / st.vinv;
+      st.vinv = vinv;
+      st.vlim = pow2(x + 1);
+#pragma unroll
+      for (int m = 0; m < D / 16; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) st.o[m][n][i] *= f;
+    }
+  }
+  // running maximum, moved only when a score passes it by 2^kSlack
+  {
+    float mx[NT][2];
+    bool over = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        mx[n][i] = fmaxf(fmaxf(s[0][n][i], s[0][n][2 + i]), fmaxf(s[1][n][i], s[1][n][2 + i])) * st.rowc[n][i];
+        over |= mx[n][i] > st.thr[n][i];
+      }
+    if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float v = mx[n][i];
+#pragma unroll
+          for (int o = 4; o <= 16; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+          const bool had = st.thr[n][i] != -CUDART_INF_F;
+          v = had ? fmaxf(v, st.mrc[n][i]) : v;
+          if (v != -CUDART_INF_F) {
+            const float f = had ? ex2(st.mrc[n][i] - v) : 0.0f;
+            st.mrc[n][i] = v;
+            st.thr[n][i] = v + kSlack;
+            st.l[n][i] *= f;
+            st.low[n][i] *= f;
+#pragma unroll
+            for (int m = 0; m < D / 16; ++m) {
+              st.o[m][n][i] *= f;
+              st.o[m][n][2 + i] *= f;
+            }
+          }
+        }
+    }
+  }
+#pragma unroll
+  for (int mt = 0; mt < 2; ++mt) {
+    uint32_t b[NT][2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float c = vs[mt][e] * st.vinv;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float pc[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float x = s[mt][n][2 * e + i];
+          const float pr = ex2(fmaf(x, st.rowc[n][i], -st.mrc[n][i]));
+          if (MASK && x == -CUDART_INF_F) {      // unseen: its numbers may be anything
+            pc[i] = 0.0f;
+          } else {
+            st.l[n][i] += pr;
+            st.low[n][i] = fmaf(pr, vl[mt][e], st.low[n][i]);
+            pc[i] = pr * c;
+          }
+        }
+        b[n][e] = movmatrix(pack_half2(pc[0], pc[1]));
+      }
+    }
+    // V^T fragments: keys of tile rows 2t, 2t + 1 (low) and 2t + 8, 2t + 9 (high)
+    const int k0 = 16 * mt + ((2 * t) ^ (t & 1)), k1 = 16 * mt + ((2 * t + 1) ^ (t & 1));
+    uint32_t v0[VW], v1[VW], v2[VW], v3[VW];
+    lds_words<VW>(vb + k0 * RB + g * VW * 4, v0);
+    lds_words<VW>(vb + k1 * RB + g * VW * 4, v1);
+    lds_words<VW>(vb + (k0 + 8) * RB + g * VW * 4, v2);
+    lds_words<VW>(vb + (k1 + 8) * RB + g * VW * 4, v3);
+#pragma unroll
+    for (int w = 0; w < VW; ++w)
+#pragma unroll
+      for (int by = 0; by < 4; ++by) {
+        // byte `by` of the first key's word in the low half, of the second's in the high half
+        const uint32_t sel = (uint32_t)(by * 0x0011 + (4 + by) * 0x1100);
+        const uint32_t l2 = prmt(v0[w], v1[w], sel), h2 = prmt(v2[w], v3[w], sel);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          mma_f16(st.o[4 * w + by][n], l2 & 0x000F000Fu, l2 & 0x00F000F0u, h2 & 0x000F000Fu, h2 & 0x00F000F0u, b[n][0],
+                  b[n][1]);
+      }
+  }
+}
+
+
+// Position of the line of tiles: the unit `start` of the CTA lies in sequence b at offset off.
+// Every CTA sums the batch's units itself (the lengths are on the device); block 0 leaves the
+// sums for kv_combine_kernel.
+template <int R>
+__device__ __forceinline__ void find_start(const Params& p, long long* sh, long long& total, long long& per, int& b0,
+                                           long long& off, int* err) {
+  const int tid = threadIdx.x, nb = (p.batch + THREADS - 1) / THREADS;
+  long long sum = 0;
+  for (int k = 0; k < nb; ++k) {
+    const int b = tid * nb + k;
+    if (b < p.batch) sum += load_seq(p, b, R, err).units;
+  }
+  long long inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+    if ((tid & 31) >= o) inc += v;
+  }
+  if ((tid & 31) == 31) sh[tid >> 5] = inc;
+  if (tid == 0) sh[6] = p.batch;                 // no sequence unless one is found below
+  __syncthreads();
+  long long before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    if (w < (tid >> 5)) before += sh[w];
+    total += sh[w];
+  }
+  long long at = before + inc - sum;             // units before this thread's sequences
+  per = (total + gridDim.x - 1) / gridDim.x;
+  const long long start = per * blockIdx.x;
+  if (blockIdx.x == 0) {
+    long long a = at;
+    for (int k = 0; k < nb; ++k) {
+      const int b = tid * nb + k;
+      if (b < p.batch) {
+        p.offs[b] = a;
+        a += load_seq(p, b, R, err).units;
+      }
+    }
+    if (tid == 0) p.offs[p.batch] = per;
+  }
+  if (start >= at && start < at + sum) {         // exactly one thread when start < total
+    for (int k = 0; k < nb; ++k) {
+      const int b = tid * nb + k;
+      const long long u = load_seq(p, b, R, err).units;
+      if (start < at + u) {
+        sh[6] = b;
+        sh[7] = start - at;
+        break;
+      }
+      at += u;
+    }
+  }
+  __syncthreads();
+  b0 = (int)sh[6];
+  off = sh[7];
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(THREADS, Cfg<D, NT>::OCC) kv_split_kernel(Params p, int* __restrict__ err) {
+  using C = Cfg<D, NT>;
+  constexpr int R = C::R, NS = C::NS, KW = D / 32, VW = D / 64;
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::BIG);
+  long long* sh = reinterpret_cast<long long*>(smem + C::BIG + WARPS * NS * 8);          // 8 values
+  float* red = reinterpret_cast<float*>(smem + C::BIG + WARPS * NS * 8 + 64);            // maximum, sum, low sum: [3][WARPS][R]
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  uint64_t* bar = bars + warp * NS;
+  const uint32_t ring = smem_u32(smem) + warp * NS * C::STAGE;
+  if (lane == 0) {
+    for (int i = 0; i < NS; ++i) mbar_init(&bar[i], 1);
+    fence_mbar_init();
+  }
+  long long total, per, off;
+  int b;
+  find_start<R>(p, sh, total, per, b, off, err);
+  grid_dep_launch();
+  long long left = total - per * blockIdx.x;
+  left = left < per ? left : per;
+  const long long block = (long long)p.page * (D + 8);
+  const int p16 = p.page >> 4;
+  uint32_t phase = 0, stage = 0;                 // the ring goes on through all items
+  bool dead = false, first = true;
+
+  for (; left > 0 && b < p.batch && !dead; ++b, off = 0) {
+    const Seq sq = load_seq(p, b, R, err);
+    while (left > 0 && off < sq.units && !dead) {
+      // ---- one item, or this CTA's part of it
+      const int item = (int)(off / sq.tiles), ta = (int)(off - (long long)item * sq.tiles);
+      const int tn = (int)(left < sq.tiles - ta ? left : sq.tiles - ta);
+      const int h = item / sq.nrt, rt = item - h * sq.nrt;
+      const bool lead = ta > 0, whole = !lead && tn == sq.tiles;
+      const int rows = (int)(((long long)sq.nq * p.G - (long long)rt * R) < R ? (long long)sq.nq * p.G - (long long)rt * R : R);
+      const int i0 = rt * R / p.G, i1 = (rt * R + rows - 1) / p.G;
+      const int pos0 = sq.len - sq.nq;           // position of the sequence's first query token
+      long long klo = p.window > 0 ? (long long)pos0 + i0 - p.window + 1 : 0;
+      const int lo_all = klo > 0 ? (int)klo : 0;
+      const int hi_all = p.causal ? min(sq.len, max(0, pos0 + i1 + 1)) : sq.len;      // keys lo_all ... hi_all - 1
+      // rows whose keys bound the unmasked chunks
+      const int hi_min = p.causal ? min(sq.len, max(0, pos0 + i0 + 1)) : sq.len;
+      const long long klo1 = p.window > 0 ? (long long)pos0 + i1 - p.window + 1 : 0;
+      const int lo_max = klo1 > 0 ? (int)(klo1 < sq.len ? klo1 : sq.len) : 0;
+      const int c_lo = max((sq.t0 + ta) * WARPS, lo_all / KC), c_hi = min((sq.t0 + ta + tn) * WARPS, (hi_all + KC - 1) / KC);
+      const int c0 = c_lo + ((warp - c_lo) & (WARPS - 1));            // this warp's chunks: c0, c0 + WARPS, ... < c_hi
+      const int* trow = p.table + (long long)b * p.ldt;
+      const uint8_t* head = p.pool + (long long)h * block;
+      const long long page_step = (long long)p.H * block;
+
+      // a chunk is two halves of 16 keys, each inside one page: K codes, V codes and numbers of
+      // a half are one copy each, of both halves where they lie in one page
+      const int half = lane >= 3 ? 1 : 0, part = lane - 3 * half;
+      auto page_of = [&](int c) -> int {         // lanes 0 ... 5: the page of this lane's half (-1: no keys there)
+        const int j16 = 2 * c + half;
+        if (lane >= 6 || c >= c_hi || 16 * j16 >= hi_all) return -1;
+        const int idx = p16 == 1 ? j16 : (int)__umulhi((uint32_t)j16, p.page_mul);
+        int pg = trow[idx];
+        if (pg < 0 || pg >= p.num_pages) {
+          report_device_error(err, DEVERR_INDEX);
+          pg = 0;
+        }
+        return pg;
+      };
+      auto issue = [&](int c, int pg, uint32_t st) {
+        const uint32_t dst = ring + st * C::STAGE;
+        const int j16 = 2 * c + half;
+        const int idx = p16 == 1 ? j16 : (int)__umulhi((uint32_t)j16, p.page_mul);
+        const int at = (j16 - idx * p16) << 4;   // first token of the half in its page
+        const int other = __shfl_down_sync(0xffffffffu, pg, 3), oidx = __shfl_down_sync(0xffffffffu, idx, 3);
+        const unsigned valid = __ballot_sync(0xffffffffu, pg >= 0);
+        const bool both = (valid & 0x08u) && __shfl_sync(0xffffffffu, (int)(oidx == idx && other >= 0), 0);
+        if (lane == 0)
+          mbar_arrive_expect_tx(&bar[st], ((valid & 0x08u) ? 2u : 1u) * (uint32_t)(C::STAGE / 2));
+        __syncwarp();
+        if (pg >= 0 && !(both && half)) {
+          const uint8_t* src = head + pg * page_step;
+          const uint32_t n = both ? 2u : 1u;
+          if (part == 0) bulk_load(dst + half * (16 * D / 2), src + at * (D / 2), n * (16 * D / 2), &bar[st]);
+          else if (part == 1)
+            bulk_load(dst + KC * D / 2 + half * (16 * D / 2), src + (p.page + at) * (D / 2), n * (16 * D / 2), &bar[st]);
+          else
+            bulk_load(dst + KC * D + half * 128, src + (long long)p.page * D + at * 8, n * 128, &bar[st]);
+        }
+      };
+      if (!first) {                              // the ring's memory was read and written as the join's
+        fence_proxy_async_smem();
+        __syncthreads();
+      }
+      first = false;
+      uint32_t ist = stage;
+      int ic = c0;
+      for (int i = 0; i < NS - 1; ++i, ic += WARPS) {
+        if (ic < c_hi) {
+          issue(ic, page_of(ic), ist);
+          ist = ist + 1 == NS ? 0 : ist + 1;
+        }
+      }
+      int next_page = page_of(ic);
+
+      // ---- the query rows as B fragments
+      State<D, NT> st;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int r = rt * R + 8 * n + g;
+        float mx = 0.0f, sum = 0.0f;
+        uint4 raw[KW];
+#pragma unroll
+        for (int w = 0; w < KW; ++w) raw[w] = make_uint4(0u, 0u, 0u, 0u);
+        if (8 * n + g < rows) {
+          const int i = r / p.G, hq = h * p.G + r - i * p.G;
+          const uint16_t* qp = reinterpret_cast<const uint16_t*>(p.Q) + (sq.tok0 + i) * p.ldq + (long long)hq * D + t * KW * 8;
+#pragma unroll
+          for (int w = 0; w < KW; ++w) raw[w] = *reinterpret_cast<const uint4*>(qp + 8 * w);
+        }
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {
+          float v[8];
+          if (p.q_f16) unpack8<F16>(&raw[w], v); else unpack8<BF16>(&raw[w], v);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            mx = fmaxf(mx, fabsf(v[k]));
+            sum += v[k];
+          }
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        int e = 14 - ((int)(__float_as_uint(mx) >> 23) - 127);
+        e = mx == 0.0f || mx > 3.0e38f ? 0 : max(-126, min(126, e));
+        const float f = pow2(e);
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {
+          float v[8];
+          if (p.q_f16) unpack8<F16>(&raw[w], v); else unpack8<BF16>(&raw[w], v);
+          st.q[n][4 * w] = pack_half2(v[0] * f, v[4] * f);
+          st.q[n][4 * w + 1] = pack_half2(v[1] * f * 0.0625f, v[5] * f * 0.0625f);
+          st.q[n][4 * w + 2] = pack_half2(v[2] * f, v[6] * f);
+          st.q[n][4 * w + 3] = pack_half2(v[3] * f * 0.0625f, v[7] * f * 0.0625f);
+        }
+        const float rs = sum * f, rc = p.scale_log2 * pow2(-e);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {            // rows 2t, 2t + 1 of the n-tile, from the lanes that read them
+          st.rq[n][i] = __shfl_sync(0xffffffffu, rs, 4 * (2 * t + i));
+          st.rowc[n][i] = __shfl_sync(0xffffffffu, rc, 4 * (2 * t + i));
+          const int rr = 8 * n + 2 * t + i, tk = (rt * R + rr) / p.G;
+          const long long lo = p.window > 0 ? (long long)pos0 + tk - p.window + 1 : 0;
+          st.lo[n][i] = lo > 0 ? (lo < 0x7FFFFFFF ? (int)lo : 0x7FFFFFFF) : 0;
+          st.hi[n][i] = rr >= rows ? -1 : (p.causal ? min(sq.len - 1, pos0 + tk) : sq.len - 1);
+          st.mrc[n][i] = 0.0f;
+          st.thr[n][i] = -CUDART_INF_F;
+          st.l[n][i] = 0.0f;
+          st.low[n][i] = 0.0f;
+        }
+#pragma unroll
+        for (int m = 0; m < D / 16; ++m)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) st.o[m][n][i] = 0.0f;
+      }
+      st.vlim = pow2(-24);
+      st.vinv = pow2(kVExp + 25);
+
+      // ---- this warp's chunks
+      for (int c = c0; c < c_hi && !dead; c += WARPS) {
+        if (ic < c_hi) {
+          issue(ic, next_page, ist);
+          ist = ist + 1 == NS ? 0 : ist + 1;
+          ic += WARPS;
+          next_page = page_of(ic);
+        }
+        if (!mbar_wait_bounded(&bar[stage], (phase >> stage) & 1u, nullptr)) {
+          if (lane == 0) report_device_error(err, DEVERR_TIMEOUT);
+          dead = true;
+        }
+        phase ^= 1u << stage;
+        const uint32_t base = ring + stage * C::STAGE;
+        const int key0 = c * KC;
+        if (key0 >= lo_max && key0 + KC <= hi_min) chunk<D, NT, false>(st, base, key0, g, t);
+        else chunk<D, NT, true>(st, base, key0, g, t);
+        stage = stage + 1 == NS ? 0 : stage + 1;
+        __syncwarp();                            // every lane has read the stage before it is filled again
+      }
+
+      // ---- the four warps meet
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int o = 4; o <= 16; o <<= 1) {
+            st.l[n][i] += __shfl_xor_sync(0xffffffffu, st.l[n][i], o);
+            st.low[n][i] += __shfl_xor_sync(0xffffffffu, st.low[n][i], o);
+          }
+          if (g == 0) {
+            const int r = 8 * n + 2 * t + i;
+            red[warp * R + r] = st.thr[n][i] == -CUDART_INF_F ? (st.l[n][i] != 0.0f ? 0.0f : -CUDART_INF_F) : st.mrc[n][i];
+            red[(WARPS + warp) * R + r] = st.l[n][i];
+            red[(2 * WARPS + warp) * R + r] = st.low[n][i];
+          }
+        }
+      dead = __syncthreads_or(dead);             // every warp is done with its ring
+      float* ob = reinterpret_cast<float*>(smem) + warp * R * C::RED_LD;
+      const float ue = 16777216.0f / st.vinv, uo = ue * 0.0625f;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int w = 0; w < VW; ++w)
+#pragma unroll
+            for (int by = 0; by < 4; by += 2) {
+              const int m = 4 * w + by;
+              *reinterpret_cast<float4*>(ob + (8 * n + 2 * t + i) * C::RED_LD + (VW * g + w) * 8 + 2 * by) =
+                  make_float4(st.o[m][n][i] * ue, st.o[m][n][2 + i] * uo, st.o[m + 1][n][i] * ue, st.o[m + 1][n][2 + i] * uo);
+            }
+      __syncthreads();
+      float* out = p.part + (2LL * blockIdx.x + (lead ? 0 : 1)) * C::PART;
+      for (int x = tid; x < R * (D / 4); x += THREADS) {
+        const int r = x / (D / 4), d = (x - r * (D / 4)) * 4;
+        if (r >= rows) continue;
+        float mm = -CUDART_INF_F, ll = 0.0f, lw = 0.0f;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) mm = fmaxf(mm, red[w * R + r]);
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+          const float mw = red[w * R + r];
+          if (mw == -CUDART_INF_F) continue;
+          const float f = ex2(mw - mm);
+          ll = fmaf(f, red[(WARPS + w) * R + r], ll);
+          lw = fmaf(f, red[(2 * WARPS + w) * R + r], lw);
+          const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<float*>(smem) + (w * R + r) * C::RED_LD + d);
+          acc.x = fmaf(f, v.x, acc.x); acc.y = fmaf(f, v.y, acc.y);
+          acc.z = fmaf(f, v.z, acc.z); acc.w = fmaf(f, v.w, acc.w);
+        }
+        acc.x += lw; acc.y += lw; acc.z += lw; acc.w += lw;
+        if (whole) {
+          const int rr = rt * R + r, i = rr / p.G, hq = h * p.G + rr - i * p.G;
+          const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+          store_out(p, (sq.tok0 + i) * p.ldo + (long long)hq * D + d,
+                    make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+          if (p.lse && d == 0)
+            p.lse[(sq.tok0 + i) * p.Hq + hq] = ll == 0.0f ? -CUDART_INF_F : (mm + log2f(ll)) * 0.6931471805599453f;
+        } else {
+          *reinterpret_cast<float4*>(out + r * D + d) = acc;
+          if (d == 0) {
+            out[R * D + r] = mm;
+            out[R * D + R + r] = ll;
+          }
+        }
+      }
+      off += tn;
+      left -= tn;
+    }
+  }
+  if (dead) {                                    // copies still in flight (none otherwise)
+    for (int i = 0; i < NS; ++i) mbar_wait_bounded(&bar[i], (phase >> i) & 1u, nullptr, 1000000ull);
+  }
+}
+
+// Joins the parts of the items that were cut between CTAs: one warp per query token and head.
+template <int D, int NT>
+__global__ void __launch_bounds__(THREADS) kv_combine_kernel(Params p, int* __restrict__ err) {
+  using C = Cfg<D, NT>;
+  constexpr int R = C::R, VPL = D / 32;
   const int lane = threadIdx.x & 31;
   const long long unit = (long long)blockIdx.x * WARPS + (threadIdx.x >> 5);
+  grid_dep_wait();
   const long long tok = unit / p.Hq;
   if (tok >= p.total_q) return;
-  const int hq = (int)(unit - tok * p.Hq), h = hq / (p.Hq / p.H);
-  int lo = 0, hi = p.batch;                              // the last sequence that starts at or before tok
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (p.cu_q[mid] <= tok) lo = mid; else hi = mid - 1;
+  const int hq = (int)(unit - tok * p.Hq), h = hq / p.G;
+  int a = 0, z = p.batch - 1;                    // the last sequence that starts at or before tok
+  while (a < z) {
+    const int mid = (a + z + 1) >> 1;
+    if (p.cu_q[mid] <= tok) a = mid; else z = mid - 1;
   }
-  const int b = lo;
-  if (b >= p.batch || tok < p.cu_q[0]) return;
-  const long long nq = (long long)p.cu_q[b + 1] - p.cu_q[b];
-  long long len = p.kv_lens[b];
-  if (len < 0 || len > p.table_width * p.page) {
-    if (lane == 0) report_device_error(err, DEVERR_INDEX);
-    len = len < 0 ? 0 : p.table_width * p.page;
-  }
-  const long long pos = len - nq + (tok - p.cu_q[b]);
-  const long long end = p.causal ? (pos + 1 < len ? pos + 1 : len) : len;
-  const long long begin = (p.window > 0 && pos - p.window + 1 > 0) ? pos - p.window + 1 : 0;
-  float q[VPL], o[VPL];
-  const typename E::T* qp = reinterpret_cast<const typename E::T*>(p.Q) + tok * p.ldq + (long long)hq * D + lane * VPL;
+  const Seq sq = load_seq(p, a, R, err);
+  if (tok < sq.tok0 || tok >= sq.tok0 + sq.nq) return;
+  const int rr = (int)(tok - sq.tok0) * p.G + hq - h * p.G, rt = rr / R, r = rr - rt * R;
+  const long long per = p.offs[p.batch], s0 = p.offs[a] + ((long long)h * sq.nrt + rt) * sq.tiles, s1 = s0 + sq.tiles - 1;
+  const long long c0 = s0 / per, c1 = s1 / per;
+  if (c0 == c1) return;                          // one CTA had the whole item and wrote it
+  const int np = (int)(c1 - c0) + 1;
+  // the first CTA's part is its second when the item starts inside that CTA's units
+  auto part_of = [&](int k) { return p.part + (2 * (c0 + k) + (k == 0 ? 1 : 0)) * C::PART; };
+  float mm = -CUDART_INF_F;
+  for (int k = lane; k < np; k += 32) mm = fmaxf(mm, part_of(k)[R * D + r]);
 #pragma unroll
-  for (int k = 0; k < VPL; ++k) { q[k] = (float)qp[k]; o[k] = 0.0f; }
-  float m = -CUDART_INF_F, sum = 0.0f;
-  const long long block = (long long)p.page * (D + 8);
-  for (long long j = begin; j < end; ++j) {
-    const int page = p.table[b * p.ldt + j / p.page], at = (int)(j % p.page);
-    if (page < 0 || page >= p.num_pages) {
-      if (lane == 0) report_device_error(err, DEVERR_INDEX);
-      continue;
+  for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+  float ll = 0.0f, acc[VPL];
+#pragma unroll
+  for (int k = 0; k < VPL; ++k) acc[k] = 0.0f;
+  for (int k0 = 0; k0 < np; k0 += 32) {
+    float f = 0.0f;
+    if (k0 + lane < np) {
+      const float* pt = part_of(k0 + lane);
+      const float mk = pt[R * D + r];
+      f = mk == -CUDART_INF_F ? 0.0f : ex2(mk - mm);
+      if (f != 0.0f) ll = fmaf(f, pt[R * D + R + r], ll);
     }
-    const uint8_t* blk = p.pool + ((long long)page * p.H + h) * block;
-    const uint16_t* n = reinterpret_cast<const uint16_t*>(blk + (long long)p.page * D) + 4 * at;
-    float num[4];
+    const int n = min(32, np - k0);
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) {
+      const float fk = __shfl_sync(0xffffffffu, f, k);
+      const float* pt = part_of(k0 + k) + r * D + lane * VPL;
+      if (fk != 0.0f) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) num[k] = __half2float(__ushort_as_half(n[k]));
-    const uint8_t* kc = blk + (long long)at * (D / 2) + lane * (VPL / 2);
-    const uint8_t* vc = kc + (long long)p.page * (D / 2);
-    float dot = 0.0f;
-#pragma unroll
-    for (int k = 0; k < VPL / 2; ++k) {
-      dot = fmaf(q[2 * k], fmaf((float)(kc[k] & 15), num[0], num[1]), dot);
-      dot = fmaf(q[2 * k + 1], fmaf((float)(kc[k] >> 4), num[0], num[1]), dot);
-    }
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, s);
-    const float x = dot * p.scale_log2, mn = fmaxf(m, x);
-    const float f = mn == -CUDART_INF_F ? 0.0f : exp2f(m - mn), e = mn == -CUDART_INF_F ? 0.0f : exp2f(x - mn);
-    m = mn;
-    sum = fmaf(sum, f, e);
-#pragma unroll
-    for (int k = 0; k < VPL / 2; ++k) {
-      o[2 * k] = fmaf(e, fmaf((float)(vc[k] & 15), num[2], num[3]), o[2 * k] * f);
-      o[2 * k + 1] = fmaf(e, fmaf((float)(vc[k] >> 4), num[2], num[3]), o[2 * k + 1] * f);
+        for (int x = 0; x < VPL; ++x) acc[x] = fmaf(fk, pt[x], acc[x]);
+      }
     }
   }
-  typename E::T* op = reinterpret_cast<typename E::T*>(p.O) + tok * p.ldo + (long long)hq * D + lane * VPL;
-  const float inv = begin < end ? 1.0f / sum : 0.0f;
 #pragma unroll
-  for (int k = 0; k < VPL; ++k) {
-    float x = o[k] * inv;
-    if (std::is_same<E, F16>::value && x == x) x = fminf(fmaxf(x, -65504.0f), 65504.0f);
-    op[k] = (typename E::T)x;
+  for (int o = 16; o > 0; o >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, o);
+  const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+#pragma unroll
+  for (int x = 0; x < VPL; ++x) {
+    float v = acc[x] * inv;
+    const long long at = tok * p.ldo + (long long)hq * D + lane * VPL + x;
+    if (p.q_f16) {
+      v = v == v ? fminf(fmaxf(v, -65504.0f), 65504.0f) : v;
+      reinterpret_cast<__half*>(p.O)[at] = __float2half_rn(v);
+    } else {
+      reinterpret_cast<__nv_bfloat16*>(p.O)[at] = __float2bfloat16_rn(v);
+    }
   }
-  if (p.lse && lane == 0) p.lse[tok * p.Hq + hq] = begin < end ? (m + log2f(sum)) * 0.6931471805599453f : -CUDART_INF_F;
+  if (p.lse && lane == 0) p.lse[tok * p.Hq + hq] = ll == 0.0f ? -CUDART_INF_F : (mm + log2f(ll)) * 0.6931471805599453f;
 }
+
+// Query rows of one head that a CTA takes at once: the eight columns of an n-tile times NT.
+int row_tiles(int D, long long rows) { return rows <= 8 ? 1 : (rows <= 16 || D == 256 ? 2 : 4); }
+
+template <typename F>
+void with_shape(int D, int nt, F&& f) {
+  auto go = [&](auto d) {
+    constexpr int DD = decltype(d)::value;
+    if (nt == 1) f(d, std::integral_constant<int, 1>{});
+    else if (nt == 2 || DD == 256) f(d, std::integral_constant<int, 2>{});
+    else if constexpr (DD != 256) f(d, std::integral_constant<int, 4>{});
+  };
+  if (D == 64) go(std::integral_constant<int, 64>{});
+  else if (D == 128) go(std::integral_constant<int, 128>{});
+  else go(std::integral_constant<int, 256>{});
+}
+
+size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 }  // namespace kva
 
-size_t kv_attention_workspace_bytes(long long, int, int, int, long long, long long) { return 256; }
+// Workspace: the batch's sums of units, and two parts per CTA.
+size_t kv_attention_workspace_bytes(long long total_q, int Hq, int H, int D, long long batch, long long max_q) {
+  using namespace kva;
+  (void)total_q;
+  size_t bytes = 0;
+  with_shape(D, row_tiles(D, max_q * (Hq / H)), [&](auto d, auto n) {
+    using C = Cfg<decltype(d)::value, decltype(n)::value>;
+    bytes = round256(8 * (size_t)(batch + 1)) + (size_t)sm_count() * C::OCC * 2 * C::PART * 4;
+  });
+  return bytes;
+}
 
 gptq_status kv_attention_launch(const void* Q, int dtype, long long total_q, int Hq, int H, int D, long long ldq,
                                 const int* cu_q, const int* kv_lens, const int* table, long long ldt,
@@ -112,27 +777,39 @@ gptq_status kv_attention_launch(const void* Q, int dtype, long long total_q, int
                                 long long num_pages, int page, float sm_scale, int causal, long long window, void* O,
                                 long long ldo, float* lse, void* ws, cudaStream_t s) {
   using namespace kva;
-  (void)ws;
-  (void)max_q;
   Params p{};
   p.Q = Q; p.O = O; p.lse = lse; p.cu_q = cu_q; p.kv_lens = kv_lens; p.table = table;
   p.pool = reinterpret_cast<const uint8_t*>(pool);
   p.ldq = ldq; p.ldo = ldo; p.ldt = ldt; p.total_q = total_q; p.table_width = table_width; p.num_pages = num_pages;
-  p.Hq = Hq; p.H = H; p.page = page; p.batch = (int)batch; p.causal = causal; p.window = window;
+  p.Hq = Hq; p.H = H; p.G = Hq / H; p.page = page; p.batch = (int)batch; p.causal = causal; p.q_f16 = dtype == GPTQ_F16;
+  const int p16 = page / 16;
+  p.page_mul = p16 == 1 ? 0u : (uint32_t)((0x100000000ULL + (unsigned)p16 - 1) / (unsigned)p16);
+  p.window = window;
   p.scale_log2 = sm_scale * 1.4426950408889634f;
-  const long long grid = (total_q * Hq + WARPS - 1) / WARPS;
-  if (grid > 0x7FFFFFFFLL) return set_error(GPTQ_ERR_INVALID_ARG, "too many query heads for one launch");
-  auto go = [&](auto e, auto d) {
-    kv_attention_kernel<decltype(e), decltype(d)::value><<<(unsigned)grid, WARPS * 32, 0, s>>>(p, device_error_word());
-  };
-  auto width = [&](auto e) {
-    if (D == 64) go(e, std::integral_constant<int, 64>{});
-    else if (D == 128) go(e, std::integral_constant<int, 128>{});
-    else go(e, std::integral_constant<int, 256>{});
-  };
-  if (dtype == GPTQ_BF16) width(BF16{}); else width(F16{});
-  count_launch();
-  return check_launch("kv_attention_kernel");
+  const long long grid2 = (total_q * Hq + WARPS - 1) / WARPS;
+  if (grid2 > 0x7FFFFFFFLL) return set_error(GPTQ_ERR_INVALID_ARG, "too many query heads for one launch");
+  p.offs = reinterpret_cast<long long*>(ws);
+  p.part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(ws) + round256(8 * (size_t)(batch + 1)));
+  gptq_status st = GPTQ_OK;
+  with_shape(D, row_tiles(D, max_q * p.G), [&](auto d, auto n) {
+    constexpr int DD = decltype(d)::value, NT = decltype(n)::value;
+    using C = Cfg<DD, NT>;
+    static bool attr_done = false;
+    if (!attr_done) {
+      if (cudaFuncSetAttribute(kv_split_kernel<DD, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) {
+        st = set_error(GPTQ_ERR_CUDA, "cudaFuncSetAttribute(kv_split_kernel) failed");
+        return;
+      }
+      attr_done = true;
+    }
+    kv_split_kernel<DD, NT><<<(unsigned)(sm_count() * C::OCC), THREADS, C::SMEM, s>>>(p, device_error_word());
+    count_launch();
+    if ((st = check_launch("kv_split_kernel"))) return;
+    launch_pdl(kv_combine_kernel<DD, NT>, dim3((unsigned)grid2), dim3(THREADS), 0, s, p, device_error_word());
+    count_launch();
+    st = check_launch("kv_combine_kernel");
+  });
+  return st;
 }
 
 }  // namespace gptq
