@@ -63,6 +63,38 @@ template <> __device__ __forceinline__ void pack8<F16>(void* p, const float (&v)
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Four consecutive values (8-byte accesses; 16 bytes for fp32); Raw4 is their bits.
+template <typename E> struct Raw4 { using T = uint2; };
+template <> struct Raw4<F32> { using T = float4; };
+template <typename E> __device__ __forceinline__ void unpack4(const void* p, float* v);
+template <typename E> __device__ __forceinline__ void pack4(void* p, const float* v);
+template <> __device__ __forceinline__ void unpack4<F32>(const void* p, float* v) {
+  const float4 a = *reinterpret_cast<const float4*>(p);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+}
+template <> __device__ __forceinline__ void unpack4<BF16>(const void* p, float* v) {
+  const uint2 a = *reinterpret_cast<const uint2*>(p);
+  v[0] = __uint_as_float(a.x << 16); v[1] = __uint_as_float(a.x & 0xFFFF0000u);
+  v[2] = __uint_as_float(a.y << 16); v[3] = __uint_as_float(a.y & 0xFFFF0000u);
+}
+template <> __device__ __forceinline__ void unpack4<F16>(const void* p, float* v) {
+  const uint2 a = *reinterpret_cast<const uint2*>(p);
+  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a.x));
+  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&a.y));
+  v[0] = x.x; v[1] = x.y; v[2] = y.x; v[3] = y.y;
+}
+template <> __device__ __forceinline__ void pack4<F32>(void* p, const float* v) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+template <> __device__ __forceinline__ void pack4<BF16>(void* p, const float* v) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+template <> __device__ __forceinline__ void pack4<F16>(void* p, const float* v) {
+  const __half2 a = __floats2half2_rn(v[0], v[1]), b = __floats2half2_rn(v[2], v[3]);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
 // Call f with the element type of a dtype code (checked by the caller).
 template <typename F>
 inline void with_dtype(int dtype, F&& f) {

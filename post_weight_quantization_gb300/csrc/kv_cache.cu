@@ -5,14 +5,12 @@
 //
 // One page of one head is one block: K codes of its page_size tokens, V codes, then four
 // fp16 per token (K scale, K low, V scale, V low), so attention fetches a page of a head
-// with one contiguous copy. A row (K or V of one token and head) lies in LPR = D / 8
-// lanes, eight values each: one 16-byte load and one word of eight codes per lane.
+// with one contiguous copy.
 //
-// The division is exact to the last bit without a division per value: with
-// r = fl(1 / scale), q = fl(a r), q' = fl(q + fl(a - q scale) r) is the correctly rounded
-// a / scale (Markstein, "Computation of elementary functions on the IBM RISC System/6000
-// processor", 1990), and a is limited to [0, 15 scale] first, which limits the quotient
-// to [0, 15] exactly and keeps infinities out.
+// The divisions are exact to the last bit without the divide's instructions: with
+// r = fl(1 / s), q = fl(a r), q' = fl(q + fl(a - q s) r) is the correctly rounded
+// a / s (Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990); code_of has the limits.
 //
 // Bound: HBM bandwidth (16-bit rows read once, D / 2 + 4 bytes written per row).
 #include <type_traits>
@@ -36,6 +34,89 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
+__device__ __forceinline__ float2 to_float2(__half2 h) { return __half22float2(h); }
+__device__ __forceinline__ float2 to_float2(__nv_bfloat162 h) { return __bfloat1622float2(h); }
+__device__ __forceinline__ __half2 lows_of(__half2 a, __half2 b) { return __lows2half2(a, b); }
+__device__ __forceinline__ __half2 highs_of(__half2 a, __half2 b) { return __highs2half2(a, b); }
+__device__ __forceinline__ __nv_bfloat162 lows_of(__nv_bfloat162 a, __nv_bfloat162 b) { return __lows2bfloat162(a, b); }
+__device__ __forceinline__ __nv_bfloat162 highs_of(__nv_bfloat162 a, __nv_bfloat162 b) { return __highs2bfloat162(a, b); }
+
+// a / s, correctly rounded, with inv = fl(1 / s).
+__device__ __forceinline__ float divide(float a, float s, float inv) {
+  const float q = __fmul_rn(a, inv);
+  return __fmaf_rn(__fmaf_rn(-q, s, a), inv, q);
+}
+// fl(1 / s) of an fp16 value: the hardware's approximation and one Newton step (checked for
+// every positive fp16 value).
+__device__ __forceinline__ float reciprocal(float s) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(s));
+  return __fmaf_rn(__fmaf_rn(-s, y, 1.0f), y, y);
+}
+
+// Sixteen values of a row as they lie in memory: eight at 8 l and eight at D / 2 + 8 l of lane l.
+template <typename E> struct alignas(16) Row8 { uint32_t w[4]; };
+template <> struct alignas(16) Row8<F32> { uint32_t w[8]; };
+template <typename E> struct Row16 { Row8<E> r[2]; };
+
+// Smallest and largest value of a row (NaN if it holds one) over its LANES lanes: pairs at a
+// time for the 16-bit types, the lanes' (minimum, -maximum) as one pair.
+template <typename E, int LANES>
+__device__ __forceinline__ void row_range(const Row16<E>& r, float& lo, float& hi) {
+  if constexpr (std::is_same<E, F32>::value) {
+    lo = hi = __uint_as_float(r.r[0].w[0]);
+#pragma unroll
+    for (int k = 1; k < 16; ++k) {
+      const float v = __uint_as_float(r.r[k >> 3].w[k & 7]);
+      lo = min_nan(lo, v);
+      hi = max_nan(hi, v);
+    }
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) {
+      lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
+  } else {
+    using P = typename std::conditional<std::is_same<E, BF16>::value, __nv_bfloat162, __half2>::type;
+    const P *p = reinterpret_cast<const P*>(r.r[0].w), *q = reinterpret_cast<const P*>(r.r[1].w);
+    P mn = __hmin2_nan(p[0], q[0]), mx = __hmax2_nan(p[0], q[0]);
+#pragma unroll
+    for (int k = 1; k < 4; ++k) {
+      mn = __hmin2_nan(mn, __hmin2_nan(p[k], q[k]));
+      mx = __hmax2_nan(mx, __hmax2_nan(p[k], q[k]));
+    }
+    mx = __hneg2(mx);
+    P both = __hmin2_nan(lows_of(mn, mx), highs_of(mn, mx));
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) {
+      uint32_t w = __shfl_xor_sync(0xffffffffu, *reinterpret_cast<uint32_t*>(&both), o);
+      both = __hmin2_nan(both, *reinterpret_cast<P*>(&w));
+    }
+    const float2 f = to_float2(both);
+    lo = f.x;
+    hi = -f.y;
+  }
+}
+
+// The code of x in fp32: round((x - low) / s) limited to [0, 15], ties to even. The limit from
+// above is put on the numerator (15 s / s is 15 exactly, and an infinity stays out of the
+// correction); the conversion to an unsigned integer limits from below.
+__device__ __forceinline__ uint32_t code_of(float x, float low, float s, float inv, float top) {
+  const float q = divide(fminf(__fsub_rn(x, low), top), s, inv);
+  uint32_t c;
+  asm("cvt.rni.u32.f32 %0, %1;" : "=r"(c) : "f"(q));
+  return c;
+}
+
+// A warp takes one token and NB * RPW / 2 heads of it (RPW rows at once): NB rows per lane
+// group, whose loads are all in flight before the first is used (the token's slot and its
+// page, a 64-bit multiply by a host-computed reciprocal instead of a division, are the same
+// for all of them). Appending, a lane holds 16 values of a row, so that a row's statistics,
+// which all its lanes compute, cost half as much as with eight: the kernel is bound by
+// instruction issue before bandwidth.
+constexpr int NB_APPEND = 2, NB_READ = 4;
+template <int D> constexpr int append_lanes() { return D / 16; }
+
 struct Params {
   const void* x[2];            // K, V
   long long ldx[2];
@@ -43,102 +124,149 @@ struct Params {
   long long ldy[2];
   const long long* slots;
   uint8_t* pool;
-  long long T, n_slots;        // tokens, num_pages * page_size
+  long long n_slots;           // num_pages * page_size
+  unsigned long long page_inv; // ceil(2^64 / page_size): slot * page_size < 2^48, so the high word is exact
+  uint32_t T, blocks;          // tokens, head blocks per token
   int H, page;
 };
 
-template <int LPR>
-__device__ __forceinline__ uint8_t* block_of(const Params& p, long long slot, int h, int& at) {
-  constexpr int D = 8 * LPR;
-  const long long page = slot / p.page;
+// The token and the first head of a warp's unit; false past the last token.
+template <int HEADS>
+__device__ __forceinline__ bool unit_of(const Params& p, uint32_t& t, int& h0) {
+  const uint32_t unit = blockIdx.x * WARPS + (threadIdx.x >> 5);
+  t = unit / p.blocks;
+  h0 = (int)(unit - t * p.blocks) * HEADS;
+  return t < p.T;
+}
+
+template <int D>
+__device__ __forceinline__ uint8_t* page_of(const Params& p, long long slot, int& at) {
+  const long long page = (long long)__umul64hi((unsigned long long)slot, p.page_inv);
   at = (int)(slot - page * p.page);
-  return p.pool + (page * p.H + h) * ((long long)p.page * (D + 8));
+  return p.pool + page * p.H * ((long long)p.page * (D + 8));
 }
 
-// Row r of the call: r = (token * H + head) * 2 + (0: K, 1: V).
-template <typename E, int LPR>
+template <typename E, int D>
 __global__ void __launch_bounds__(WARPS * 32) kv_append_kernel(Params p, int* __restrict__ err) {
-  constexpr int D = 8 * LPR, RPW = 32 / LPR;
-  const int lane = threadIdx.x & 31, l = lane % LPR;
-  const long long r = ((long long)blockIdx.x * WARPS + (threadIdx.x >> 5)) * RPW + lane / LPR;
-  const long long th = r >> 1;
-  const long long t = th / p.H;
-  const int h = (int)(th - t * p.H), kv = (int)(r & 1);
-  bool live = t < p.T;
-  const long long slot = live ? p.slots[t] : -1;
-  if (slot >= p.n_slots && l == 0) report_device_error(err, DEVERR_INDEX);
-  live = slot >= 0 && slot < p.n_slots;
-  float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-  if (live) unpack8<E>(reinterpret_cast<const typename E::T*>(p.x[kv]) + t * p.ldx[kv] + (long long)h * D + 8 * l, v);
-  float lo = v[0], hi = v[0];
-#pragma unroll
-  for (int k = 1; k < 8; ++k) { lo = min_nan(lo, v[k]); hi = max_nan(hi, v[k]); }
-#pragma unroll
-  for (int o = LPR / 2; o > 0; o >>= 1) {
-    lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-  }
-  const bool bad = lo != lo;
-  lo = bad ? 0.0f : fminf(fmaxf(lo, -kHalfMax), kHalfMax);     // a NaN row: codes of 0, its scale says the rest
-  hi = bad ? 0.0f : fminf(fmaxf(hi, -kHalfMax), kHalfMax);
-  const __half hs = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.0f)), hl = __float2half_rn(lo);
-  const float sc = __half2float(hs), low = __half2float(hl);
-  const float inv = sc > 0.0f ? __frcp_rn(sc) : 0.0f, top = 15.0f * sc;
-  uint32_t word = 0;
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const float a = fminf(fmaxf(__fsub_rn(v[k], low), 0.0f), top);
-    float q = __fmul_rn(a, inv);
-    q = __fmaf_rn(__fmaf_rn(-q, sc, a), inv, q);
-    // 2^23 + q rounds q to an integer, ties to even, in the mantissa's low bits
-    word |= (__float_as_uint(__fadd_rn(q, 8388608.0f)) & 15u) << (4 * k);
-  }
-  if (!live) return;
-  int at;
-  uint8_t* b = block_of<LPR>(p, slot, h, at);
-  reinterpret_cast<uint32_t*>(b + ((long long)kv * p.page + at) * (D / 2))[l] = word;
-  if (l == 0) {
-    const uint32_t s16 = bad ? 0x7FFFu : (uint32_t)__half_as_ushort(hs);
-    reinterpret_cast<uint32_t*>(b + (long long)p.page * D)[2 * at + kv] = s16 | ((uint32_t)__half_as_ushort(hl) << 16);
-  }
-}
-
-template <typename E, int LPR>
-__global__ void __launch_bounds__(WARPS * 32) kv_read_kernel(Params p, int* __restrict__ err) {
-  constexpr int D = 8 * LPR, RPW = 32 / LPR;
-  const int lane = threadIdx.x & 31, l = lane % LPR;
-  const long long r = ((long long)blockIdx.x * WARPS + (threadIdx.x >> 5)) * RPW + lane / LPR;
-  const long long th = r >> 1;
-  const long long t = th / p.H;
-  const int h = (int)(th - t * p.H), kv = (int)(r & 1);
-  if (t >= p.T) return;
+  constexpr int NB = NB_APPEND, LANES = append_lanes<D>(), RPW = 32 / LANES;
+  const int lane = threadIdx.x & 31, l = lane % LANES, sub = lane / LANES;
+  uint32_t t;
+  int h0;
+  if (!unit_of<NB * RPW / 2>(p, t, h0)) return;
   const long long slot = p.slots[t];
-  float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-  if (slot >= p.n_slots) {
-    if (l == 0) report_device_error(err, DEVERR_INDEX);
-  } else if (slot >= 0) {
-    int at;
-    const uint8_t* b = block_of<LPR>(p, slot, h, at);
-    const uint32_t word = reinterpret_cast<const uint32_t*>(b + ((long long)kv * p.page + at) * (D / 2))[l];
-    const uint32_t n = reinterpret_cast<const uint32_t*>(b + (long long)p.page * D)[2 * at + kv];
-    const float sc = __half2float(__ushort_as_half((unsigned short)n));
-    const float low = __half2float(__ushort_as_half((unsigned short)(n >> 16)));
+  Row16<E> raw[NB];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = fmaf((float)((word >> (4 * k)) & 15u), sc, low);
-    if (std::is_same<E, F16>::value) {                  // 15 scale + low can round past fp16's range
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (v[k] == v[k]) v[k] = fminf(fmaxf(v[k], -kHalfMax), kHalfMax);
+  for (int i = 0; i < NB; ++i) {                        // row i * RPW + sub: K and V of a head in turn
+    const int row = i * RPW + sub, h = h0 + (row >> 1), kv = row & 1;
+    raw[i] = Row16<E>{};
+    if (h < p.H) {
+      const typename E::T* x = reinterpret_cast<const typename E::T*>(kv ? p.x[1] : p.x[0]) +
+                               t * (kv ? p.ldx[1] : p.ldx[0]) + h * D + 8 * l;
+      raw[i].r[0] = *reinterpret_cast<const Row8<E>*>(x);
+      raw[i].r[1] = *reinterpret_cast<const Row8<E>*>(x + D / 2);
     }
   }
-  pack8<E>(reinterpret_cast<typename E::T*>(p.y[kv]) + t * p.ldy[kv] + (long long)h * D + 8 * l, v);
+  if (slot < 0) return;
+  if (slot >= p.n_slots) {
+    if (lane == 0) report_device_error(err, DEVERR_INDEX);
+    return;
+  }
+  int at;
+  uint8_t* page = page_of<D>(p, slot, at);
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    const int row = i * RPW + sub, h = h0 + (row >> 1), kv = row & 1;
+    float lo, hi;
+    row_range<E, LANES>(raw[i], lo, hi);
+    const bool bad = lo != lo;
+    lo = bad ? 0.0f : fminf(fmaxf(lo, -kHalfMax), kHalfMax);   // a NaN row: codes of 0, its scale says the rest
+    hi = bad ? 0.0f : fminf(fmaxf(hi, -kHalfMax), kHalfMax);
+    constexpr float kFifteenth = 1.0f / 15.0f;
+    const __half hs = __float2half_rn(divide(__fsub_rn(hi, lo), 15.0f, kFifteenth)), hl = __float2half_rn(lo);
+    const float sc = __half2float(hs), low = __half2float(hl);
+    const float inv = sc > 0.0f ? reciprocal(sc) : 0.0f, top = 15.0f * sc;
+    uint32_t word[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      float v[8];
+      unpack8<E>(&raw[i].r[x], v);
+      word[x] = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) word[x] += code_of(v[k], low, sc, inv, top) << (4 * k);
+    }
+    if (h >= p.H) continue;
+    uint8_t* b = page + (long long)h * p.page * (D + 8);
+    uint32_t* c = reinterpret_cast<uint32_t*>(b + (kv * p.page + at) * (D / 2));
+    c[l] = word[0];
+    c[D / 16 + l] = word[1];
+    if (l == 0) {
+      const uint32_t s16 = bad ? 0x7FFFu : (uint32_t)__half_as_ushort(hs);
+      reinterpret_cast<uint32_t*>(b + p.page * D)[2 * at + kv] = s16 | ((uint32_t)__half_as_ushort(hl) << 16);
+    }
+  }
+}
+
+template <typename E, int D>
+__global__ void __launch_bounds__(WARPS * 32) kv_read_kernel(Params p, int* __restrict__ err) {
+  constexpr int NB = NB_READ, LPR = D / 8, RPW = 32 / LPR;
+  const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
+  uint32_t t;
+  int h0;
+  if (!unit_of<NB * RPW / 2>(p, t, h0)) return;
+  const long long slot = p.slots[t];
+  uint32_t word[NB], num[NB];
+  const bool live = slot >= 0 && slot < p.n_slots;
+  if (slot >= p.n_slots && lane == 0) report_device_error(err, DEVERR_INDEX);
+  int at = 0;
+  const uint8_t* page = live ? page_of<D>(p, slot, at) : nullptr;
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    const int row = i * RPW + sub, h = h0 + (row >> 1), kv = row & 1;
+    word[i] = num[i] = 0u;
+    if (live && h < p.H) {
+      const uint8_t* b = page + (long long)h * p.page * (D + 8);
+      word[i] = reinterpret_cast<const uint32_t*>(b + (kv * p.page + at) * (D / 2))[l];
+      num[i] = reinterpret_cast<const uint32_t*>(b + p.page * D)[2 * at + kv];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    const int row = i * RPW + sub, h = h0 + (row >> 1), kv = row & 1;
+    if (h >= p.H) continue;
+    const float sc = __half2float(__ushort_as_half((unsigned short)num[i]));
+    const float low = __half2float(__ushort_as_half((unsigned short)(num[i] >> 16)));
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      // 2^23 + code - 2^23: the code as a float without an integer conversion
+      const float c = __uint_as_float(((word[i] >> (4 * k)) & 15u) | 0x4B000000u) - 8388608.0f;
+      v[k] = fmaf(c, sc, low);
+      if (std::is_same<E, F16>::value && v[k] == v[k]) v[k] = fminf(fmaxf(v[k], -kHalfMax), kHalfMax);   // 15 scale + low can round past it
+    }
+    pack8<E>(reinterpret_cast<typename E::T*>(kv ? p.y[1] : p.y[0]) + t * (kv ? p.ldy[1] : p.ldy[0]) + h * D + 8 * l, v);
+  }
 }
 
 template <typename F>
 void with_width(int D, F&& f) {
-  if (D == 64) f(std::integral_constant<int, 8>{});
-  else if (D == 128) f(std::integral_constant<int, 16>{});
-  else f(std::integral_constant<int, 32>{});
+  if (D == 64) f(std::integral_constant<int, 64>{});
+  else if (D == 128) f(std::integral_constant<int, 128>{});
+  else f(std::integral_constant<int, 256>{});
+}
+
+// Fills in the sizes for warps of `heads` heads; returns the grid (0: too large).
+unsigned set_sizes(Params& p, long long T, int H, int heads, long long num_pages, int page, const long long* slots,
+                   void* pool) {
+  p.slots = slots;
+  p.pool = reinterpret_cast<uint8_t*>(pool);
+  p.n_slots = num_pages * page;
+  p.page_inv = ~0ULL / (unsigned)page + 1;             // page is no power of two, or one: ceil(2^64 / page) either way
+  p.T = (uint32_t)T;
+  p.blocks = (uint32_t)((H + heads - 1) / heads);
+  p.H = H;
+  p.page = page;
+  const unsigned long long units = (unsigned long long)p.T * p.blocks;
+  return units > 0xFFFFFFFFull - WARPS ? 0u : (unsigned)((units + WARPS - 1) / WARPS);
 }
 
 }  // namespace kvc
@@ -149,14 +277,11 @@ gptq_status kv_append_launch(const void* K, const void* V, int dtype, long long 
   using namespace kvc;
   Params p{};
   p.x[0] = K; p.x[1] = V; p.ldx[0] = ldk; p.ldx[1] = ldv;
-  p.slots = slots; p.pool = reinterpret_cast<uint8_t*>(pool);
-  p.T = T; p.n_slots = num_pages * page; p.H = H; p.page = page;
-  const long long rows = 2 * T * H, per = WARPS * (32 / (D / 8)), grid = (rows + per - 1) / per;
-  if (grid > 0x7FFFFFFFLL) return set_error(GPTQ_ERR_INVALID_ARG, "too many rows for one launch");
+  const unsigned grid = set_sizes(p, T, H, NB_APPEND * (32 / (D / 16)) / 2, num_pages, page, slots, pool);
+  if (!grid) return set_error(GPTQ_ERR_INVALID_ARG, "too many rows for one launch");
   with_dtype(dtype, [&](auto e) {
-    with_width(D, [&](auto lpr) {
-      kv_append_kernel<decltype(e), decltype(lpr)::value>
-          <<<(unsigned)grid, WARPS * 32, 0, s>>>(p, device_error_word());
+    with_width(D, [&](auto d) {
+      kv_append_kernel<decltype(e), decltype(d)::value><<<grid, WARPS * 32, 0, s>>>(p, device_error_word());
     });
   });
   count_launch();
@@ -168,13 +293,11 @@ gptq_status kv_read_launch(const void* pool, long long num_pages, int page, int 
   using namespace kvc;
   Params p{};
   p.y[0] = K; p.y[1] = V; p.ldy[0] = ldk; p.ldy[1] = ldv;
-  p.slots = slots; p.pool = reinterpret_cast<uint8_t*>(const_cast<void*>(pool));
-  p.T = T; p.n_slots = num_pages * page; p.H = H; p.page = page;
-  const long long rows = 2 * T * H, per = WARPS * (32 / (D / 8)), grid = (rows + per - 1) / per;
-  if (grid > 0x7FFFFFFFLL) return set_error(GPTQ_ERR_INVALID_ARG, "too many rows for one launch");
+  const unsigned grid = set_sizes(p, T, H, NB_READ * (32 / (D / 8)) / 2, num_pages, page, slots, const_cast<void*>(pool));
+  if (!grid) return set_error(GPTQ_ERR_INVALID_ARG, "too many rows for one launch");
   with_dtype(dtype, [&](auto e) {
-    with_width(D, [&](auto lpr) {
-      kv_read_kernel<decltype(e), decltype(lpr)::value><<<(unsigned)grid, WARPS * 32, 0, s>>>(p, device_error_word());
+    with_width(D, [&](auto d) {
+      kv_read_kernel<decltype(e), decltype(d)::value><<<grid, WARPS * 32, 0, s>>>(p, device_error_word());
     });
   });
   count_launch();
