@@ -1,91 +1,942 @@
 // A packed projection with the low-rank adapters of many requests beside it:
 //
 //   Y[t] = X[t] W_hat^T + alpha[a] (X[t] A[a]^T) B[a]^T,   a = ids[t]
+//   X[t] W_hat[r]^T = sum_g scale[r][g] * sum_{j in g} X[t][j] (code[r][j] - zero[r][g])
 //
-// adapter_shrink_kernel  U[t][r] = alpha[a] * A[a][r] . X[t] (fp32, workspace): one CTA per
-//                        token, its warps over the ranks
-// base                   X W_hat^T in fp32: the dequant GEMV or GEMM
-// adapter_expand_kernel  Y[t][i] = base + B[a][i] . U[t]
+// adapter_shrink_kernel, adapter_shrink_few_kernel   U[t] = alpha[a] A[a] X[t], alpha[a] in fp32
+// adapter_gemm_kernel    the rest, launched behind it without waiting (programmatic launch): it
+//                        needs U only after its own sum over d
+//
+// adapter_gemm_kernel computes a tile of 128 rows of W by N tokens on the 5th-generation tensor
+// cores with W_hat's integers as the A operand IN TENSOR MEMORY: eight warps take the packed
+// words from HBM straight to registers, unpack them there and store them with tcgen05.st;
+// no dequantized operand passes through shared memory or HBM. (Through shared memory the 16-bit
+// operand would be written and read once per tile, four times the 4-bit codes' bytes each way,
+// which bounds a decoding batch before HBM does.) X comes by TMA. Unpacking keeps k in its
+// order: bytes of codes are spread to 16-bit halves by a byte permute, where a small integer c
+// is the bf16 number c * 2^-133 (subnormals, and the first binade for c >= 128), and one
+// bf16 fused multiply-add, c * 2^-133 * 2^127 - zero * 2^-6, leaves (code - zero) * 2^-6
+// exactly; 64 goes into the scale. At 4 bits that is 11 instructions per 8 codes.
+// Every product with a bf16 token is exact in fp32. The sum of a group (or of up to 128 columns
+// of it) leaves tensor memory through the epilogue warps, which add it times the row's scale, a
+// value per lane, in fp32.
+//
+//   warp 0       TMA producer: stages of 64 columns of X
+//   warp 1       MMA issuer
+//   warps 4-19   unpack: four sets of four (a warp per 32 tensor-memory lanes), 128-column
+//                blocks in turn, an A buffer each (two sets with two buffers each: 1100 cycles a
+//                block, a set's own instructions being a chain of about 2000)
+//   warps 20-27  epilogue: per unit N / 2 accumulators a thread
+//
+// Few tokens (N <= 64): a cluster of CTAs splits d for one tile, and the members sum their parts
+// from each other's shared memory, each a share of the rows, adding B[a] U there (one dot
+// product of `rank` values per output). Many tokens (N = 128): a persistent CTA per SM; the
+// adapters are further units of the same product, A = B[a]'s rows, B = U as two bf16 parts
+// (high and low, so the sum keeps 16 bits of U), one unit per run of tokens with one adapter,
+// which the epilogue adds to that run's columns only.
+#include <cudaTypedefs.h>
+
 #include <algorithm>
+#include <type_traits>
 
 #include "elem.cuh"
 
 namespace gptq {
 
-gptq_status dequant_gemv_launch(const uint32_t* qweight, const float* scales, const float* zeros, const int32_t* g_idx,
-                                long long m, long long d, int bits, int group_size, const uint16_t* X, long long T,
-                                long long ldx, float* Y, long long ldy, cudaStream_t s);
-size_t dequant_gemm_workspace_bytes(long long m, long long d);
-gptq_status dequant_gemm_launch(const uint32_t* qweight, const float* scales, const float* zeros, long long m,
-                                long long d, int bits, int group_size, const uint16_t* X, long long T, long long ldx,
-                                void* Y, int y_bf16, long long ldy, void* ws, cudaStream_t s);
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();   // tc_gemm.cu
 
 namespace adp {
 
-constexpr int WARPS = 8;
+// ---------------------------------------------------------------------------------
+// U = alpha A X
+constexpr int SH_WARPS = 8, SH_TOK = 16;
+constexpr int SH_FEW = 64;                               // tokens up to which each reads its adapter by itself
 
-__global__ void __launch_bounds__(WARPS * 32)
-adapter_shrink_kernel(const uint16_t* __restrict__ X, long long ldx, int d, const uint16_t* __restrict__ A,
-                      const float* __restrict__ alpha, long long n_adapters, int rank, const int* __restrict__ ids,
-                      float* __restrict__ U, int* __restrict__ err) {
-  const long long t = blockIdx.x;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int a = ids[t];
-  if (a >= n_adapters && threadIdx.x == 0) report_device_error(err, DEVERR_INDEX);
-  const bool has = a >= 0 && a < n_adapters;
-  for (int r = warp; r < rank; r += WARPS) {
-    float sum = 0.0f;
-    if (has) {
-      const uint16_t* ar = A + ((long long)a * rank + r) * d;
-      for (int c = 8 * lane; c < d; c += 256) {
-        float x[8], w[8];
-        unpack8<BF16>(X + t * ldx + c, x);
-        unpack8<BF16>(ar + c, w);
+struct ShrinkParams {
+  const uint16_t* X;
+  const uint16_t* A;
+  const float* alpha;
+  const int* ids;
+  long long ldx, n_adapters;
+  int T, d, rank, splits;
+  float* part;                 // [splits][T][rank] fp32, or NULL and
+  __nv_bfloat16* hl;           // [T][2 rank], high parts, low parts
+};
+
+// Few tokens: a CTA per (token, slice of d), its warps over the adapter's rows, four 16-byte loads
+// of a row in flight per lane; the token's slice stays in registers.
+constexpr int SL_COLS = 1024;                            // columns of a slice, at most
+__global__ void __launch_bounds__(SH_WARPS * 32) adapter_shrink_few_kernel(ShrinkParams p, int* __restrict__ err) {
+  grid_dep_launch();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = blockIdx.x;
+  const int a = p.ids[t];
+  if (a >= p.n_adapters && threadIdx.x == 0) report_device_error(err, DEVERR_INDEX);
+  const bool has = a >= 0 && a < p.n_adapters;
+  const int n8 = p.d / 8, c0 = (int)((long long)n8 * blockIdx.y / p.splits), c1 = (int)((long long)n8 * (blockIdx.y + 1) / p.splits);
+  float* out = p.part + ((long long)blockIdx.y * p.T + t) * p.rank;
+  if (!has) {
+    for (int r = threadIdx.x; r < p.rank; r += SH_WARPS * 32) out[r] = 0.0f;
+    return;
+  }
+  constexpr int J = SL_COLS / 256;
+  const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+  uint4 x[J];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) sum = fmaf(x[k], w[k], sum);
-      }
+  for (int j = 0; j < J; ++j) {
+    const int c = c0 + lane + 32 * j;
+    x[j] = c < c1 ? reinterpret_cast<const uint4*>(p.X + (long long)t * p.ldx)[c] : z;
+  }
+  const uint4* ar = reinterpret_cast<const uint4*>(p.A + (long long)a * p.rank * p.d);
+  const float al = p.alpha ? p.alpha[a] : 1.0f;
+#pragma unroll 2
+  for (int r = warp; r < p.rank; r += SH_WARPS) {
+    uint4 w[J];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (alpha) sum *= alpha[a];
+    for (int j = 0; j < J; ++j) {
+      const int c = c0 + lane + 32 * j;
+      w[j] = c < c1 ? ar[(long long)r * n8 + c] : z;
     }
-    if (lane == 0) U[t * rank + r] = sum;
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      float u[8], v[8];
+      unpack8<BF16>(&x[j], u);
+      unpack8<BF16>(&w[j], v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s = fmaf(u[k], v[k], s);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) out[r] = s * al;
   }
 }
 
-__global__ void __launch_bounds__(256)
-adapter_expand_kernel(const float* __restrict__ base, long long ldb, const uint16_t* __restrict__ B,
-                      long long n_adapters, int rank, const int* __restrict__ ids, const float* __restrict__ U,
-                      long long T, long long m, void* Y, int y_bf16, long long ldy) {
-  const long long n = T * m;
-  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < n; i += gridDim.x * 256LL) {
-    const long long t = i / m, r = i - t * m;
-    float sum = base[t * ldb + r];
-    const int a = ids ? ids[t] : -1;
-    if (a >= 0 && a < n_adapters) {
-      const uint16_t* b = B + ((long long)a * m + r) * rank;
-      const float* u = U + t * rank;
-      for (int c = 0; c < rank; c += 8) {
-        float w[8];
-        unpack8<BF16>(b + c, w);
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Many tokens: a CTA per 16 tokens, its warps over d; for each adapter among the tokens NT groups
+// of eight of its rows at a time on mma.sync, so neighbours that share an adapter share the
+// reads of its rows. A batch of UN 32-column blocks is loaded before the first is multiplied.
+template <int NT>
+__global__ void __launch_bounds__(SH_WARPS * 32) adapter_shrink_kernel(ShrinkParams p, int* __restrict__ err) {
+  constexpr int UN = 4;
+  __shared__ float red[SH_WARPS][SH_TOK][8 * NT + 1];
+  grid_dep_launch();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int t0 = blockIdx.x * SH_TOK;
+  int id = -1;
+  if (lane < SH_TOK && t0 + lane < p.T) {
+    id = p.ids[t0 + lane];
+    if (id >= p.n_adapters) {
+      report_device_error(err, DEVERR_INDEX);
+      id = -1;
+    }
+  }
+  const int ida = __shfl_sync(0xffffffffu, id, g), idb = __shfl_sync(0xffffffffu, id, g + 8);
+  // lane (g, t) holds columns 8 t ... 8 t + 7 of a block: two MMAs' k in a fixed order, the
+  // same for both operands. Tokens past the end repeat the last one.
+  const int nb = p.d / 32, b0 = nb * warp / SH_WARPS, b1 = nb * (warp + 1) / SH_WARPS;   // this warp's blocks
+  const uint16_t* xa = p.X + (long long)min(t0 + g, p.T - 1) * p.ldx + 8 * t;
+  const uint16_t* xb = p.X + (long long)min(t0 + g + 8, p.T - 1) * p.ldx + 8 * t;
+  for (int r0 = 0; r0 < p.rank; r0 += 8 * NT) {
+    const int nr = min(8 * NT, p.rank - r0);
+    float acc[NT][4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) sum = fmaf(w[k], u[c + k], sum);
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
+    unsigned todo = __ballot_sync(0xffffffffu, id >= 0);
+    while (todo) {
+      const int a = __shfl_sync(0xffffffffu, id, __ffs(todo) - 1);
+      todo &= ~__ballot_sync(0xffffffffu, id == a);
+      const uint16_t* ap[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)             // rows past the rank repeat the first: their sums are not used
+        ap[n] = p.A + ((long long)a * p.rank + r0 + (8 * n < nr ? 8 * n : 0) + g) * p.d + 8 * t;
+      float c[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[n][i] = 0.0f;
+      for (int b = b0; b < b1; b += UN) {
+        uint4 u[UN], v[UN], w[UN][NT];
+#pragma unroll
+        for (int k = 0; k < UN; ++k) {
+          const int bk = b + k;
+          u[k] = v[k] = make_uint4(0u, 0u, 0u, 0u);
+          if (bk < b1) {
+            u[k] = *reinterpret_cast<const uint4*>(xa + 32 * bk);
+            v[k] = *reinterpret_cast<const uint4*>(xb + 32 * bk);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) w[k][n] = __ldg(reinterpret_cast<const uint4*>(ap[n] + 32 * bk));
+          } else {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) w[k][n] = make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < UN; ++k)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma_bf16(c[n], u[k].x, v[k].x, u[k].y, v[k].y, w[k][n].x, w[k][n].y);
+            mma_bf16(c[n], u[k].z, v[k].z, u[k].w, v[k].w, w[k][n].z, w[k][n].w);
+          }
+      }
+      const float al = p.alpha ? p.alpha[a] : 1.0f;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        if (ida == a) { acc[n][0] = c[n][0] * al; acc[n][1] = c[n][1] * al; }
+        if (idb == a) { acc[n][2] = c[n][2] * al; acc[n][3] = c[n][3] * al; }
       }
     }
-    if (y_bf16) reinterpret_cast<__nv_bfloat16*>(Y)[t * ldy + r] = __float2bfloat16_rn(sum);
-    else reinterpret_cast<float*>(Y)[t * ldy + r] = sum;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      red[warp][g][8 * n + 2 * t] = acc[n][0];
+      red[warp][g][8 * n + 2 * t + 1] = acc[n][1];
+      red[warp][g + 8][8 * n + 2 * t] = acc[n][2];
+      red[warp][g + 8][8 * n + 2 * t + 1] = acc[n][3];
+    }
+    __syncthreads();
+    for (int x = threadIdx.x; x < SH_TOK * nr; x += SH_WARPS * 32) {
+      const int i = x / nr, r = x - i * nr;
+      float s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < SH_WARPS; ++w) s += red[w][i][r];
+      if (t0 + i < p.T && p.part) {
+        p.part[(long long)(t0 + i) * p.rank + r0 + r] = s;
+      } else if (t0 + i < p.T) {
+        const __nv_bfloat16 h = __float2bfloat16_rn(s);
+        p.hl[(long long)(t0 + i) * (2 * p.rank) + r0 + r] = h;
+        p.hl[(long long)(t0 + i) * (2 * p.rank) + p.rank + r0 + r] = __float2bfloat16_rn(s - __bfloat162float(h));
+      }
+    }
+    __syncthreads();
   }
+}
+
+// ---------------------------------------------------------------------------------
+// the packed product
+constexpr int BM = 128, KB = 128, XK = 64;               // rows, columns of an A block, columns of an X stage
+constexpr int NA = 4;                                    // A buffers, one per unpacking set
+constexpr int SETS = 4, UNPACK0 = 4, EPI0 = UNPACK0 + 4 * SETS, NEPI = 8;
+constexpr int THREADS = (EPI0 + NEPI) * 32;              // 896: 72 registers a thread at launch
+// Many tokens: the epilogue's 64 accumulators a thread take registers from the other warps.
+// 128 x 40 + 512 x 56 + 256 x 112 is below 896 x 72, the registers the block has at launch.
+constexpr int REG_ISSUE = 40, REG_UNPACK = 56, REG_EPI = 112;
+
+struct Params {
+  const uint32_t* qweight;
+  const float* scales;
+  const float* zeros;
+  const uint16_t* B;
+  const int* ids;              // NULL: no adapters
+  const float* part;           // few tokens: U's parts [splits][T][rank]
+  void* Y;
+  long long ldy, n_adapters;
+  int m, d, T, gs, G, wpr, unit, rank, splits, y_bf16;
+  uint32_t gs32_mul;           // ceil(2^32 / (gs / 32)), 0 when gs is 32
+  int mt, nt, S;               // row tiles, token tiles, CTAs that split d
+};
+
+template <int N>
+struct Cfg {
+  static constexpr bool MANY = N == 128;
+  static constexpr int STAGES = 6;
+  static constexpr int X_BYTES = N * XK * 2;
+  static constexpr int TMEM_A = 2 * N;                     // columns: two accumulators, then NA A blocks of 64
+  static constexpr uint32_t TMEM_COLS = 512;
+  static constexpr int P_LD = BM + 4;
+  static constexpr int P_BYTES = MANY ? 0 : N * P_LD * 4;  // the tile's sums, token-major, for the cluster
+  static constexpr int SMEM_FIX = STAGES * X_BYTES + 1024 + 256 + P_BYTES;
+};
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+  return d;
+}
+// c * 2^-133 (a bf16 pair of small integers' bits) to (c - zero) * 2^-6; nz is the pair -zero * 2^-6
+__device__ __forceinline__ uint32_t to_int(uint32_t c, uint32_t nz) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(c), "r"(0x7F007F00u), "r"(nz));
+  return d;
+}
+__device__ __forceinline__ uint32_t neg_zero(float z) {
+  return (__float_as_uint(-z * 0.015625f) >> 16) * 0x00010001u;      // an integer below 256: exact in bf16
+}
+
+// 32 codes (BITS words) as 16 bf16 pairs of (code - zero) * 2^-6 in the columns' order.
+template <int BITS>
+__device__ __forceinline__ void unpack32(const uint32_t* w, uint32_t nz, uint32_t (&o)[16]) {
+  if constexpr (BITS == 4) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t e = w[j] & 0x0F0F0F0Fu, d = (w[j] >> 4) & 0x0F0F0F0Fu;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)           // bytes i of both; a selector's top bit repeats a byte's sign bit: 0
+        o[4 * j + i] = to_int(prmt(e, d, (uint32_t)(i | ((8 + i) << 4) | ((4 + i) << 8) | ((12 + i) << 12))), nz);
+    }
+  } else if constexpr (BITS == 8) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      o[2 * j] = to_int(prmt(w[j], 0u, 0x4140u), nz);
+      o[2 * j + 1] = to_int(prmt(w[j], 0u, 0x4342u), nz);
+    }
+  } else if constexpr (BITS == 2) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      uint32_t c[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) c[k] = (w[j] >> (2 * k)) & 0x03030303u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t sel = (uint32_t)(i | ((8 + i) << 4) | ((4 + i) << 8) | ((12 + i) << 12));
+        o[8 * j + 2 * i] = to_int(prmt(c[0], c[1], sel), nz);
+        o[8 * j + 2 * i + 1] = to_int(prmt(c[2], c[3], sel), nz);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int b = 6 * i, k = b >> 5, sh = b & 31;
+      const uint32_t s = k < 2 ? __funnelshift_r(w[k], w[k + 1], sh) : w[2] >> sh;
+      o[i] = to_int((s & 7u) | ((s << 13) & 0x00070000u), nz);
+    }
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void load_words(const uint32_t* p, uint32_t* w) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p + i));
+      w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
+    }
+  } else if constexpr (N == 2) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    w[0] = v.x; w[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = __ldg(p + i);
+  }
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D (tensor memory) += A (tensor memory) B (shared memory), issued by the lane with `leader` set of a
+// converged warp: no branch around it, so its operands stay warp-uniform.
+__device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate, uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit_by(uint64_t* bar, uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t elect_leader() {
+  uint32_t l;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(l));
+  return l;
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t* r) {
+  if constexpr (N == 8) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+  } else {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+  }
+}
+
+__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
+  float v;
+  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
+               : "=f"(v)
+               : "r"(addr), "r"(rank));
+  return v;
+}
+
+// The runs of one adapter among a tile's N tokens (N = 128: four words of boundary bits), the
+// same in every warp: next() gives a run's columns [c0, c1) and its adapter.
+struct Runs {
+  uint32_t starts[4];
+  int ids[4], c, n;
+  __device__ __forceinline__ void init(const Params& p, int t0, int lane) {
+    n = min(128, p.T - t0);
+    c = 0;
+    int prev = -2;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int t = 32 * k + lane;
+      int id = -1;
+      if (t < n) {
+        id = p.ids[t0 + t];
+        if (id < 0 || id >= p.n_adapters) id = -1;
+      }
+      ids[k] = id;
+      int before = __shfl_up_sync(0xffffffffu, id, 1);
+      if (lane == 0) before = prev;
+      starts[k] = __ballot_sync(0xffffffffu, id != before || (k == 0 && lane == 0));
+      prev = __shfl_sync(0xffffffffu, id, 31);
+    }
+  }
+  __device__ __forceinline__ bool next(int& c0, int& c1, int& id) {
+    while (c < n) {
+      c0 = c;
+      int e = 128;                                         // the next start after c
+#pragma unroll
+      for (int k = 3; k >= 0; --k) {
+        const uint32_t after = 32 * k > c ? starts[k] : (32 * k + 31 > c ? starts[k] & (0xFFFFFFFEu << (c - 32 * k)) : 0u);
+        if (after) e = 32 * k + __ffs(after) - 1;
+      }
+      c1 = min(e, n);
+      c = c1;
+      int v = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int x = __shfl_sync(0xffffffffu, ids[k], c0 & 31);
+        if ((c0 >> 5) == k) v = x;
+      }
+      id = v;
+      if (id >= 0) return true;
+    }
+    return false;
+  }
+};
+
+template <int BITS, int N>
+__global__ void __launch_bounds__(THREADS, 1)
+adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_u, Params p,
+                    int* __restrict__ err) {
+  using C = Cfg<N>;
+  constexpr bool MANY = C::MANY;
+  constexpr int STAGES = C::STAGES, NC = N / 2;            // columns of an epilogue thread
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  uint64_t* x_full = reinterpret_cast<uint64_t*>(smem + STAGES * C::X_BYTES);
+  uint64_t* x_empty = x_full + STAGES;
+  uint64_t* a_full = x_empty + STAGES;
+  uint64_t* a_empty = a_full + NA;
+  uint64_t* d_full = a_empty + NA;
+  uint64_t* d_empty = d_full + 2;
+  uint64_t* drain = d_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* P = reinterpret_cast<float*>(smem + STAGES * C::X_BYTES + 256);
+  float* Us = P + C::P_BYTES / 4;                          // few tokens: U, N x rank
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&x_full[s], 1);
+      mbar_init(&x_empty[s], 1);
+    }
+    for (int b = 0; b < NA; ++b) {
+      mbar_init(&a_full[b], 4);
+      mbar_init(&a_empty[b], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&d_full[b], 1);
+      mbar_init(&d_empty[b], NEPI);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&map_x);
+    if (MANY) prefetch_tmap(&map_u);
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, C::TMEM_COLS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_dep_launch();
+
+  const int S = MANY ? 1 : p.S, rank_c = MANY ? 0 : (int)(blockIdx.x % S);
+  const int ntiles = p.mt * p.nt, step = MANY ? (int)gridDim.x : ntiles;       // few tokens: one tile per cluster
+  const int tile0 = MANY ? (int)blockIdx.x : (int)(blockIdx.x / S);
+  const int nblk = (p.d + KB - 1) / KB, blk0 = (int)((long long)nblk * rank_c / S), blk1 = (int)((long long)nblk * (rank_c + 1) / S);
+  const int k_lo = blk0 * KB, k_hi = min(p.d, blk1 * KB);
+  const int ad_units = (2 * p.rank + KB - 1) / KB;         // A blocks of one adapter
+  constexpr uint32_t IDESC = umma_idesc(/*bf16*/ 1, false, false, BM, N);
+
+  if (warp < UNPACK0) {
+    if (MANY) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_ISSUE));
+    if (warp == 0) {
+    // ---------------- TMA producer ----------------
+    uint32_t stage = 0, phase = 0, armed = 0, last_phase = 0;
+    bool ok = true, waited = false;
+    auto push = [&](const CUtensorMap* map, int k, int t) {
+      if (!ok) return;
+      if (!mbar_wait_bounded(&x_empty[stage], phase ^ 1u, abort_flag)) { ok = false; return; }
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&x_full[stage], C::X_BYTES);
+        tma_load_2d(smem + stage * C::X_BYTES, map, &x_full[stage], k, t);
+      }
+      armed |= 1u << stage;
+      last_phase = (last_phase & ~(1u << stage)) | (phase << stage);
+      if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+    };
+    for (int tile = tile0; ok && tile < ntiles; tile += step) {
+      const int t0 = (tile / p.mt) * N;
+      for (int k = k_lo; k < k_hi; k += XK) push(&map_x, k, t0);
+      if (MANY && p.ids) {
+        if (!waited) { grid_dep_wait(); waited = true; }   // U is the launch before's
+        Runs runs;
+        runs.init(p, t0, lane);
+        int c0, c1, id;
+        while (ok && runs.next(c0, c1, id))
+          for (int k = 0; k < 2 * p.rank; k += XK) push(&map_u, k, t0);
+      }
+    }
+    if (!ok) { *abort_flag = 1; if (lane == 0) report_device_error(err, DEVERR_TIMEOUT); }
+    for (int s = 0; s < STAGES; ++s)
+      if (armed & (1u << s)) mbar_wait_bounded(&x_full[s], (last_phase >> s) & 1u, nullptr);
+  } else if (warp == 1) {
+    // ---------------- MMA issuer ----------------
+    uint32_t stage = 0, phase = 0, ab = 0, unit_no = 0;
+    bool ok = true, issued = false;
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t leader = elect_leader();
+    // Columns [0, len) of one A operand in units of `unit`; an A buffer holds KB columns, an X
+    // stage XK, and both begin with the operand. The warp waits and fences once per A block
+    // where it can (a unit of KB columns): a tcgen05 fence between the MMAs of one sum lets each
+    // wait for the one before (measured: 500 cycles an MMA).
+    auto take_x = [&]() -> bool {
+      if (mbar_wait_bounded(&x_full[stage], phase, abort_flag)) return true;
+      ok = false;
+      return false;
+    };
+    auto give_x = [&]() {
+      umma_commit_by(&x_empty[stage], leader);
+      if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+    };
+    auto b_desc = [&](int k) { return umma_sdesc_sw128(sbase + stage * C::X_BYTES + k * 2, 16, 1024); };
+    auto stream = [&](int len, int unit) {
+      for (int k0 = 0; ok && k0 < len; k0 += KB) {
+        const int kn = min(KB, len - k0);
+        if (!mbar_wait_poll(&a_full[ab % NA], (ab / NA) & 1u, abort_flag)) { ok = false; break; }
+        const uint32_t at = tmem + C::TMEM_A + (ab % NA) * (KB / 2);
+        issued = true;
+        if (unit == KB && kn == KB) {
+          const uint32_t buf = unit_no & 1u, dt = tmem + buf * N;
+          if (!mbar_wait_poll(&d_empty[buf], ((unit_no >> 1) & 1u) ^ 1u, abort_flag)) { ok = false; break; }
+          if (!take_x()) break;
+          tc_fence_after();
+          const uint64_t b0 = b_desc(0);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) umma_f16_ta(dt, at + 8 * kk, b0 + 2 * kk, IDESC, kk != 0, leader);
+          give_x();
+          if (!take_x()) break;
+          const uint64_t b1 = b_desc(0);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) umma_f16_ta(dt, at + 32 + 8 * kk, b1 + 2 * kk, IDESC, 1u, leader);
+          give_x();
+          umma_commit_by(&d_full[buf], leader);
+          ++unit_no;
+        } else {
+          int kin = 0;
+          for (int k = 0; k < kn; k += 16) {
+            const uint32_t buf = unit_no & 1u;
+            if ((k & (XK - 1)) == 0 && !take_x()) break;
+            if (kin == 0) {
+              if (!mbar_wait_poll(&d_empty[buf], ((unit_no >> 1) & 1u) ^ 1u, abort_flag)) { ok = false; break; }
+              tc_fence_after();
+            }
+            umma_f16_ta(tmem + buf * N, at + k / 2, b_desc(k & (XK - 1)), IDESC, kin != 0, leader);
+            kin += 16;
+            if (((k + 16) & (XK - 1)) == 0 || k + 16 >= kn) give_x();
+            if (kin == unit || k + 16 >= kn) {
+              umma_commit_by(&d_full[buf], leader);
+              ++unit_no;
+              kin = 0;
+            }
+          }
+          if (!ok) break;
+        }
+        umma_commit_by(&a_empty[ab % NA], leader);
+        ++ab;
+      }
+    };
+    for (int tile = tile0; ok && tile < ntiles; tile += step) {
+      stream(k_hi - k_lo, p.unit);
+      if (MANY && p.ids) {
+        Runs runs;
+        runs.init(p, (tile / p.mt) * N, lane);
+        int c0, c1, id;
+        while (ok && runs.next(c0, c1, id)) stream(2 * p.rank, KB);
+      }
+    }
+    if (!ok) { *abort_flag = 1; if (lane == 0) report_device_error(err, DEVERR_TIMEOUT); }
+    if (issued) {
+      umma_commit_by(drain, leader);
+      mbar_wait_bounded(drain, 0, nullptr);
+    }
+    }
+  } else if (warp < EPI0) {
+    // ---------------- unpack: words -> registers -> tensor memory ----------------
+    if (MANY) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_UNPACK));
+    constexpr int W32 = BITS, WB = 4 * W32;                // words of 32 columns, of a block
+    const int set = (warp - UNPACK0) >> 2, q = warp & 3, row_l = 32 * q + lane;
+    const uint32_t ta0 = tmem + ((uint32_t)(32 * q) << 16) + C::TMEM_A;
+    const bool one_zero = p.gs % KB == 0;
+    auto group_of = [&](int c32) -> int {                  // the group of columns 32 c32 ...
+      return p.gs32_mul ? (int)__umulhi((uint32_t)c32, p.gs32_mul) : c32;
+    };
+    uint32_t ab = 0;                                       // A blocks so far, all sets'
+    bool ok = true;
+    uint32_t ta = 0;
+    auto ready = [&]() -> bool {                           // the block's buffer is free
+      ta = ta0 + (ab % NA) * (KB / 2);
+      if (!mbar_wait_bounded(&a_empty[ab % NA], ((ab / NA) & 1u) ^ 1u, abort_flag)) {
+        *abort_flag = 1;
+        if (lane == 0) report_device_error(err, DEVERR_TIMEOUT);
+        return false;
+      }
+      tc_fence_after();
+      return true;
+    };
+    auto publish = [&]() {
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&a_full[ab % NA]);
+    };
+    for (int tile = tile0; ok && tile < ntiles; tile += step) {
+      const int row = (tile % p.mt) * BM + row_l;
+      const bool live = row < p.m;
+      const float* zr = p.zeros + (long long)(live ? row : 0) * p.G;
+      // this set's blocks: first, first + SETS, ... (ab counts every set's, to the tile's end)
+      const uint32_t ab0 = ab;
+      const int first = blk0 + (int)((set - ab0) % SETS);
+      const uint32_t* wp = p.qweight + (long long)(live ? row : 0) * p.wpr + (long long)first * WB;
+      uint32_t w[WB];
+      float z = 0.0f;
+      auto fetch = [&](int b) {                            // block b's words and (one per block) zero
+        if (b >= blk1) return;
+        if ((b + 1) * KB <= p.d) {
+          if constexpr (BITS == 3) load_words<WB>(wp, w);
+          else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) load_words<W32>(wp + c * W32, w + c * W32);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (b * KB + 32 * c < p.d) load_words<W32>(wp + c * W32, w + c * W32);
+        }
+        wp += SETS * WB;
+        if (one_zero) z = __ldg(zr + group_of(4 * b));
+      };
+      fetch(first);
+      for (int b = first; b < blk1; b += SETS) {
+        ab = ab0 + (uint32_t)(b - blk0);
+        if (!ready()) { ok = false; break; }
+        const uint32_t nzb = neg_zero(z);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (b * KB + 32 * c < p.d) {
+            const uint32_t nz = one_zero ? nzb : neg_zero(__ldg(zr + group_of(4 * b + c)));
+            uint32_t o[16];
+            unpack32<BITS>(w + c * W32, nz, o);
+            tmem_st16(ta + 16 * c, o);
+          }
+        }
+        fetch(b + SETS);                                   // in flight while the other sets' blocks are multiplied
+        publish();
+      }
+      ab = ab0 + (uint32_t)(blk1 - blk0);
+      if (MANY && p.ids) {
+        // the adapters' rows as further A blocks: column k is B[a][row][k mod rank]
+        Runs runs;
+        runs.init(p, (tile / p.mt) * N, lane);
+        int c0, c1, id;
+        while (ok && runs.next(c0, c1, id)) {
+          const uint32_t* br = reinterpret_cast<const uint32_t*>(p.B + ((long long)id * p.m + (live ? row : 0)) * p.rank);
+          for (int u = 0; u < ad_units; ++u, ++ab) {
+            if ((int)(ab % SETS) != set) continue;
+            if (!ready()) { ok = false; break; }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              if (u * KB + 32 * c < 2 * p.rank) {
+                uint32_t o[16];
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) {          // eight columns, one 16-byte load (rank % 8 == 0)
+                  const int k = u * KB + 32 * c + 2 * i;
+                  const uint4 v = k < 2 * p.rank ? __ldg(reinterpret_cast<const uint4*>(br + (k >= p.rank ? k - p.rank : k) / 2))
+                                                 : make_uint4(0u, 0u, 0u, 0u);
+                  o[i] = v.x; o[i + 1] = v.y; o[i + 2] = v.z; o[i + 3] = v.w;
+                }
+                tmem_st16(ta + 16 * c, o);
+              }
+            }
+            publish();
+          }
+        }
+      }
+    }
+  } else {
+    // ---------------- epilogue ----------------
+    if (MANY) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_EPI));
+    const int q = warp & 3, h = (warp - EPI0) >> 2;
+    const uint32_t td = tmem + ((uint32_t)(32 * q) << 16) + h * NC;
+    uint32_t unit_no = 0;
+    bool ok = true;
+    constexpr int LD = NC < 16 ? 8 : 16;
+    for (int tile = tile0; ok && tile < ntiles; tile += step) {
+      const int row = (tile % p.mt) * BM + 32 * q + lane, t0 = (tile / p.mt) * N;
+      const float* sr = p.scales + (long long)(row < p.m ? row : 0) * p.G;
+      float run[NC];
+#pragma unroll
+      for (int c = 0; c < NC; ++c) run[c] = 0.0f;
+      auto wait = [&]() -> bool {
+        if (!mbar_wait_bounded(&d_full[unit_no & 1], (unit_no >> 1) & 1u, abort_flag)) {
+          *abort_flag = 1;
+          if (lane == 0) report_device_error(err, DEVERR_TIMEOUT);
+          return false;
+        }
+        tc_fence_after();
+        return true;
+      };
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&d_empty[unit_no & 1]);
+        ++unit_no;
+      };
+      int grp = k_lo / p.gs, kg = k_lo - grp * p.gs;
+      float sn = k_lo < k_hi ? __ldg(sr + grp) : 0.0f;
+      for (int k = k_lo; k < k_hi; k += p.unit) {
+        const float s = sn * 64.0f;
+        kg += p.unit;
+        if (kg >= p.gs) {
+          kg = 0;
+          ++grp;
+          if (k + p.unit < k_hi) sn = __ldg(sr + grp);
+        }
+        if (!wait()) { ok = false; break; }
+#pragma unroll
+        for (int c = 0; c < NC; c += LD) {
+          uint32_t a[LD];
+          tmem_ld<LD>(td + (unit_no & 1u) * N + c, a);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < LD; ++i) run[c + i] = fmaf(__uint_as_float(a[i]), s, run[c + i]);
+        }
+        release();
+      }
+      if (MANY) {
+        if (p.ids) {
+          Runs runs;
+          runs.init(p, t0, lane);
+          int c0, c1, id;
+          while (ok && runs.next(c0, c1, id)) {
+            for (int u = 0; u < ad_units; ++u) {
+              if (!wait()) { ok = false; break; }
+#pragma unroll
+              for (int c = 0; c < NC; c += LD) {
+                uint32_t a[LD];
+                tmem_ld<LD>(td + (unit_no & 1u) * N + c, a);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < LD; ++i)
+                  if (h * NC + c + i >= c0 && h * NC + c + i < c1) run[c + i] += __uint_as_float(a[i]);
+              }
+              release();
+            }
+          }
+        }
+        if (ok && row < p.m) {
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const int t = t0 + h * NC + c;
+            if (t < p.T) {
+              if (p.y_bf16) reinterpret_cast<__nv_bfloat16*>(p.Y)[(long long)t * p.ldy + row] = __float2bfloat16_rn(run[c]);
+              else reinterpret_cast<float*>(p.Y)[(long long)t * p.ldy + row] = run[c];
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) P[(h * NC + c) * C::P_LD + 32 * q + lane] = run[c];
+      }
+    }
+  }
+
+  if (!MANY) {
+    // ---- few tokens: U, then the cluster's parts, each member its share of the rows
+    const int t0 = (tile0 / p.mt) * N, r0 = (tile0 % p.mt) * BM;
+    grid_dep_wait();
+    if (p.ids) {
+      for (int x = threadIdx.x; x < N * p.rank; x += THREADS) {
+        const int c = x / p.rank;
+        float s = 0.0f;
+        if (t0 + c < p.T)
+          for (int k = 0; k < p.splits; ++k) s += p.part[((long long)k * p.T + t0) * p.rank + x];
+        Us[x] = s;
+      }
+    }
+    __syncthreads();
+    cluster_sync();
+    const int rows = BM / S, nout = rows * min(N, p.T - t0);
+    for (int x = threadIdx.x; x < nout; x += THREADS) {
+      const int c = x / rows, rl = rank_c * rows + (x - c * rows), row = r0 + rl;
+      if (row >= p.m) continue;
+      float s = 0.0f;
+      for (int k = 0; k < S; ++k) s += ld_cluster(smem_u32(&P[c * C::P_LD + rl]), (uint32_t)k);
+      const int id = p.ids ? p.ids[t0 + c] : -1;
+      if (id >= 0 && id < p.n_adapters) {
+        const uint16_t* b = p.B + ((long long)id * p.m + row) * p.rank;
+        const float* u = Us + c * p.rank;
+        for (int r = 0; r < p.rank; r += 8) {
+          float v[8];
+          unpack8<BF16>(b + r, v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s = fmaf(v[i], u[r + i], s);
+        }
+      }
+      if (p.y_bf16) reinterpret_cast<__nv_bfloat16*>(p.Y)[(long long)(t0 + c) * p.ldy + row] = __float2bfloat16_rn(s);
+      else reinterpret_cast<float*>(p.Y)[(long long)(t0 + c) * p.ldy + row] = s;
+    }
+    cluster_sync();                                        // nobody leaves while its sums are read
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+bool make_map(CUtensorMap* m, const void* base, long long inner, long long outer, long long ld, int rows) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
+  cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+  cuuint32_t box[2] = {XK, (cuuint32_t)rows};
+  cuuint32_t es[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
+// How a call of T tokens is cut. Tiles of 128 tokens where they give at least half the SMs one
+// each; else tiles of up to 64 tokens with clusters that split d so that about every SM has a CTA.
+struct Plan {
+  int N, mt, nt, S, splits;
+};
+Plan plan_of(long long m, long long d, long long T) {
+  Plan p;
+  const int sms = sm_count();
+  p.mt = (int)((m + BM - 1) / BM);
+  const long long tiles = (long long)p.mt * ((T + 127) / 128);
+  p.S = 1;
+  p.splits = 1;
+  if (T > 64 && 2 * tiles >= sms) {
+    p.N = 128;
+  } else {
+    p.N = T <= 16 ? 16 : (T <= 32 ? 32 : 64);
+    const long long few = (long long)p.mt * ((T + p.N - 1) / p.N);
+    while (p.S < 8 && 2 * p.S * few <= sms && 2 * p.S * KB <= d) p.S *= 2;
+    // slices of d for U: at most SL_COLS columns, at least 256 where there are few tokens
+    if (T <= SH_FEW) {
+      p.splits = (int)((d + SL_COLS - 1) / SL_COLS);
+      while (p.splits < 16 && p.splits * 512 <= d && T * p.splits < 2 * sms) p.splits *= 2;
+    }
+  }
+  p.nt = (int)((T + p.N - 1) / p.N);
+  return p;
+}
+
+template <int BITS, int N>
+gptq_status launch(const CUtensorMap& mx, const CUtensorMap& mu, const Params& p, bool pdl, cudaStream_t s) {
+  using C = Cfg<N>;
+  const size_t smem = C::SMEM_FIX + (C::MANY ? 0 : (size_t)N * p.rank * 4);
+  static bool attr_done = false;
+  if (!attr_done) {
+    const size_t most = C::SMEM_FIX + (C::MANY ? 0 : (size_t)N * 128 * 4);
+    if (cudaFuncSetAttribute(adapter_gemm_kernel<BITS, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess)
+      return set_error(GPTQ_ERR_CUDA, "cudaFuncSetAttribute(adapter_gemm_kernel) failed");
+    attr_done = true;
+  }
+  const long long tiles = (long long)p.mt * p.nt;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(C::MANY ? std::min<long long>(tiles, sm_count()) : tiles * p.S));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  int na = 0;
+  attr[na].id = cudaLaunchAttributeClusterDimension;
+  attr[na].val.clusterDim.x = (unsigned)(C::MANY ? 1 : p.S);
+  attr[na].val.clusterDim.y = 1;
+  attr[na].val.clusterDim.z = 1;
+  ++na;
+  if (pdl) {
+    attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[na].val.programmaticStreamSerializationAllowed = 1;
+    ++na;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = na;
+  cudaLaunchKernelEx(&cfg, adapter_gemm_kernel<BITS, N>, mx, mu, p, device_error_word());
+  count_launch();
+  return check_launch("adapter_gemm_kernel");
+}
+
+template <int BITS>
+gptq_status launch_n(int N, const CUtensorMap& mx, const CUtensorMap& mu, const Params& p, bool pdl, cudaStream_t s) {
+  switch (N) {
+    case 16: return launch<BITS, 16>(mx, mu, p, pdl, s);
+    case 32: return launch<BITS, 32>(mx, mu, p, pdl, s);
+    case 64: return launch<BITS, 64>(mx, mu, p, pdl, s);
+    default: return launch<BITS, 128>(mx, mu, p, pdl, s);
+  }
+}
+
 }  // namespace adp
 
-// Workspace: U (T x rank fp32), the base product (T x m fp32), the dequant GEMM's operand.
+// Workspace: U, as parts in fp32 or as two bf16 parts.
 size_t adapter_workspace_bytes(long long m, long long d, int bits, int group_size, long long T, int rank) {
   using namespace adp;
   (void)bits;
   (void)group_size;
-  return round256(4 * (size_t)T * rank) + round256(4 * (size_t)T * m) + dequant_gemm_workspace_bytes(m, d) + 256;
+  const Plan p = plan_of(m, d, std::max(1LL, T));
+  return round256(4 * (size_t)std::max(1LL, T) * rank * p.splits);
 }
 
 gptq_status adapter_linear_launch(const uint32_t* qweight, const float* scales, const float* zeros, long long m,
@@ -94,23 +945,46 @@ gptq_status adapter_linear_launch(const uint32_t* qweight, const float* scales, 
                                   int rank, const int* ids, void* Y, int y_dtype, long long ldy, void* ws,
                                   cudaStream_t s) {
   using namespace adp;
-  float* U = reinterpret_cast<float*>(ws);
-  float* base = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(ws) + round256(4 * (size_t)T * rank));
-  void* gws = reinterpret_cast<uint8_t*>(base) + round256(4 * (size_t)T * m);
+  const Plan pl = plan_of(m, d, T);
+  if ((long long)pl.mt * pl.nt * pl.S > 0x7FFFFFFF) return set_error(GPTQ_ERR_INVALID_ARG, "too many output tiles");
   if (ids) {
-    adapter_shrink_kernel<<<(unsigned)T, WARPS * 32, 0, s>>>(X, ldx, (int)d, A, alpha, n_adapters, rank, ids, U,
-                                                            device_error_word());
+    ShrinkParams q{};
+    q.X = X; q.A = A; q.alpha = alpha; q.ids = ids; q.ldx = ldx; q.n_adapters = n_adapters;
+    q.T = (int)T; q.d = (int)d; q.rank = rank; q.splits = pl.splits;
+    if (pl.N == 128) q.hl = reinterpret_cast<__nv_bfloat16*>(ws);
+    else q.part = reinterpret_cast<float*>(ws);
+    const unsigned grid = (unsigned)((T + SH_TOK - 1) / SH_TOK);
+    if (T <= SH_FEW) adapter_shrink_few_kernel<<<dim3((unsigned)T, pl.splits), SH_WARPS * 32, 0, s>>>(q, device_error_word());
+    else if (rank == 8) adapter_shrink_kernel<1><<<grid, SH_WARPS * 32, 0, s>>>(q, device_error_word());
+    else if (rank == 16) adapter_shrink_kernel<2><<<grid, SH_WARPS * 32, 0, s>>>(q, device_error_word());
+    else adapter_shrink_kernel<4><<<grid, SH_WARPS * 32, 0, s>>>(q, device_error_word());
     count_launch();
     if (gptq_status st = check_launch("adapter_shrink_kernel")) return st;
   }
-  gptq_status st = T <= 32 ? dequant_gemv_launch(qweight, scales, zeros, nullptr, m, d, bits, group_size, X, T, ldx, base, m, s)
-                           : dequant_gemm_launch(qweight, scales, zeros, m, d, bits, group_size, X, T, ldx, base, 0, m, gws, s);
-  if (st) return st;
-  const long long grid = std::min<long long>((T * m + 255) / 256, 16LL * sm_count());
-  adapter_expand_kernel<<<(unsigned)grid, 256, 0, s>>>(base, m, B, n_adapters, rank, ids, U, T, m, Y,
-                                                       y_dtype == GPTQ_BF16, ldy);
-  count_launch();
-  return check_launch("adapter_expand_kernel");
+  Params p{};
+  p.qweight = qweight; p.scales = scales; p.zeros = zeros; p.B = B; p.ids = ids; p.part = reinterpret_cast<const float*>(ws);
+  p.Y = Y; p.ldy = ldy; p.n_adapters = n_adapters;
+  p.m = (int)m; p.d = (int)d; p.T = (int)T;
+  p.gs = group_size < 0 ? (int)d : group_size;
+  p.G = (int)(d / p.gs);
+  p.wpr = (int)(d / 32 * bits);
+  const unsigned gs32 = (unsigned)p.gs / 32;
+  p.gs32_mul = gs32 == 1 ? 0u : (uint32_t)((0x100000000ULL + gs32 - 1) / gs32);
+  p.unit = p.gs % 128 == 0 ? 128 : (p.gs % 64 == 0 ? 64 : 32);
+  p.rank = rank; p.splits = pl.splits; p.y_bf16 = y_dtype == GPTQ_BF16;
+  p.mt = pl.mt; p.nt = pl.nt; p.S = pl.S;
+  CUtensorMap mx, mu;
+  if (!make_map(&mx, X, d, T, ldx, pl.N)) return set_error(GPTQ_ERR_CUDA, "cuTensorMapEncodeTiled failed for X");
+  mu = mx;
+  if (ids && pl.N == 128 && !make_map(&mu, ws, 2 * rank, T, 2 * rank, pl.N))
+    return set_error(GPTQ_ERR_CUDA, "cuTensorMapEncodeTiled failed for the adapters' inner product");
+  const bool pdl = ids != nullptr;
+  switch (bits) {
+    case 2: return launch_n<2>(pl.N, mx, mu, p, pdl, s);
+    case 3: return launch_n<3>(pl.N, mx, mu, p, pdl, s);
+    case 4: return launch_n<4>(pl.N, mx, mu, p, pdl, s);
+    default: return launch_n<8>(pl.N, mx, mu, p, pdl, s);
+  }
 }
 
 }  // namespace gptq

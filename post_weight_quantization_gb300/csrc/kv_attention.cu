@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, NT>::OCC) kv_split_kernel(Para
   };
   auto issue = [&](uint32_t u, long long src) {
     const uint32_t st = u % NS;
-    if (!mbar_wait_bounded(&empty[st], (u / NS & 1u) ^ 1u, nullptr)) {
+    if (!mbar_wait_poll(&empty[st], (u / NS & 1u) ^ 1u, nullptr)) {
       if (lane == 0) report_device_error(err, DEVERR_TIMEOUT);
       dead = true;
       return;
