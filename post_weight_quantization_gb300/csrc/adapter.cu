@@ -21,11 +21,12 @@
 // of it) leaves tensor memory through the epilogue warps, which add it times the row's scale, a
 // value per lane, in fp32.
 //
-//   warp 0       TMA producer: stages of 64 columns of X
+//   warp 0       TMA producer of X, 128 columns a slot
 //   warp 1       MMA issuer
+//   warp 2       TMA producer of the packed codes (a lane reading its own row from global memory
+//                touches a cache line per 16 bytes: 32 per load, which paced the unpacking)
 //   warps 4-19   unpack: four sets of four (a warp per 32 tensor-memory lanes), 128-column
-//                blocks in turn, an A buffer each (two sets with two buffers each: 1100 cycles a
-//                block, a set's own instructions being a chain of about 2000)
+//                blocks in turn, an A buffer each
 //   warps 20-27  epilogue: per unit N / 2 accumulators a thread
 //
 // Few tokens (N <= 64): a cluster of CTAs splits d for one tile, and the members sum their parts
@@ -220,8 +221,8 @@ __global__ void __launch_bounds__(SH_WARPS * 32) adapter_shrink_kernel(ShrinkPar
 
 // ---------------------------------------------------------------------------------
 // the packed product
-constexpr int BM = 128, KB = 128, XK = 64;               // rows, columns of an A block, columns of an X stage
-constexpr int NA = 4;                                    // A buffers, one per unpacking set
+constexpr int BM = 128, KB = 128, XK = 64;               // rows, columns of a block, columns of one box of X
+constexpr int SLOTS = 4;                                 // blocks in the ring: an A buffer, X, and packed codes each
 constexpr int SETS = 4, UNPACK0 = 4, EPI0 = UNPACK0 + 4 * SETS, NEPI = 8;
 constexpr int THREADS = (EPI0 + NEPI) * 32;              // 896: 72 registers a thread at launch
 // Many tokens: the epilogue's 64 accumulators a thread take registers from the other warps.
@@ -239,19 +240,21 @@ struct Params {
   long long ldy, n_adapters;
   int m, d, T, gs, G, wpr, unit, rank, splits, y_bf16;
   uint32_t gs32_mul;           // ceil(2^32 / (gs / 32)), 0 when gs is 32
+  int codes_tma;               // the packed rows meet TMA's 16-byte rules: codes come through shared memory
   int mt, nt, S;               // row tiles, token tiles, CTAs that split d
 };
 
-template <int N>
+template <int BITS, int N>
 struct Cfg {
   static constexpr bool MANY = N == 128;
-  static constexpr int STAGES = 6;
-  static constexpr int X_BYTES = N * XK * 2;
-  static constexpr int TMEM_A = 2 * N;                     // columns: two accumulators, then NA A blocks of 64
+  static constexpr int ROW_BYTES = 16 * BITS;              // packed codes of a row in one block
+  static constexpr int C_BYTES = (BM * ROW_BYTES + 1023) / 1024 * 1024;
+  static constexpr int X_BOX = N * XK * 2, X_BYTES = 2 * X_BOX;
+  static constexpr int TMEM_A = 2 * N;                     // columns: two accumulators, then SLOTS A blocks of 64
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr int P_LD = BM + 4;
   static constexpr int P_BYTES = MANY ? 0 : N * P_LD * 4;  // the tile's sums, token-major, for the cluster
-  static constexpr int SMEM_FIX = STAGES * X_BYTES + 1024 + 256 + P_BYTES;
+  static constexpr int SMEM_FIX = SLOTS * (X_BYTES + C_BYTES) + 1024 + 256 + P_BYTES;
 };
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
@@ -324,6 +327,16 @@ __device__ __forceinline__ void load_words(const uint32_t* p, uint32_t* w) {
 #pragma unroll
     for (int i = 0; i < N; ++i) w[i] = __ldg(p + i);
   }
+}
+
+// 16 bytes (piece i) of row r from a stage of packed codes. Rows are swizzled as their length asks,
+// so that eight lanes reading eight rows meet no bank twice (3 bits: 48-byte rows need none).
+template <int BITS>
+__device__ __forceinline__ void lds_piece(uint32_t stage, int r, int i, uint32_t* w) {
+  const int at = BITS == 8 ? i ^ (r & 7) : BITS == 4 ? i ^ ((r >> 1) & 3) : BITS == 2 ? i ^ ((r >> 2) & 1) : i;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+               : "r"(stage + r * (16 * BITS) + at * 16));
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -435,35 +448,37 @@ struct Runs {
 
 template <int BITS, int N>
 __global__ void __launch_bounds__(THREADS, 1)
-adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_u, Params p,
+adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_u,
+                    const __grid_constant__ CUtensorMap map_c, Params p,
                     int* __restrict__ err) {
-  using C = Cfg<N>;
+  using C = Cfg<BITS, N>;
   constexpr bool MANY = C::MANY;
-  constexpr int STAGES = C::STAGES, NC = N / 2;            // columns of an epilogue thread
+  constexpr int NC = N / 2;                                // columns of an epilogue thread
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-  uint64_t* x_full = reinterpret_cast<uint64_t*>(smem + STAGES * C::X_BYTES);
-  uint64_t* x_empty = x_full + STAGES;
-  uint64_t* a_full = x_empty + STAGES;
-  uint64_t* a_empty = a_full + NA;
-  uint64_t* d_full = a_empty + NA;
+  uint8_t* codes = smem + SLOTS * C::X_BYTES;
+  // full[i]: slot i's A block is in tensor memory (four warps arrive) and its X in shared memory
+  // (the producer arrives, TMA completes); empty[i]: its MMAs are done. c_*: the packed codes.
+  uint64_t* full = reinterpret_cast<uint64_t*>(codes + SLOTS * C::C_BYTES);
+  uint64_t* empty = full + SLOTS;
+  uint64_t* c_full = empty + SLOTS;
+  uint64_t* c_empty = c_full + SLOTS;
+  uint64_t* d_full = c_empty + SLOTS;
   uint64_t* d_empty = d_full + 2;
   uint64_t* drain = d_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  float* P = reinterpret_cast<float*>(smem + STAGES * C::X_BYTES + 256);
+  float* P = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(full) + 256);
   float* Us = P + C::P_BYTES / 4;                          // few tokens: U, N x rank
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&x_full[s], 1);
-      mbar_init(&x_empty[s], 1);
-    }
-    for (int b = 0; b < NA; ++b) {
-      mbar_init(&a_full[b], 4);
-      mbar_init(&a_empty[b], 1);
+    for (int b = 0; b < SLOTS; ++b) {
+      mbar_init(&full[b], 5);
+      mbar_init(&empty[b], 1);
+      mbar_init(&c_full[b], 1);
+      mbar_init(&c_empty[b], 4);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&d_full[b], 1);
@@ -473,6 +488,7 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tmap(&map_x);
+    prefetch_tmap(&map_c);
     if (MANY) prefetch_tmap(&map_u);
   }
   if (warp == 1) tmem_alloc(tmem_slot, C::TMEM_COLS);
@@ -493,99 +509,72 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
   if (warp < UNPACK0) {
     if (MANY) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_ISSUE));
     if (warp == 0) {
-    // ---------------- TMA producer ----------------
-    uint32_t stage = 0, phase = 0, armed = 0, last_phase = 0;
+    // ---------------- TMA producer of X (and of U) ----------------
+    uint32_t ab = 0;                                       // blocks so far
     bool ok = true, waited = false;
-    auto push = [&](const CUtensorMap* map, int k, int t) {
-      if (!ok) return;
-      if (!mbar_wait_bounded(&x_empty[stage], phase ^ 1u, abort_flag)) { ok = false; return; }
+    // a block of `cols` columns from k on: one box, or two
+    auto push = [&](const CUtensorMap* map, int k, int cols, int t) {
+      const uint32_t i = ab % SLOTS;
+      if (!mbar_wait_bounded(&empty[i], ((ab / SLOTS) & 1u) ^ 1u, abort_flag)) { ok = false; return; }
       if (lane == 0) {
-        mbar_arrive_expect_tx(&x_full[stage], C::X_BYTES);
-        tma_load_2d(smem + stage * C::X_BYTES, map, &x_full[stage], k, t);
+        mbar_arrive_expect_tx(&full[i], cols > XK ? C::X_BYTES : C::X_BOX);
+        tma_load_2d(smem + i * C::X_BYTES, map, &full[i], k, t);
+        if (cols > XK) tma_load_2d(smem + i * C::X_BYTES + C::X_BOX, map, &full[i], k + XK, t);
       }
-      armed |= 1u << stage;
-      last_phase = (last_phase & ~(1u << stage)) | (phase << stage);
-      if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+      ++ab;
     };
     for (int tile = tile0; ok && tile < ntiles; tile += step) {
       const int t0 = (tile / p.mt) * N;
-      for (int k = k_lo; k < k_hi; k += XK) push(&map_x, k, t0);
+      for (int k = k_lo; ok && k < k_hi; k += KB) push(&map_x, k, k_hi - k, t0);
       if (MANY && p.ids) {
         if (!waited) { grid_dep_wait(); waited = true; }   // U is the launch before's
         Runs runs;
         runs.init(p, t0, lane);
         int c0, c1, id;
         while (ok && runs.next(c0, c1, id))
-          for (int k = 0; k < 2 * p.rank; k += XK) push(&map_u, k, t0);
+          for (int k = 0; ok && k < 2 * p.rank; k += KB) push(&map_u, k, 2 * p.rank - k, t0);
       }
     }
     if (!ok) { *abort_flag = 1; if (lane == 0) report_device_error(err, DEVERR_TIMEOUT); }
-    for (int s = 0; s < STAGES; ++s)
-      if (armed & (1u << s)) mbar_wait_bounded(&x_full[s], (last_phase >> s) & 1u, nullptr);
-  } else if (warp == 1) {
+    // copies still in flight when something gave up: their slots' barriers, with a limit
+    for (uint32_t u = ab > SLOTS ? ab - SLOTS : 0; u < ab; ++u) mbar_wait_bounded(&full[u % SLOTS], (u / SLOTS) & 1u, abort_flag);
+    } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
-    uint32_t stage = 0, phase = 0, ab = 0, unit_no = 0;
-    bool ok = true, issued = false;
-    const uint32_t sbase = smem_u32(smem);
+    uint32_t ab = 0, unit_no = 0;
+    bool ok = true;
     const uint32_t leader = elect_leader();
-    // Columns [0, len) of one A operand in units of `unit`; an A buffer holds KB columns, an X
-    // stage XK, and both begin with the operand. The warp waits and fences once per A block
-    // where it can (a unit of KB columns): a tcgen05 fence between the MMAs of one sum lets each
-    // wait for the one before (measured: 500 cycles an MMA).
-    auto take_x = [&]() -> bool {
-      if (mbar_wait_bounded(&x_full[stage], phase, abort_flag)) return true;
-      ok = false;
-      return false;
-    };
-    auto give_x = [&]() {
-      umma_commit_by(&x_empty[stage], leader);
-      if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-    };
-    auto b_desc = [&](int k) { return umma_sdesc_sw128(sbase + stage * C::X_BYTES + k * 2, 16, 1024); };
+    const uint64_t b_desc0 = umma_sdesc_sw128(smem_u32(smem), 16, 1024);
+    // Columns [0, len) of one A operand in blocks of KB and units of `unit`. The warp shares its
+    // scheduler with six busy ones, so a block has as few instructions here as it can: two
+    // waits, one fence (a fence between the MMAs of one sum makes each wait for the one
+    // before: 500 cycles an MMA), eight MMAs, two commits.
     auto stream = [&](int len, int unit) {
-      for (int k0 = 0; ok && k0 < len; k0 += KB) {
+      for (int k0 = 0; ok && k0 < len; k0 += KB, ++ab) {
         const int kn = min(KB, len - k0);
-        if (!mbar_wait_poll(&a_full[ab % NA], (ab / NA) & 1u, abort_flag)) { ok = false; break; }
-        const uint32_t at = tmem + C::TMEM_A + (ab % NA) * (KB / 2);
-        issued = true;
+        const uint32_t i = ab % SLOTS, at = tmem + C::TMEM_A + i * (KB / 2);
+        const uint64_t bd = b_desc0 + (uint64_t)(i * (C::X_BYTES / 16));
+        if (!mbar_wait_poll(&full[i], (ab / SLOTS) & 1u, abort_flag)) { ok = false; break; }
         if (unit == KB && kn == KB) {
           const uint32_t buf = unit_no & 1u, dt = tmem + buf * N;
           if (!mbar_wait_poll(&d_empty[buf], ((unit_no >> 1) & 1u) ^ 1u, abort_flag)) { ok = false; break; }
-          if (!take_x()) break;
           tc_fence_after();
-          const uint64_t b0 = b_desc(0);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) umma_f16_ta(dt, at + 8 * kk, b0 + 2 * kk, IDESC, kk != 0, leader);
-          give_x();
-          if (!take_x()) break;
-          const uint64_t b1 = b_desc(0);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) umma_f16_ta(dt, at + 32 + 8 * kk, b1 + 2 * kk, IDESC, 1u, leader);
-          give_x();
+          for (int kk = 0; kk < 8; ++kk)
+            umma_f16_ta(dt, at + 8 * kk, bd + (kk >= 4 ? C::X_BOX / 16 : 0) + 2 * (kk & 3), IDESC, kk != 0, leader);
           umma_commit_by(&d_full[buf], leader);
           ++unit_no;
         } else {
-          int kin = 0;
-          for (int k = 0; k < kn; k += 16) {
+          for (int u = 0; u < kn; u += unit, ++unit_no) {
             const uint32_t buf = unit_no & 1u;
-            if ((k & (XK - 1)) == 0 && !take_x()) break;
-            if (kin == 0) {
-              if (!mbar_wait_poll(&d_empty[buf], ((unit_no >> 1) & 1u) ^ 1u, abort_flag)) { ok = false; break; }
-              tc_fence_after();
-            }
-            umma_f16_ta(tmem + buf * N, at + k / 2, b_desc(k & (XK - 1)), IDESC, kin != 0, leader);
-            kin += 16;
-            if (((k + 16) & (XK - 1)) == 0 || k + 16 >= kn) give_x();
-            if (kin == unit || k + 16 >= kn) {
-              umma_commit_by(&d_full[buf], leader);
-              ++unit_no;
-              kin = 0;
-            }
+            if (!mbar_wait_poll(&d_empty[buf], ((unit_no >> 1) & 1u) ^ 1u, abort_flag)) { ok = false; break; }
+            tc_fence_after();
+            for (int k = u; k < min(u + unit, kn); k += 16)
+              umma_f16_ta(tmem + buf * N, at + k / 2, bd + (k >= XK ? C::X_BOX / 16 : 0) + (k & (XK - 1)) / 8, IDESC, k != u, leader);
+            umma_commit_by(&d_full[buf], leader);
           }
           if (!ok) break;
         }
-        umma_commit_by(&a_empty[ab % NA], leader);
-        ++ab;
+        umma_commit_by(&empty[i], leader);
       }
     };
     for (int tile = tile0; ok && tile < ntiles; tile += step) {
@@ -598,10 +587,25 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
       }
     }
     if (!ok) { *abort_flag = 1; if (lane == 0) report_device_error(err, DEVERR_TIMEOUT); }
-    if (issued) {
-      umma_commit_by(drain, leader);
-      mbar_wait_bounded(drain, 0, nullptr);
+    umma_commit_by(drain, leader);
+    mbar_wait_bounded(drain, 0, nullptr);
+    } else if (warp == 2 && p.codes_tma) {
+    // ---------------- TMA producer of the packed codes ----------------
+    uint32_t cn = 0;
+    bool ok = true;
+    for (int tile = tile0; ok && tile < ntiles; tile += step) {
+      const int r0 = (tile % p.mt) * BM;
+      for (int b = blk0; b < blk1; ++b, ++cn) {
+        const uint32_t i = cn % SLOTS;
+        if (!mbar_wait_bounded(&c_empty[i], ((cn / SLOTS) & 1u) ^ 1u, abort_flag)) { ok = false; break; }
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&c_full[i], BM * C::ROW_BYTES);
+          tma_load_2d(codes + i * C::C_BYTES, &map_c, &c_full[i], b * C::ROW_BYTES, r0);
+        }
+      }
     }
+    if (!ok) { *abort_flag = 1; if (lane == 0) report_device_error(err, DEVERR_TIMEOUT); }
+    for (uint32_t u = cn > SLOTS ? cn - SLOTS : 0; u < cn; ++u) mbar_wait_bounded(&c_full[u % SLOTS], (u / SLOTS) & 1u, nullptr);
     }
   } else if (warp < EPI0) {
     // ---------------- unpack: words -> registers -> tensor memory ----------------
@@ -613,12 +617,12 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
     auto group_of = [&](int c32) -> int {                  // the group of columns 32 c32 ...
       return p.gs32_mul ? (int)__umulhi((uint32_t)c32, p.gs32_mul) : c32;
     };
-    uint32_t ab = 0;                                       // A blocks so far, all sets'
+    uint32_t ab = 0, cb0 = 0;                              // A blocks and stages of codes so far, all sets'
     bool ok = true;
     uint32_t ta = 0;
     auto ready = [&]() -> bool {                           // the block's buffer is free
-      ta = ta0 + (ab % NA) * (KB / 2);
-      if (!mbar_wait_bounded(&a_empty[ab % NA], ((ab / NA) & 1u) ^ 1u, abort_flag)) {
+      ta = ta0 + (ab % SLOTS) * (KB / 2);
+      if (!mbar_wait_bounded(&empty[ab % SLOTS], ((ab / SLOTS) & 1u) ^ 1u, abort_flag)) {
         *abort_flag = 1;
         if (lane == 0) report_device_error(err, DEVERR_TIMEOUT);
         return false;
@@ -630,7 +634,7 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&a_full[ab % NA]);
+      if (lane == 0) mbar_arrive(&full[ab % SLOTS]);
     };
     for (int tile = tile0; ok && tile < ntiles; tile += step) {
       const int row = (tile % p.mt) * BM + row_l;
@@ -640,29 +644,33 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
       const uint32_t ab0 = ab;
       const int first = blk0 + (int)((set - ab0) % SETS);
       const uint32_t* wp = p.qweight + (long long)(live ? row : 0) * p.wpr + (long long)first * WB;
-      uint32_t w[WB];
       float z = 0.0f;
-      auto fetch = [&](int b) {                            // block b's words and (one per block) zero
-        if (b >= blk1) return;
-        if ((b + 1) * KB <= p.d) {
-          if constexpr (BITS == 3) load_words<WB>(wp, w);
-          else {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) load_words<W32>(wp + c * W32, w + c * W32);
+      if (one_zero && first < blk1) z = __ldg(zr + group_of(4 * first));
+      for (int b = first; b < blk1; b += SETS) {
+        ab = ab0 + (uint32_t)(b - blk0);
+        uint32_t w[WB];
+        if (p.codes_tma) {
+          const uint32_t cn = cb0 + (uint32_t)(b - blk0), st = cn % SLOTS;
+          if (!mbar_wait_bounded(&c_full[st], (cn / SLOTS) & 1u, abort_flag)) {
+            *abort_flag = 1;
+            if (lane == 0) report_device_error(err, DEVERR_TIMEOUT);
+            ok = false;
+            break;
           }
+          const uint32_t sc = smem_u32(codes) + st * C::C_BYTES;
+#pragma unroll
+          for (int i = 0; i < BITS; ++i) lds_piece<BITS>(sc, row_l, i, w + 4 * i);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&c_empty[st]);
         } else {
 #pragma unroll
           for (int c = 0; c < 4; ++c)
             if (b * KB + 32 * c < p.d) load_words<W32>(wp + c * W32, w + c * W32);
+          wp += SETS * WB;
         }
-        wp += SETS * WB;
-        if (one_zero) z = __ldg(zr + group_of(4 * b));
-      };
-      fetch(first);
-      for (int b = first; b < blk1; b += SETS) {
-        ab = ab0 + (uint32_t)(b - blk0);
-        if (!ready()) { ok = false; break; }
         const uint32_t nzb = neg_zero(z);
+        if (one_zero && b + SETS < blk1) z = __ldg(zr + group_of(4 * (b + SETS)));
+        if (!ready()) { ok = false; break; }
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           if (b * KB + 32 * c < p.d) {
@@ -672,9 +680,9 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
             tmem_st16(ta + 16 * c, o);
           }
         }
-        fetch(b + SETS);                                   // in flight while the other sets' blocks are multiplied
         publish();
       }
+      cb0 += (uint32_t)(blk1 - blk0);
       ab = ab0 + (uint32_t)(blk1 - blk0);
       if (MANY && p.ids) {
         // the adapters' rows as further A blocks: column k is B[a][row][k mod rank]
@@ -735,14 +743,25 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
         ++unit_no;
       };
       int grp = k_lo / p.gs, kg = k_lo - grp * p.gs;
-      float sn = k_lo < k_hi ? __ldg(sr + grp) : 0.0f;
+      // a lane's row of scales is its own cache line: four at a time where they are aligned
+      const bool by4 = (p.G & 3) == 0 && (reinterpret_cast<uintptr_t>(p.scales) & 15) == 0;
+      float4 s4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      float sn = 0.0f;
+      auto next_scale = [&](bool begin) {
+        if (by4) {
+          if (begin || (grp & 3) == 0) s4 = __ldg(reinterpret_cast<const float4*>(sr + (grp & ~3)));
+        } else {
+          sn = __ldg(sr + grp);
+        }
+      };
+      if (k_lo < k_hi) next_scale(true);
       for (int k = k_lo; k < k_hi; k += p.unit) {
-        const float s = sn * 64.0f;
+        const float s = 64.0f * (by4 ? ((grp & 2) ? ((grp & 1) ? s4.w : s4.z) : ((grp & 1) ? s4.y : s4.x)) : sn);
         kg += p.unit;
         if (kg >= p.gs) {
           kg = 0;
           ++grp;
-          if (k + p.unit < k_hi) sn = __ldg(sr + grp);
+          if (k + p.unit < k_hi) next_scale(false);
         }
         if (!wait()) { ok = false; break; }
 #pragma unroll
@@ -852,6 +871,24 @@ bool make_map(CUtensorMap* m, const void* base, long long inner, long long outer
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The packed rows as bytes, a block's 16 * bits of 128 rows a box. False where TMA cannot take them
+// (rows that are no multiple of 16 bytes: 2 bits with d % 64, 3 bits with d % 128, or a base that
+// is not 16-byte aligned): the unpacking warps then read their rows from global memory.
+bool make_code_map(CUtensorMap* m, const void* base, long long rows, long long row_bytes, int bits) {
+  auto enc = tensor_map_encoder();
+  if (!enc || row_bytes % 16 || reinterpret_cast<uintptr_t>(base) % 16) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
+  cuuint32_t box[2] = {(cuuint32_t)(16 * bits), BM};
+  cuuint32_t es[2] = {1, 1};
+  const CUtensorMapSwizzle sw = bits == 8 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                : bits == 4 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                            : bits == 2 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_NONE;
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // How a call of T tokens is cut. Tiles of 128 tokens where they give at least half the SMs one
@@ -883,8 +920,10 @@ Plan plan_of(long long m, long long d, long long T) {
 }
 
 template <int BITS, int N>
-gptq_status launch(const CUtensorMap& mx, const CUtensorMap& mu, const Params& p, bool pdl, cudaStream_t s) {
-  using C = Cfg<N>;
+gptq_status launch(const CUtensorMap& mx, const CUtensorMap& mu, Params p, bool pdl, cudaStream_t s) {
+  CUtensorMap mc = mx;
+  p.codes_tma = make_code_map(&mc, p.qweight, p.m, (long long)p.wpr * 4, BITS) ? 1 : 0;
+  using C = Cfg<BITS, N>;
   const size_t smem = C::SMEM_FIX + (C::MANY ? 0 : (size_t)N * p.rank * 4);
   static bool attr_done = false;
   if (!attr_done) {
@@ -913,7 +952,7 @@ gptq_status launch(const CUtensorMap& mx, const CUtensorMap& mu, const Params& p
   }
   cfg.attrs = attr;
   cfg.numAttrs = na;
-  cudaLaunchKernelEx(&cfg, adapter_gemm_kernel<BITS, N>, mx, mu, p, device_error_word());
+  cudaLaunchKernelEx(&cfg, adapter_gemm_kernel<BITS, N>, mx, mu, mc, p, device_error_word());
   count_launch();
   return check_launch("adapter_gemm_kernel");
 }

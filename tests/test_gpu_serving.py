@@ -463,6 +463,16 @@ def test_adapter_linear_prompts(g, T, ids, m, d, bits, gs):
     _check_adapter(g, m, d, bits, gs, T, 7, 16, ids, T % 2 == 0, seed=T)
 
 
+@pytest.mark.parametrize("m,d,bits,gs", [(130, 96, 2, 32), (70, 160, 3, 32), (257, 1120, 3, -1), (64, 32, 4, 32),
+                                         (129, 1056, 2, 96), (1, 224, 8, -1), (300, 800, 4, 160)])
+@pytest.mark.parametrize("T", [1, 33, 140])
+def test_adapter_linear_odd_widths(g, m, d, bits, gs, T):
+    """Widths whose packed rows are no multiple of 16 bytes, widths that end inside a block,
+    groups that no power of two above 32 divides."""
+    rng = np.random.default_rng(m + T)
+    _check_adapter(g, m, d, bits, gs, T, 3, 8, rng.integers(-1, 3, T), T == 33, seed=d + T)
+
+
 def test_adapter_linear_without_adapters_and_bad_ids(g):
     rng = np.random.default_rng(1)
     m, d, T = 100, 256, 7
