@@ -25,9 +25,8 @@
 //   warp 1       MMA issuer
 //   warp 2       TMA producer of the packed codes (a lane reading its own row from global memory
 //                touches a cache line per 16 bytes: 32 per load, which paced the unpacking)
-//   warps 4-19   unpack: four sets of four (a warp per 32 tensor-memory lanes), 128-column
-//                blocks in turn, an A buffer each
-//   warps 20-27  epilogue: per unit N / 2 accumulators a thread
+//   warps 4 ...  unpack: sets of four (a warp per 32 tensor-memory lanes), 128-column blocks in turn
+//   last eight   epilogue: per unit N / 2 accumulators a thread
 //
 // Few tokens (N <= 64): a cluster of CTAs splits d for one tile, and the members sum their parts
 // from each other's shared memory, each a share of the rows, adding B[a] U there (one dot
@@ -60,56 +59,75 @@ struct ShrinkParams {
   const int* ids;
   long long ldx, n_adapters;
   int T, d, rank, splits;
-  float* part;                 // [splits][T][rank] fp32, or NULL and
+  float* part;                 // [T][rank] fp32, or NULL and
   __nv_bfloat16* hl;           // [T][2 rank], high parts, low parts
 };
 
-// Few tokens: a CTA per (token, slice of d), its warps over the adapter's rows, four 16-byte loads
-// of a row in flight per lane; the token's slice stays in registers.
-constexpr int SL_COLS = 1024;                            // columns of a slice, at most
+__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
+  float v;
+  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
+               : "=f"(v)
+               : "r"(addr), "r"(rank));
+  return v;
+}
+
+// Few tokens: a cluster per token, a slice of d per CTA, its warps over the adapter's rows, four
+// 16-byte loads of a row in flight per lane; the token's piece stays in registers. The first CTA
+// adds the slices' sums.
+constexpr int SL_COLS = 1024;                            // columns of a piece
 __global__ void __launch_bounds__(SH_WARPS * 32) adapter_shrink_few_kernel(ShrinkParams p, int* __restrict__ err) {
+  __shared__ float sums[128];
   grid_dep_launch();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = blockIdx.y;
   const int a = p.ids[t];
-  if (a >= p.n_adapters && threadIdx.x == 0) report_device_error(err, DEVERR_INDEX);
+  if (a >= p.n_adapters && blockIdx.x == 0 && threadIdx.x == 0) report_device_error(err, DEVERR_INDEX);
   const bool has = a >= 0 && a < p.n_adapters;
-  const int n8 = p.d / 8, c0 = (int)((long long)n8 * blockIdx.y / p.splits), c1 = (int)((long long)n8 * (blockIdx.y + 1) / p.splits);
-  float* out = p.part + ((long long)blockIdx.y * p.T + t) * p.rank;
-  if (!has) {
-    for (int r = threadIdx.x; r < p.rank; r += SH_WARPS * 32) out[r] = 0.0f;
-    return;
-  }
-  constexpr int J = SL_COLS / 256;
-  const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-  uint4 x[J];
+  const int n8 = p.d / 8, c0 = (int)((long long)n8 * blockIdx.x / p.splits), c1 = (int)((long long)n8 * (blockIdx.x + 1) / p.splits);
+  if (has) {
+    constexpr int J = SL_COLS / 256;
+    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+    const uint4* ar = reinterpret_cast<const uint4*>(p.A + (long long)a * p.rank * p.d);
+    const float al = p.alpha ? p.alpha[a] : 1.0f;
+    for (int s0 = c0; s0 < c1; s0 += SL_COLS / 8) {
+      uint4 x[J];
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    const int c = c0 + lane + 32 * j;
-    x[j] = c < c1 ? reinterpret_cast<const uint4*>(p.X + (long long)t * p.ldx)[c] : z;
-  }
-  const uint4* ar = reinterpret_cast<const uint4*>(p.A + (long long)a * p.rank * p.d);
-  const float al = p.alpha ? p.alpha[a] : 1.0f;
+      for (int j = 0; j < J; ++j) {
+        const int c = s0 + lane + 32 * j;
+        x[j] = c < c1 ? reinterpret_cast<const uint4*>(p.X + (long long)t * p.ldx)[c] : z;
+      }
 #pragma unroll 2
-  for (int r = warp; r < p.rank; r += SH_WARPS) {
-    uint4 w[J];
+      for (int r = warp; r < p.rank; r += SH_WARPS) {
+        uint4 w[J];
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const int c = c0 + lane + 32 * j;
-      w[j] = c < c1 ? ar[(long long)r * n8 + c] : z;
+        for (int j = 0; j < J; ++j) {
+          const int c = s0 + lane + 32 * j;
+          w[j] = c < c1 ? ar[(long long)r * n8 + c] : z;
+        }
+        float s = 0.0f;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          float u[8], v[8];
+          unpack8<BF16>(&x[j], u);
+          unpack8<BF16>(&w[j], v);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) s = fmaf(u[k], v[k], s);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == 0) sums[r] = s0 == c0 ? s * al : fmaf(s, al, sums[r]);
+      }
     }
-    float s = 0.0f;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      float u[8], v[8];
-      unpack8<BF16>(&x[j], u);
-      unpack8<BF16>(&w[j], v);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) s = fmaf(u[k], v[k], s);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) out[r] = s * al;
+  } else {
+    for (int r = threadIdx.x; r < p.rank; r += SH_WARPS * 32) sums[r] = 0.0f;
   }
+  __syncthreads();
+  cluster_sync();
+  if (blockIdx.x == 0 && threadIdx.x < p.rank) {
+    float s = 0.0f;
+    for (int k = 0; k < p.splits; ++k) s += ld_cluster(smem_u32(&sums[threadIdx.x]), (uint32_t)k);
+    p.part[(long long)t * p.rank + threadIdx.x] = s;
+  }
+  cluster_sync();
 }
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -222,12 +240,7 @@ __global__ void __launch_bounds__(SH_WARPS * 32) adapter_shrink_kernel(ShrinkPar
 // ---------------------------------------------------------------------------------
 // the packed product
 constexpr int BM = 128, KB = 128, XK = 64;               // rows, columns of a block, columns of one box of X
-constexpr int SLOTS = 4;                                 // blocks in the ring: an A buffer, X, and packed codes each
-constexpr int SETS = 4, UNPACK0 = 4, EPI0 = UNPACK0 + 4 * SETS, NEPI = 8;
-constexpr int THREADS = (EPI0 + NEPI) * 32;              // 896: 72 registers a thread at launch
-// Many tokens: the epilogue's 64 accumulators a thread take registers from the other warps.
-// 128 x 40 + 512 x 56 + 256 x 112 is below 896 x 72, the registers the block has at launch.
-constexpr int REG_ISSUE = 40, REG_UNPACK = 56, REG_EPI = 112;
+constexpr int UNPACK0 = 4, NEPI = 8;                     // first unpacking warp, epilogue warps
 
 struct Params {
   const uint32_t* qweight;
@@ -235,7 +248,7 @@ struct Params {
   const float* zeros;
   const uint16_t* B;
   const int* ids;              // NULL: no adapters
-  const float* part;           // few tokens: U's parts [splits][T][rank]
+  const float* part;           // few tokens: U [T][rank]
   void* Y;
   long long ldy, n_adapters;
   int m, d, T, gs, G, wpr, unit, rank, splits, y_bf16;
@@ -244,13 +257,25 @@ struct Params {
   int mt, nt, S;               // row tiles, token tiles, CTAs that split d
 };
 
+// Few tokens: tiles of N = 16, 32 or 64 with four accumulators in turn, four sets of unpacking
+// warps. Many: tiles of 256 tokens as two parts, an accumulator each, so a block is unpacked once
+// for both and one part's epilogue runs beside the other's MMAs; two sets are enough then, and
+// the epilogue's 128 sums a thread take registers from the other warps (setmaxnreg: 128 x 32 +
+// 256 x 56 + 256 x 168 = 640 x 96, the registers the block has at launch). Four parts of 64
+// columns, measured, take 157 instead of 128 us at 3001 tokens: waiting, fencing and issuing
+// cost the MMA warp about 450 cycles a part.
 template <int BITS, int N>
 struct Cfg {
-  static constexpr bool MANY = N == 128;
+  static constexpr bool MANY = N == 256;
+  static constexpr int PARTS = MANY ? 2 : 1, NP = N / PARTS;        // accumulators of a unit, their columns
+  static constexpr int ND = MANY ? 2 : 4;                  // accumulators in all
+  static constexpr int SETS = MANY ? 2 : 4, EPI0 = UNPACK0 + 4 * SETS, THREADS = (EPI0 + NEPI) * 32;
+  static constexpr int REG_ISSUE = 32, REG_UNPACK = 56, REG_EPI = 168;
+  static constexpr int SLOTS = !MANY ? 4 : (BITS == 8 ? 2 : 3);     // blocks in the ring: an A buffer, X, packed codes
   static constexpr int ROW_BYTES = 16 * BITS;              // packed codes of a row in one block
   static constexpr int C_BYTES = (BM * ROW_BYTES + 1023) / 1024 * 1024;
   static constexpr int X_BOX = N * XK * 2, X_BYTES = 2 * X_BOX;
-  static constexpr int TMEM_A = 2 * N;                     // columns: two accumulators, then SLOTS A blocks of 64
+  static constexpr int TMEM_A = ND * NP;                   // columns: the accumulators, then the A blocks of 64
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr int P_LD = BM + 4;
   static constexpr int P_BYTES = MANY ? 0 : N * P_LD * 4;  // the tile's sums, token-major, for the cluster
@@ -374,6 +399,21 @@ __device__ __forceinline__ uint32_t elect_leader() {
   return l;
 }
 
+// Pairs of fp32 in one 64-bit register pair, two operations an instruction.
+__device__ __forceinline__ uint64_t pack2u(uint32_t lo, uint32_t hi) { return (uint64_t)lo | ((uint64_t)hi << 32); }
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) { return pack2u(__float_as_uint(lo), __float_as_uint(hi)); }
+__device__ __forceinline__ float half2f(uint64_t v, int i) { return __uint_as_float((uint32_t)(i ? v >> 32 : v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t* r) {
   if constexpr (N == 8) {
@@ -390,25 +430,18 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t* r) {
   }
 }
 
-__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
-  float v;
-  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
-               : "=f"(v)
-               : "r"(addr), "r"(rank));
-  return v;
-}
-
-// The runs of one adapter among a tile's N tokens (N = 128: four words of boundary bits), the
-// same in every warp: next() gives a run's columns [c0, c1) and its adapter.
+// The runs of one adapter among a tile's 256 tokens, the same in every warp: next() gives a run's
+// columns [c0, c1) and its adapter. Lane l holds the ids of columns l, l + 32, ...
 struct Runs {
-  uint32_t starts[4];
-  int ids[4], c, n;
+  static constexpr int K = 8;
+  uint32_t starts[K];
+  int ids[K], c, n;
   __device__ __forceinline__ void init(const Params& p, int t0, int lane) {
-    n = min(128, p.T - t0);
+    n = min(32 * K, p.T - t0);
     c = 0;
     int prev = -2;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < K; ++k) {
       const int t = 32 * k + lane;
       int id = -1;
       if (t < n) {
@@ -418,27 +451,23 @@ struct Runs {
       ids[k] = id;
       int before = __shfl_up_sync(0xffffffffu, id, 1);
       if (lane == 0) before = prev;
-      starts[k] = __ballot_sync(0xffffffffu, id != before || (k == 0 && lane == 0));
+      starts[k] = __ballot_sync(0xffffffffu, id != before);
       prev = __shfl_sync(0xffffffffu, id, 31);
     }
   }
   __device__ __forceinline__ bool next(int& c0, int& c1, int& id) {
     while (c < n) {
       c0 = c;
-      int e = 128;                                         // the next start after c
+      int e = 32 * K, v = -1;                              // the next start after c
 #pragma unroll
-      for (int k = 3; k >= 0; --k) {
+      for (int k = K - 1; k >= 0; --k) {
         const uint32_t after = 32 * k > c ? starts[k] : (32 * k + 31 > c ? starts[k] & (0xFFFFFFFEu << (c - 32 * k)) : 0u);
         if (after) e = 32 * k + __ffs(after) - 1;
-      }
-      c1 = min(e, n);
-      c = c1;
-      int v = 0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
         const int x = __shfl_sync(0xffffffffu, ids[k], c0 & 31);
         if ((c0 >> 5) == k) v = x;
       }
+      c1 = min(e, n);
+      c = c1;
       id = v;
       if (id >= 0) return true;
     }
@@ -447,13 +476,14 @@ struct Runs {
 };
 
 template <int BITS, int N>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(Cfg<BITS, N>::THREADS, 1)
 adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_u,
                     const __grid_constant__ CUtensorMap map_c, Params p,
                     int* __restrict__ err) {
   using C = Cfg<BITS, N>;
   constexpr bool MANY = C::MANY;
-  constexpr int NC = N / 2;                                // columns of an epilogue thread
+  constexpr int SLOTS = C::SLOTS, SETS = C::SETS, EPI0 = C::EPI0, THREADS = C::THREADS, NP = C::NP, PARTS = C::PARTS, ND = C::ND;
+  constexpr int NC = NP / 2;                               // columns of an epilogue thread in an accumulator
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -465,8 +495,8 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
   uint64_t* c_full = empty + SLOTS;
   uint64_t* c_empty = c_full + SLOTS;
   uint64_t* d_full = c_empty + SLOTS;
-  uint64_t* d_empty = d_full + 2;
-  uint64_t* drain = d_empty + 2;
+  uint64_t* d_empty = d_full + ND;
+  uint64_t* drain = d_empty + ND;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* P = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(full) + 256);
@@ -480,7 +510,7 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
       mbar_init(&c_full[b], 1);
       mbar_init(&c_empty[b], 4);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < ND; ++b) {
       mbar_init(&d_full[b], 1);
       mbar_init(&d_empty[b], NEPI);
     }
@@ -504,10 +534,10 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
   const int nblk = (p.d + KB - 1) / KB, blk0 = (int)((long long)nblk * rank_c / S), blk1 = (int)((long long)nblk * (rank_c + 1) / S);
   const int k_lo = blk0 * KB, k_hi = min(p.d, blk1 * KB);
   const int ad_units = (2 * p.rank + KB - 1) / KB;         // A blocks of one adapter
-  constexpr uint32_t IDESC = umma_idesc(/*bf16*/ 1, false, false, BM, N);
+  constexpr uint32_t IDESC = umma_idesc(/*bf16*/ 1, false, false, BM, NP);
 
   if (warp < UNPACK0) {
-    if (MANY) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_ISSUE));
+    if (MANY) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REG_ISSUE));
     if (warp == 0) {
     // ---------------- TMA producer of X (and of U) ----------------
     uint32_t ab = 0;                                       // blocks so far
@@ -555,25 +585,31 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
         const uint64_t bd = b_desc0 + (uint64_t)(i * (C::X_BYTES / 16));
         if (!mbar_wait_poll(&full[i], (ab / SLOTS) & 1u, abort_flag)) { ok = false; break; }
         if (unit == KB && kn == KB) {
-          const uint32_t buf = unit_no & 1u, dt = tmem + buf * N;
-          if (!mbar_wait_poll(&d_empty[buf], ((unit_no >> 1) & 1u) ^ 1u, abort_flag)) { ok = false; break; }
-          tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            umma_f16_ta(dt, at + 8 * kk, bd + (kk >= 4 ? C::X_BOX / 16 : 0) + 2 * (kk & 3), IDESC, kk != 0, leader);
-          umma_commit_by(&d_full[buf], leader);
-          ++unit_no;
-        } else {
-          for (int u = 0; u < kn; u += unit, ++unit_no) {
-            const uint32_t buf = unit_no & 1u;
-            if (!mbar_wait_poll(&d_empty[buf], ((unit_no >> 1) & 1u) ^ 1u, abort_flag)) { ok = false; break; }
+          for (int h = 0; h < PARTS; ++h, ++unit_no) {
+            const uint32_t buf = unit_no % ND, dt = tmem + buf * NP;
+            if (!mbar_wait_poll(&d_empty[buf], ((unit_no / ND) & 1u) ^ 1u, abort_flag)) { ok = false; break; }
             tc_fence_after();
-            for (int k = u; k < min(u + unit, kn); k += 16)
-              umma_f16_ta(tmem + buf * N, at + k / 2, bd + (k >= XK ? C::X_BOX / 16 : 0) + (k & (XK - 1)) / 8, IDESC, k != u, leader);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              umma_f16_ta(dt, at + 8 * kk, bd + (h * NP * XK * 2 + (kk >= 4 ? C::X_BOX : 0)) / 16 + 2 * (kk & 3), IDESC, kk != 0,
+                          leader);
             umma_commit_by(&d_full[buf], leader);
           }
-          if (!ok) break;
+        } else {
+          for (int u = 0; ok && u < kn; u += unit) {
+            for (int h = 0; h < PARTS; ++h, ++unit_no) {
+              const uint32_t buf = unit_no % ND;
+              if (!mbar_wait_poll(&d_empty[buf], ((unit_no / ND) & 1u) ^ 1u, abort_flag)) { ok = false; break; }
+              tc_fence_after();
+              for (int k = u; k < min(u + unit, kn); k += 16)
+                umma_f16_ta(tmem + buf * NP, at + k / 2, bd + (h * NP * XK * 2 + (k >= XK ? C::X_BOX : 0)) / 16 + (k & (XK - 1)) / 8,
+                            IDESC, k != u, leader);
+              umma_commit_by(&d_full[buf], leader);
+            }
+          }
         }
+        if (!ok) break;
         umma_commit_by(&empty[i], leader);
       }
     };
@@ -606,10 +642,17 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
     }
     if (!ok) { *abort_flag = 1; if (lane == 0) report_device_error(err, DEVERR_TIMEOUT); }
     for (uint32_t u = cn > SLOTS ? cn - SLOTS : 0; u < cn; ++u) mbar_wait_bounded(&c_full[u % SLOTS], (u / SLOTS) & 1u, nullptr);
+    } else if (warp == 3 && !MANY && p.ids) {
+    // ---------------- U, while the others work ----------------
+    grid_dep_wait();
+    const int t0 = (tile0 / p.mt) * N, n4 = min(N, p.T - t0) * p.rank / 4;
+    const float4* u = reinterpret_cast<const float4*>(p.part + (long long)t0 * p.rank);
+#pragma unroll 4
+    for (int x = lane; x < n4; x += 32) reinterpret_cast<float4*>(Us)[x] = u[x];
     }
   } else if (warp < EPI0) {
     // ---------------- unpack: words -> registers -> tensor memory ----------------
-    if (MANY) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_UNPACK));
+    if (MANY) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REG_UNPACK));
     constexpr int W32 = BITS, WB = 4 * W32;                // words of 32 columns, of a block
     const int set = (warp - UNPACK0) >> 2, q = warp & 3, row_l = 32 * q + lane;
     const uint32_t ta0 = tmem + ((uint32_t)(32 * q) << 16) + C::TMEM_A;
@@ -715,7 +758,7 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
     }
   } else {
     // ---------------- epilogue ----------------
-    if (MANY) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_EPI));
+    if (MANY) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REG_EPI));
     const int q = warp & 3, h = (warp - EPI0) >> 2;
     const uint32_t td = tmem + ((uint32_t)(32 * q) << 16) + h * NC;
     uint32_t unit_no = 0;
@@ -724,11 +767,13 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
     for (int tile = tile0; ok && tile < ntiles; tile += step) {
       const int row = (tile % p.mt) * BM + 32 * q + lane, t0 = (tile / p.mt) * N;
       const float* sr = p.scales + (long long)(row < p.m ? row : 0) * p.G;
-      float run[NC];
+      uint64_t run[PARTS][NC / 2];                        // fp32 pairs
 #pragma unroll
-      for (int c = 0; c < NC; ++c) run[c] = 0.0f;
+      for (int x = 0; x < PARTS; ++x)
+#pragma unroll
+        for (int c = 0; c < NC / 2; ++c) run[x][c] = 0ull;
       auto wait = [&]() -> bool {
-        if (!mbar_wait_bounded(&d_full[unit_no & 1], (unit_no >> 1) & 1u, abort_flag)) {
+        if (!mbar_wait_bounded(&d_full[unit_no % ND], (unit_no / ND) & 1u, abort_flag)) {
           *abort_flag = 1;
           if (lane == 0) report_device_error(err, DEVERR_TIMEOUT);
           return false;
@@ -739,7 +784,7 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
       auto release = [&]() {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&d_empty[unit_no & 1]);
+        if (lane == 0) mbar_arrive(&d_empty[unit_no % ND]);
         ++unit_no;
       };
       int grp = k_lo / p.gs, kg = k_lo - grp * p.gs;
@@ -763,16 +808,21 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
           ++grp;
           if (k + p.unit < k_hi) next_scale(false);
         }
-        if (!wait()) { ok = false; break; }
+        const uint64_t ss = pack2(s, s);
 #pragma unroll
-        for (int c = 0; c < NC; c += LD) {
-          uint32_t a[LD];
-          tmem_ld<LD>(td + (unit_no & 1u) * N + c, a);
-          tmem_ld_wait();
+        for (int x = 0; x < PARTS; ++x) {
+          if (!wait()) { ok = false; break; }
 #pragma unroll
-          for (int i = 0; i < LD; ++i) run[c + i] = fmaf(__uint_as_float(a[i]), s, run[c + i]);
+          for (int c = 0; c < NC; c += LD) {
+            uint32_t a[LD];
+            tmem_ld<LD>(td + (unit_no % ND) * NP + c, a);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < LD; i += 2) run[x][(c + i) / 2] = fma2(pack2u(a[i], a[i + 1]), ss, run[x][(c + i) / 2]);
+          }
+          release();
         }
-        release();
+        if (!ok) break;
       }
       if (MANY) {
         if (p.ids) {
@@ -780,74 +830,114 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
           runs.init(p, t0, lane);
           int c0, c1, id;
           while (ok && runs.next(c0, c1, id)) {
-            for (int u = 0; u < ad_units; ++u) {
-              if (!wait()) { ok = false; break; }
+            for (int u = 0; ok && u < ad_units; ++u) {
 #pragma unroll
-              for (int c = 0; c < NC; c += LD) {
-                uint32_t a[LD];
-                tmem_ld<LD>(td + (unit_no & 1u) * N + c, a);
-                tmem_ld_wait();
+              for (int x = 0; x < PARTS; ++x) {
+                if (!wait()) { ok = false; break; }
+                const int base = x * NP + h * NC;          // the run's columns among this thread's
+                if (c0 < base + NC && c1 > base) {
 #pragma unroll
-                for (int i = 0; i < LD; ++i)
-                  if (h * NC + c + i >= c0 && h * NC + c + i < c1) run[c + i] += __uint_as_float(a[i]);
+                  for (int c = 0; c < NC; c += LD) {
+                    uint32_t a[LD];
+                    tmem_ld<LD>(td + (unit_no % ND) * NP + c, a);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < LD; i += 2) {
+                      const bool in0 = base + c + i >= c0 && base + c + i < c1, in1 = base + c + i + 1 >= c0 && base + c + i + 1 < c1;
+                      run[x][(c + i) / 2] = add2(pack2u(in0 ? a[i] : 0u, in1 ? a[i + 1] : 0u), run[x][(c + i) / 2]);
+                    }
+                  }
+                }
+                release();
               }
-              release();
             }
           }
         }
         if (ok && row < p.m) {
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            const int t = t0 + h * NC + c;
-            if (t < p.T) {
-              if (p.y_bf16) reinterpret_cast<__nv_bfloat16*>(p.Y)[(long long)t * p.ldy + row] = __float2bfloat16_rn(run[c]);
-              else reinterpret_cast<float*>(p.Y)[(long long)t * p.ldy + row] = run[c];
+          for (int x = 0; x < PARTS; ++x)
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+              const int t = t0 + x * NP + h * NC + c;
+              const float v = half2f(run[x][c / 2], c & 1);
+              if (t < p.T) {
+                if (p.y_bf16) reinterpret_cast<__nv_bfloat16*>(p.Y)[(long long)t * p.ldy + row] = __float2bfloat16_rn(v);
+                else reinterpret_cast<float*>(p.Y)[(long long)t * p.ldy + row] = v;
+              }
             }
-          }
         }
       } else {
 #pragma unroll
-        for (int c = 0; c < NC; ++c) P[(h * NC + c) * C::P_LD + 32 * q + lane] = run[c];
+        for (int c = 0; c < NC; ++c) P[(h * NC + c) * C::P_LD + 32 * q + lane] = half2f(run[0][c / 2], c & 1);
       }
     }
   }
 
   if (!MANY) {
-    // ---- few tokens: U, then the cluster's parts, each member its share of the rows
+    // ---- few tokens: the cluster's sums, each member its share of the rows. The adapters' dot
+    // products come first: they wait for no other CTA.
     const int t0 = (tile0 / p.mt) * N, r0 = (tile0 % p.mt) * BM;
-    grid_dep_wait();
-    if (p.ids) {
-      for (int x = threadIdx.x; x < N * p.rank; x += THREADS) {
-        const int c = x / p.rank;
-        float s = 0.0f;
-        if (t0 + c < p.T)
-          for (int k = 0; k < p.splits; ++k) s += p.part[((long long)k * p.T + t0) * p.rank + x];
-        Us[x] = s;
-      }
-    }
-    __syncthreads();
-    cluster_sync();
+    __syncthreads();                                       // U is in shared memory (warp 3)
     const int rows = BM / S, nout = rows * min(N, p.T - t0);
-    for (int x = threadIdx.x; x < nout; x += THREADS) {
-      const int c = x / rows, rl = rank_c * rows + (x - c * rows), row = r0 + rl;
-      if (row >= p.m) continue;
-      float s = 0.0f;
-      for (int k = 0; k < S; ++k) s += ld_cluster(smem_u32(&P[c * C::P_LD + rl]), (uint32_t)k);
-      const int id = p.ids ? p.ids[t0 + c] : -1;
-      if (id >= 0 && id < p.n_adapters) {
-        const uint16_t* b = p.B + ((long long)id * p.m + row) * p.rank;
-        const float* u = Us + c * p.rank;
-        for (int r = 0; r < p.rank; r += 8) {
-          float v[8];
-          unpack8<BF16>(b + r, v);
+    constexpr int OUT = 4;                                 // outputs of a thread in flight
+    bool met = false;
+    for (int x0 = threadIdx.x; x0 < nout || !met; x0 += OUT * THREADS) {
+      float sum[OUT];
+      if (p.ids) {
+        int id[OUT];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) s = fmaf(v[i], u[r + i], s);
+        for (int o = 0; o < OUT; ++o) {
+          const int x = x0 + o * THREADS, c = x / rows;
+          id[o] = x < nout ? p.ids[t0 + c] : -1;
+          sum[o] = 0.0f;
         }
+        for (int r = 0; r < p.rank; r += 8) {
+          uint4 bv[OUT];
+#pragma unroll
+          for (int o = 0; o < OUT; ++o) {
+            const int x = x0 + o * THREADS, c = x / rows, row = r0 + rank_c * rows + (x - c * rows);
+            bv[o] = make_uint4(0u, 0u, 0u, 0u);
+            if (id[o] >= 0 && id[o] < p.n_adapters && row < p.m)
+              bv[o] = __ldg(reinterpret_cast<const uint4*>(p.B + ((long long)id[o] * p.m + row) * p.rank + r));
+          }
+#pragma unroll
+          for (int o = 0; o < OUT; ++o) {
+            const int c = min(x0 + o * THREADS, nout - 1) / rows;
+            float v[8];
+            unpack8<BF16>(&bv[o], v);
+            const float4 ua = *reinterpret_cast<const float4*>(Us + c * p.rank + r), ub = *reinterpret_cast<const float4*>(Us + c * p.rank + r + 4);
+            sum[o] = fmaf(v[0], ua.x, sum[o]); sum[o] = fmaf(v[1], ua.y, sum[o]);
+            sum[o] = fmaf(v[2], ua.z, sum[o]); sum[o] = fmaf(v[3], ua.w, sum[o]);
+            sum[o] = fmaf(v[4], ub.x, sum[o]); sum[o] = fmaf(v[5], ub.y, sum[o]);
+            sum[o] = fmaf(v[6], ub.z, sum[o]); sum[o] = fmaf(v[7], ub.w, sum[o]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int o = 0; o < OUT; ++o) sum[o] = 0.0f;
       }
-      if (p.y_bf16) reinterpret_cast<__nv_bfloat16*>(p.Y)[(long long)(t0 + c) * p.ldy + row] = __float2bfloat16_rn(s);
-      else reinterpret_cast<float*>(p.Y)[(long long)(t0 + c) * p.ldy + row] = s;
+      if (!met) {
+        __syncwarp();
+        if (S > 1) cluster_sync();
+        met = true;
+      }
+#pragma unroll
+      for (int o = 0; o < OUT; ++o) {
+        const int x = x0 + o * THREADS, c = x / rows, rl = rank_c * rows + (x - c * rows), row = r0 + rl;
+        if (x >= nout || row >= p.m) continue;
+        float s = 0.0f;
+        if (S > 1) {
+          for (int k = 0; k < S; ++k) s += ld_cluster(smem_u32(&P[c * C::P_LD + rl]), (uint32_t)k);
+        } else {
+          s = P[c * C::P_LD + rl];
+        }
+        s += sum[o];
+        if (p.y_bf16) reinterpret_cast<__nv_bfloat16*>(p.Y)[(long long)(t0 + c) * p.ldy + row] = __float2bfloat16_rn(s);
+        else reinterpret_cast<float*>(p.Y)[(long long)(t0 + c) * p.ldy + row] = s;
+      }
     }
-    cluster_sync();                                        // nobody leaves while its sums are read
+    __syncwarp();
+    if (S > 1) cluster_sync();                             // nobody leaves while its sums are read
   }
 
   tc_fence_before();
@@ -891,7 +981,7 @@ bool make_code_map(CUtensorMap* m, const void* base, long long rows, long long r
 
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// How a call of T tokens is cut. Tiles of 128 tokens where they give at least half the SMs one
+// How a call of T tokens is cut. Tiles of 256 tokens where they give at least half the SMs one
 // each; else tiles of up to 64 tokens with clusters that split d so that about every SM has a CTA.
 struct Plan {
   int N, mt, nt, S, splits;
@@ -900,20 +990,18 @@ Plan plan_of(long long m, long long d, long long T) {
   Plan p;
   const int sms = sm_count();
   p.mt = (int)((m + BM - 1) / BM);
-  const long long tiles = (long long)p.mt * ((T + 127) / 128);
+  const long long tiles = (long long)p.mt * ((T + 255) / 256);
   p.S = 1;
   p.splits = 1;
   if (T > 64 && 2 * tiles >= sms) {
-    p.N = 128;
+    p.N = 256;
   } else {
     p.N = T <= 16 ? 16 : (T <= 32 ? 32 : 64);
     const long long few = (long long)p.mt * ((T + p.N - 1) / p.N);
     while (p.S < 8 && 2 * p.S * few <= sms && 2 * p.S * KB <= d) p.S *= 2;
-    // slices of d for U: at most SL_COLS columns, at least 256 where there are few tokens
-    if (T <= SH_FEW) {
-      p.splits = (int)((d + SL_COLS - 1) / SL_COLS);
-      while (p.splits < 16 && p.splits * 512 <= d && T * p.splits < 2 * sms) p.splits *= 2;
-    }
+    // slices of d for U, a cluster's CTAs: at least 256 columns, while there are few CTAs
+    if (T <= SH_FEW)
+      while (p.splits < 8 && p.splits * 512 <= d && T * p.splits < 2 * sms) p.splits *= 2;
   }
   p.nt = (int)((T + p.N - 1) / p.N);
   return p;
@@ -935,7 +1023,7 @@ gptq_status launch(const CUtensorMap& mx, const CUtensorMap& mu, Params p, bool 
   const long long tiles = (long long)p.mt * p.nt;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(C::MANY ? std::min<long long>(tiles, sm_count()) : tiles * p.S));
-  cfg.blockDim = dim3(THREADS);
+  cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -963,19 +1051,20 @@ gptq_status launch_n(int N, const CUtensorMap& mx, const CUtensorMap& mu, const 
     case 16: return launch<BITS, 16>(mx, mu, p, pdl, s);
     case 32: return launch<BITS, 32>(mx, mu, p, pdl, s);
     case 64: return launch<BITS, 64>(mx, mu, p, pdl, s);
-    default: return launch<BITS, 128>(mx, mu, p, pdl, s);
+    default: return launch<BITS, 256>(mx, mu, p, pdl, s);
   }
 }
 
 }  // namespace adp
 
-// Workspace: U, as parts in fp32 or as two bf16 parts.
+// Workspace: U, in fp32 or as two bf16 parts.
 size_t adapter_workspace_bytes(long long m, long long d, int bits, int group_size, long long T, int rank) {
   using namespace adp;
   (void)bits;
   (void)group_size;
-  const Plan p = plan_of(m, d, std::max(1LL, T));
-  return round256(4 * (size_t)std::max(1LL, T) * rank * p.splits);
+  (void)m;
+  (void)d;
+  return round256(4 * (size_t)std::max(1LL, T) * rank);
 }
 
 gptq_status adapter_linear_launch(const uint32_t* qweight, const float* scales, const float* zeros, long long m,
@@ -990,10 +1079,22 @@ gptq_status adapter_linear_launch(const uint32_t* qweight, const float* scales, 
     ShrinkParams q{};
     q.X = X; q.A = A; q.alpha = alpha; q.ids = ids; q.ldx = ldx; q.n_adapters = n_adapters;
     q.T = (int)T; q.d = (int)d; q.rank = rank; q.splits = pl.splits;
-    if (pl.N == 128) q.hl = reinterpret_cast<__nv_bfloat16*>(ws);
+    if (pl.N == 256) q.hl = reinterpret_cast<__nv_bfloat16*>(ws);
     else q.part = reinterpret_cast<float*>(ws);
     const unsigned grid = (unsigned)((T + SH_TOK - 1) / SH_TOK);
-    if (T <= SH_FEW) adapter_shrink_few_kernel<<<dim3((unsigned)T, pl.splits), SH_WARPS * 32, 0, s>>>(q, device_error_word());
+    if (T <= SH_FEW) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3((unsigned)pl.splits, (unsigned)T);
+      cfg.blockDim = dim3(SH_WARPS * 32);
+      cfg.stream = s;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = (unsigned)pl.splits;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      cudaLaunchKernelEx(&cfg, adapter_shrink_few_kernel, q, device_error_word());
+    }
     else if (rank == 8) adapter_shrink_kernel<1><<<grid, SH_WARPS * 32, 0, s>>>(q, device_error_word());
     else if (rank == 16) adapter_shrink_kernel<2><<<grid, SH_WARPS * 32, 0, s>>>(q, device_error_word());
     else adapter_shrink_kernel<4><<<grid, SH_WARPS * 32, 0, s>>>(q, device_error_word());
@@ -1015,7 +1116,7 @@ gptq_status adapter_linear_launch(const uint32_t* qweight, const float* scales, 
   CUtensorMap mx, mu;
   if (!make_map(&mx, X, d, T, ldx, pl.N)) return set_error(GPTQ_ERR_CUDA, "cuTensorMapEncodeTiled failed for X");
   mu = mx;
-  if (ids && pl.N == 128 && !make_map(&mu, ws, 2 * rank, T, 2 * rank, pl.N))
+  if (ids && pl.N == 256 && !make_map(&mu, ws, 2 * rank, T, 2 * rank, pl.N))
     return set_error(GPTQ_ERR_CUDA, "cuTensorMapEncodeTiled failed for the adapters' inner product");
   const bool pdl = ids != nullptr;
   switch (bits) {

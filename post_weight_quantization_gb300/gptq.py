@@ -430,23 +430,49 @@ def gptq_gemm_f32(A: torch.Tensor, B: torch.Tensor, C: torch.Tensor, a_kmajor: b
 _DTYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _ALL = tuple(_DTYPE)
 
+# These calls are made for every token of a decoding loop, so their checks cost as little as
+# they can: the common case by attribute comparisons, the full check (which says what is
+# wrong) only where one of them fails.
 
-def _heads(t: torch.Tensor, name: str, dtypes, T: int = -1, heads: int = -1, dim: int = -1) -> None:
+
+def _dense(t, name: str, shape, dtype) -> None:
+    """_need_buffer for one dtype."""
+    if not (type(t) is torch.Tensor and t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
+        _need_buffer(t, name, shape, (dtype,))
+
+
+def _heads(t: torch.Tensor, name: str, dtypes, T: int = -1, heads: int = -1, dim: int = -1) -> int:
     """A (tokens, heads, head_dim) tensor whose heads lie densely in each token's row (the
-    token stride is free), with the given sizes where they are not -1."""
+    token stride is free), with the given sizes where they are not -1. Returns its token
+    stride (dense for a single token)."""
     _need_cuda(t, name, dtypes)
     if t.dim() != 3:
         raise ValueError(f"{name} must be (tokens, heads, head_dim), got {tuple(t.shape)}")
     n, h, d = t.shape
     if (T >= 0 and n != T) or (heads >= 0 and h != heads) or (dim >= 0 and d != dim):
         raise ValueError(f"{name} must have shape ({T}, {heads}, {dim}), got {tuple(t.shape)}")
-    if n and h and (t.stride(2) != 1 or (h > 1 and t.stride(1) != d)):
+    s0, s1, s2 = t.stride()
+    if n and h and (s2 != 1 or (h > 1 and s1 != d)):
         raise ValueError(f"{name} must hold each token's heads densely")
+    return s0 if n > 1 else h * d
 
 
-def _ld(t: torch.Tensor) -> int:
-    """The token stride of a (tokens, heads, head_dim) tensor (dense for a single token)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+def _same_device(dev: int, *tensors) -> None:
+    """All tensors on device `dev` (an index; -1 for the host), which is the current one."""
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            _one_device(*tensors)
+    if dev >= 0 and dev != torch.cuda.current_device():
+        _one_device(*tensors)
+
+
+def _keep(stream, *tensors) -> None:
+    """Tensors allocated here for work on a stream other than the current one: their memory is
+    not given out again before that work is done."""
+    if stream is not None and _stream(stream) != _stream(None):
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+        for t in tensors:
+            t.record_stream(s)
 
 
 def gptq_adapter_linear(q: "QuantizedLayer", X: torch.Tensor, m: int, A: Optional[torch.Tensor] = None,
@@ -458,44 +484,54 @@ def gptq_adapter_linear(q: "QuantizedLayer", X: torch.Tensor, m: int, A: Optiona
     rank) bf16, ids: (T,) int32, alpha: (n,) float32 or None for 1. fp32 output, or bf16 with
     out_bf16. Without A, B and ids it is the packed layer alone."""
     _need_cuda(X, "X", (torch.bfloat16, torch.int16))
-    d, T = q.d, X.shape[0]
-    if X.dim() != 2 or X.stride(1) != 1 or X.shape[1] != d:
+    d, bits, gs = q.d, q.bits, q.group_size
+    if X.dim() != 2 or X.shape[1] != d or X.stride(1) != 1:
         raise ValueError("X must be T x d with unit column stride")
-    G = 1 if q.group_size == -1 else (d // q.group_size if q.group_size > 0 else 1)
-    _need_rows(q.qweight, "q.qweight", m, (d * q.bits + 31) // 32, (torch.int32,))
-    _need_rows(q.scales, "q.scales", m, G, (torch.float32,))
-    _need_rows(q.zeros, "q.zeros", m, G, (torch.float32,))
+    T = X.shape[0]
+    G = 1 if gs == -1 else (d // gs if gs > 0 else 1)
+    qweight, scales, zeros = q.qweight, q.scales, q.zeros
+    if not (qweight.shape == (m, d * bits // 32) and qweight.is_contiguous() and qweight.dtype is torch.int32
+            and qweight.is_cuda):
+        _need_rows(qweight, "q.qweight", m, (d * bits + 31) // 32, (torch.int32,))
+    for t, name in ((scales, "q.scales"), (zeros, "q.zeros")):
+        if not (t.shape == (m, G) and t.is_contiguous() and t.dtype is torch.float32 and t.is_cuda):
+            _need_rows(t, name, m, G, (torch.float32,))
     n, rank = 0, 8
     if A is not None:
         if B is None or ids is None:
             raise ValueError("A needs B and ids")
         if A.dim() != 3:
             raise ValueError(f"A must be (adapters, rank, d), got {tuple(A.shape)}")
-        n, rank = A.shape[0], A.shape[1]
-        _need_buffer(A, "A", (n, rank, d), (torch.bfloat16,))
-        _need_buffer(B, "B", (n, m, rank), (torch.bfloat16,))
-        _need_buffer(ids, "ids", (T,), (torch.int32,))
+        n, rank, _ = A.shape
+        _dense(A, "A", (n, rank, d), torch.bfloat16)
+        _dense(B, "B", (n, m, rank), torch.bfloat16)
+        _dense(ids, "ids", (T,), torch.int32)
         if alpha is not None:
-            _need_buffer(alpha, "alpha", (n,), (torch.float32,))
+            _dense(alpha, "alpha", (n,), torch.float32)
     elif B is not None or ids is not None or alpha is not None:
         raise ValueError("B, ids and alpha need A")
+    dev = X.device
     ydt = torch.bfloat16 if out_bf16 else torch.float32
     if Y is None:
-        Y = torch.empty((T, m), dtype=ydt, device=X.device)
+        Y = torch.empty((T, m), dtype=ydt, device=dev)
+        _keep(stream, Y)
     else:
         _need_cuda(Y, "Y", (ydt,))
         if Y.dim() != 2 or tuple(Y.shape) != (T, m) or Y.stride(1) != 1:
             raise ValueError(f"Y must be ({T}, {m}) with unit column stride, got {tuple(Y.shape)}")
-    need = int(_lib.gptq_adapter_workspace_size(m, d, q.bits, q.group_size, T, rank))
+    need = _lib.gptq_adapter_workspace_size(m, d, bits, gs, T, rank)
     if ws is None:
-        ws = _workspace(need, X.device)
-    ws_bytes = _need_workspace(ws, need)
-    _one_device(q.qweight, q.scales, q.zeros, X, A, B, ids, alpha, Y, ws)
-    st = _lib.gptq_adapter_linear(_ptr(q.qweight), _ptr(q.scales), _ptr(q.zeros), m, d, q.bits, q.group_size, _ptr(X), T,
+        ws, ws_bytes = torch.empty(max(need, 256), dtype=torch.uint8, device=dev), max(need, 256)
+        _keep(stream, ws)
+    else:
+        ws_bytes = _need_workspace(ws, need)
+    _same_device(X.get_device(), qweight, scales, zeros, X, A, B, ids, alpha, Y, ws)
+    st = _lib.gptq_adapter_linear(qweight.data_ptr(), scales.data_ptr(), zeros.data_ptr(), m, d, bits, gs, X.data_ptr(), T,
                                   X.stride(0) if T > 1 else d, _ptr(A), _ptr(B), _ptr(alpha), n, rank, _ptr(ids),
-                                  _ptr(Y), 1 if out_bf16 else 0, Y.stride(0) if T > 1 else m, _ptr(ws), ws_bytes,
+                                  Y.data_ptr(), 1 if out_bf16 else 0, Y.stride(0) if T > 1 else m, ws.data_ptr(), ws_bytes,
                                   _stream(stream))
-    _check(st, "gptq_adapter_linear")
+    if st:
+        _check(st, "gptq_adapter_linear")
     return Y
 
 
@@ -509,45 +545,50 @@ def gptq_qk_norm_rope(Q: torch.Tensor, K: Optional[torch.Tensor], positions: Opt
     None for no rotation), in one pass. Q, K: (T, heads, head_dim) float32, bfloat16 or
     float16; K may be None. Returns (Q_out, K_out) of out_dtype (default: Q's type); Q_out and
     K_out may be Q and K themselves."""
-    _heads(Q, "Q", _ALL)
+    ldq = _heads(Q, "Q", _ALL)
     T, hq, dim = Q.shape
-    hk = 0
+    dtype, dev = Q.dtype, Q.device
+    hk = ldk = ldko = 0
     if K is not None:
-        _heads(K, "K", (Q.dtype,), T, -1, dim)
+        ldk = _heads(K, "K", (dtype,), T, -1, dim)
         hk = K.shape[1]
     elif K_out is not None or wk is not None:
         raise ValueError("K_out and wk need K")
-    odt = out_dtype or (Q_out.dtype if Q_out is not None else Q.dtype)
+    odt = out_dtype or (Q_out.dtype if Q_out is not None else dtype)
     if odt not in _DTYPE:
         raise TypeError(f"out_dtype must be one of {_ALL}, got {odt}")
     if Q_out is None:
-        Q_out = torch.empty((T, hq, dim), dtype=odt, device=Q.device)
+        Q_out, ldqo = torch.empty((T, hq, dim), dtype=odt, device=dev), hq * dim
+        _keep(stream, Q_out)
     else:
-        _heads(Q_out, "Q_out", (odt,), T, hq, dim)
+        ldqo = _heads(Q_out, "Q_out", (odt,), T, hq, dim)
     if K is not None:
         if K_out is None:
-            K_out = torch.empty((T, hk, dim), dtype=odt, device=Q.device)
+            K_out, ldko = torch.empty((T, hk, dim), dtype=odt, device=dev), hk * dim
+            _keep(stream, K_out)
         else:
-            _heads(K_out, "K_out", (odt,), T, hk, dim)
+            ldko = _heads(K_out, "K_out", (odt,), T, hk, dim)
     rot = n_pos = 0
     if cos is not None:
         if sin is None or positions is None or cos.dim() != 2:
             raise ValueError("a rotation needs positions and 2-D tables cos and sin")
-        n_pos, rot = cos.shape[0], 2 * cos.shape[1]
-        _need_buffer(cos, "cos", (n_pos, rot // 2), (torch.float32,))
-        _need_buffer(sin, "sin", (n_pos, rot // 2), (torch.float32,))
-        _need_buffer(positions, "positions", (T,), (torch.int32,))
+        n_pos, half = cos.shape
+        rot = 2 * half
+        _dense(cos, "cos", (n_pos, half), torch.float32)
+        _dense(sin, "sin", (n_pos, half), torch.float32)
+        _dense(positions, "positions", (T,), torch.int32)
     elif sin is not None or positions is not None:
         raise ValueError("sin and positions need cos")
-    for w, name in ((wq, "wq"), (wk, "wk")):
-        if w is not None:
-            _need_buffer(w, name, (dim,), (torch.float32,))
-    _one_device(Q, K, positions, cos, sin, wq, wk, Q_out, K_out)
-    st = _lib.gptq_qk_norm_rope(_ptr(Q), _ptr(K), _DTYPE[Q.dtype], T, hq, hk, dim, _ld(Q), _ld(K) if hk else 0, _ptr(wq),
-                                _ptr(wk), float(eps), _ptr(cos), _ptr(sin), n_pos, rot, int(bool(interleaved)),
-                                _ptr(positions), _ptr(Q_out), _ptr(K_out), _DTYPE[odt], _ld(Q_out),
-                                _ld(K_out) if hk else 0, _stream(stream))
-    _check(st, "gptq_qk_norm_rope")
+    if wq is not None:
+        _dense(wq, "wq", (dim,), torch.float32)
+    if wk is not None:
+        _dense(wk, "wk", (dim,), torch.float32)
+    _same_device(Q.get_device(), Q, K, positions, cos, sin, wq, wk, Q_out, K_out)
+    st = _lib.gptq_qk_norm_rope(Q.data_ptr(), _ptr(K), _DTYPE[dtype], T, hq, hk, dim, ldq, ldk, _ptr(wq), _ptr(wk), eps,
+                                _ptr(cos), _ptr(sin), n_pos, rot, 1 if interleaved else 0, _ptr(positions),
+                                Q_out.data_ptr(), _ptr(K_out), _DTYPE[odt], ldqo, ldko, _stream(stream))
+    if st:
+        _check(st, "gptq_qk_norm_rope")
     return Q_out, K_out
 
 
@@ -568,44 +609,51 @@ class KVCache:
 
     def check(self) -> int:
         """Raise if the pool does not have the layout; returns the number of pages."""
-        _need_buffer(self.pool, "cache.pool", (self.pool.shape[0], self.n_kv_heads,
-                                               self.page_size * (self.head_dim + 8)), (torch.uint8,))
-        return self.pool.shape[0]
+        pages = self.pool.shape[0]
+        _dense(self.pool, "cache.pool", (pages, self.n_kv_heads, self.page_size * (self.head_dim + 8)), torch.uint8)
+        return pages
 
 
 def gptq_kv_append(cache: KVCache, K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
     """Quantize K and V rows (T, n_kv_heads, head_dim; float32, bfloat16 or float16) to 4 bits
     into the cache at slots (T,) int64 = page * page_size + place; negative slots are skipped."""
-    pages = cache.check()
-    _heads(K, "K", _ALL, -1, cache.n_kv_heads, cache.head_dim)
-    T = K.shape[0]
-    _heads(V, "V", (K.dtype,), T, cache.n_kv_heads, cache.head_dim)
-    _need_buffer(slots, "slots", (T,), (torch.int64,))
-    _one_device(cache.pool, K, V, slots)
-    st = _lib.gptq_kv_append(_ptr(K), _ptr(V), _DTYPE[K.dtype], T, cache.n_kv_heads, cache.head_dim, _ld(K), _ld(V),
-                             _ptr(slots), _ptr(cache.pool), pages, cache.page_size, _stream(stream))
-    _check(st, "gptq_kv_append")
+    pages, pool, h, dim = cache.check(), cache.pool, cache.n_kv_heads, cache.head_dim
+    ldk = _heads(K, "K", _ALL, -1, h, dim)
+    T, dtype = K.shape[0], K.dtype
+    ldv = _heads(V, "V", (dtype,), T, h, dim)
+    _dense(slots, "slots", (T,), torch.int64)
+    _same_device(K.get_device(), pool, K, V, slots)
+    st = _lib.gptq_kv_append(K.data_ptr(), V.data_ptr(), _DTYPE[dtype], T, h, dim, ldk, ldv, slots.data_ptr(),
+                             pool.data_ptr(), pages, cache.page_size, _stream(stream))
+    if st:
+        _check(st, "gptq_kv_append")
 
 
 def gptq_kv_read(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
                  K: Optional[torch.Tensor] = None, V: Optional[torch.Tensor] = None, stream=None):
     """The cached values at slots (T,) int64 as (K, V), each (T, n_kv_heads, head_dim) of
     dtype; zeros for negative slots."""
-    pages = cache.check()
+    pages, pool, h, dim = cache.check(), cache.pool, cache.n_kv_heads, cache.head_dim
     T = slots.shape[0]
-    _need_buffer(slots, "slots", (T,), (torch.int64,))
+    _dense(slots, "slots", (T,), torch.int64)
     if dtype not in _DTYPE:
         raise TypeError(f"dtype must be one of {_ALL}, got {dtype}")
+    dev = pool.device
     if K is None:
-        K = torch.empty((T, cache.n_kv_heads, cache.head_dim), dtype=dtype, device=cache.pool.device)
+        K, ldk = torch.empty((T, h, dim), dtype=dtype, device=dev), h * dim
+        _keep(stream, K)
+    else:
+        ldk = _heads(K, "K", (dtype,), T, h, dim)
     if V is None:
-        V = torch.empty((T, cache.n_kv_heads, cache.head_dim), dtype=dtype, device=cache.pool.device)
-    for t, name in ((K, "K"), (V, "V")):
-        _heads(t, name, (dtype,), T, cache.n_kv_heads, cache.head_dim)
-    _one_device(cache.pool, slots, K, V)
-    st = _lib.gptq_kv_read(_ptr(cache.pool), pages, cache.page_size, cache.n_kv_heads, cache.head_dim, _ptr(slots), T,
-                           _ptr(K), _ptr(V), _DTYPE[dtype], _ld(K), _ld(V), _stream(stream))
-    _check(st, "gptq_kv_read")
+        V, ldv = torch.empty((T, h, dim), dtype=dtype, device=dev), h * dim
+        _keep(stream, V)
+    else:
+        ldv = _heads(V, "V", (dtype,), T, h, dim)
+    _same_device(pool.get_device(), pool, slots, K, V)
+    st = _lib.gptq_kv_read(pool.data_ptr(), pages, cache.page_size, h, dim, slots.data_ptr(), T, K.data_ptr(), V.data_ptr(),
+                           _DTYPE[dtype], ldk, ldv, _stream(stream))
+    if st:
+        _check(st, "gptq_kv_read")
     return K, V
 
 
@@ -619,34 +667,39 @@ def gptq_kv_attention(cache: KVCache, Q: torch.Tensor, cu_q: torch.Tensor, kv_le
     tokens are the last ones of those kv_lens[b]. max_q: the most query tokens of a sequence.
     sm_scale defaults to head_dim ** -0.5; window > 0 sees only the last `window` keys up to
     the query's own. lse, when given, is (total_q, n_q_heads) float32. Returns O."""
-    pages = cache.check()
-    _heads(Q, "Q", (torch.bfloat16, torch.float16), -1, -1, cache.head_dim)
-    total, hq, dim = Q.shape
+    pages, pool, h, dim = cache.check(), cache.pool, cache.n_kv_heads, cache.head_dim
+    ldq = _heads(Q, "Q", (torch.bfloat16, torch.float16), -1, -1, dim)
+    total, hq, _ = Q.shape
+    _need_cuda(block_table, "block_table", (torch.int32,))
     if block_table.dim() != 2:
         raise ValueError("block_table must be (batch, pages)")
     batch, width = block_table.shape
-    _need_cuda(block_table, "block_table", (torch.int32,))
-    if batch and width and block_table.stride(1) != 1:
+    ldt, unit = block_table.stride()
+    if batch and width and unit != 1:
         raise ValueError("block_table must have unit column stride")
-    _need_buffer(cu_q, "cu_q", (batch + 1,), (torch.int32,))
-    _need_buffer(kv_lens, "kv_lens", (batch,), (torch.int32,))
+    _dense(cu_q, "cu_q", (batch + 1,), torch.int32)
+    _dense(kv_lens, "kv_lens", (batch,), torch.int32)
+    dtype, dev = Q.dtype, Q.device
     if O is None:
-        O = torch.empty((total, hq, dim), dtype=Q.dtype, device=Q.device)
+        O, ldo = torch.empty((total, hq, dim), dtype=dtype, device=dev), hq * dim
+        _keep(stream, O)
     else:
-        _heads(O, "O", (Q.dtype,), total, hq, dim)
+        ldo = _heads(O, "O", (dtype,), total, hq, dim)
     if lse is not None:
-        _need_buffer(lse, "lse", (total, hq), (torch.float32,))
-    need = int(_lib.gptq_kv_attention_workspace_size(total, hq, cache.n_kv_heads, dim, batch, max_q))
+        _dense(lse, "lse", (total, hq), torch.float32)
+    need = _lib.gptq_kv_attention_workspace_size(total, hq, h, dim, batch, max_q)
     if ws is None:
-        ws = _workspace(need, Q.device)
-    ws_bytes = _need_workspace(ws, need)
-    _one_device(cache.pool, Q, cu_q, kv_lens, block_table, O, lse, ws)
-    st = _lib.gptq_kv_attention(_ptr(Q), _DTYPE[Q.dtype], total, hq, cache.n_kv_heads, dim, _ld(Q), _ptr(cu_q),
-                                _ptr(kv_lens), _ptr(block_table), block_table.stride(0) if batch > 1 else width, width,
-                                batch, max_q, _ptr(cache.pool), pages, cache.page_size,
-                                float(dim ** -0.5 if sm_scale is None else sm_scale), int(bool(causal)), int(window),
-                                _ptr(O), _ld(O), _ptr(lse), _ptr(ws), ws_bytes, _stream(stream))
-    _check(st, "gptq_kv_attention")
+        ws, ws_bytes = torch.empty(max(need, 256), dtype=torch.uint8, device=dev), max(need, 256)
+        _keep(stream, ws)
+    else:
+        ws_bytes = _need_workspace(ws, need)
+    _same_device(Q.get_device(), pool, Q, cu_q, kv_lens, block_table, O, lse, ws)
+    st = _lib.gptq_kv_attention(Q.data_ptr(), _DTYPE[dtype], total, hq, h, dim, ldq, cu_q.data_ptr(), kv_lens.data_ptr(),
+                                block_table.data_ptr(), ldt if batch > 1 else width, width, batch, max_q, pool.data_ptr(),
+                                pages, cache.page_size, dim ** -0.5 if sm_scale is None else sm_scale, 1 if causal else 0,
+                                window, O.data_ptr(), ldo, _ptr(lse), ws.data_ptr(), ws_bytes, _stream(stream))
+    if st:
+        _check(st, "gptq_kv_attention")
     return O
 
 

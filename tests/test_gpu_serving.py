@@ -463,6 +463,18 @@ def test_adapter_linear_prompts(g, T, ids, m, d, bits, gs):
     _check_adapter(g, m, d, bits, gs, T, 7, 16, ids, T % 2 == 0, seed=T)
 
 
+@pytest.mark.parametrize("d,bits,gs,rank,ids", [(256, 4, 128, 16, "runs"), (416, 4, 32, 8, "mixed"), (512, 8, 64, 64, "runs"),
+                                                (384, 2, 64, 40, "one"), (640, 3, 128, 72, "runs"), (320, 3, -1, 128, "mixed"),
+                                                (96, 8, 96, 16, "none"), (1024, 4, -1, 16, "sparse")])
+def test_adapter_linear_many_tokens(g, d, bits, gs, rank, ids):
+    """Enough rows and tokens for the tiles of 256 tokens, partial ones among them."""
+    m, T = 2500, 1300
+    rng = np.random.default_rng(d + rank)
+    ids = {"runs": np.sort(rng.integers(-1, 6, T)), "mixed": rng.integers(-1, 6, T), "one": np.full(T, 2),
+           "none": np.full(T, -1), "sparse": np.where(rng.random(T) < 0.01, 1, -1)}[ids]
+    _check_adapter(g, m, d, bits, gs, T, 6, rank, ids, rank % 16 == 0, seed=rank, ldx=16)
+
+
 @pytest.mark.parametrize("m,d,bits,gs", [(130, 96, 2, 32), (70, 160, 3, 32), (257, 1120, 3, -1), (64, 32, 4, 32),
                                          (129, 1056, 2, 96), (1, 224, 8, -1), (300, 800, 4, 160)])
 @pytest.mark.parametrize("T", [1, 33, 140])
