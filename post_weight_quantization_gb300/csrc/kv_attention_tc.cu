@@ -17,8 +17,10 @@
 //
 //   warp 0        copies of the packed tiles (bulk copies into a ring of two)
 //   warp 1        MMA issuer: S_A, S_B of the first tile; then per tile and group P V, next S
-//   warps 4-7     dequantize: a key per thread, K then V, into a ring of three 128 x D buffers
-//   warps 8-15    softmax: a query row per thread (four warps per group); at the item's end O
+//   warps 4-11    dequantize: half a key per thread, K then V, into a ring of three 128 x D buffers
+//   warps 12-19   softmax: a query row per thread (four warps per group); at the item's end O
+// The loops are unrolled no further than registers need: fully unrolled, the roles' code together
+// missed the instruction cache more often than anything else held them up.
 // The tiles of all items form a line that is cut evenly over one CTA per SM, as in the other
 // kernel, and cut items are joined afterwards.
 #include "kv_line.cuh"
@@ -27,11 +29,11 @@ namespace gptq {
 namespace kva {
 namespace tc {
 
-constexpr int R = 256, THREADS = 512;
+constexpr int R = 256, DEQ0 = 4, NDEQ = 8, SOFT0 = DEQ0 + NDEQ, THREADS = (SOFT0 + 8) * 32;
 constexpr int kItemCost = 1;
 constexpr float kSlack = 4.0f;                  // a row's maximum may lag by 2^4 before it is moved
 constexpr float kShift = 8.0f;                  // probabilities are kept 2^kShift times too large
-constexpr int REG_ISSUE = 48, REG_DEQ = 64, REG_SOFT = 200;       // 128 x 48 + 128 x 64 + 256 x 200 = 512 x 128
+constexpr int REG_ISSUE = 72, REG_DEQ = 64, REG_SOFT = 136;       // 128 x 72 + 256 x 64 + 256 x 136, below 640 x 96
 
 template <int D>
 struct Cfg {
@@ -100,12 +102,18 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
       "r"(r[30]), "r"(r[31])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Eight codes of a word as four fp16 pairs code * scale + low, one rounding each: 0x6400 | c is
-// 1024 + c, less 1024 exactly c. CLAMP keeps 15 * scale + low, where it rounds past fp16's largest
-// number, at that number.
-template <bool CLAMP>
+// 1024 + c, less 1024 exactly c. 15 * scale + low can round past fp16's largest number: it is kept
+// at that number.
 __device__ __forceinline__ uint4 dequant8(uint32_t w, __half2 scale, __half2 low) {
   const uint32_t e = w & 0x0F0F0F0Fu, d = (w >> 4) & 0x0F0F0F0Fu;
   uint32_t o[4];
@@ -113,7 +121,7 @@ __device__ __forceinline__ uint4 dequant8(uint32_t w, __half2 scale, __half2 low
   for (int i = 0; i < 4; ++i) {                 // bytes i of both; a selector's top bit repeats a byte's sign bit: 0
     const uint32_t c = prmt(e, d, (uint32_t)(i | ((8 + i) << 4) | ((4 + i) << 8) | ((12 + i) << 12))) | 0x64006400u;
     __half2 x = __hfma2(__hsub2(*reinterpret_cast<const __half2*>(&c), __float2half2_rn(1024.0f)), scale, low);
-    if (CLAMP) x = __hmin2_nan(x, __float2half2_rn(65504.0f));
+    x = __hmin2_nan(x, __float2half2_rn(65504.0f));
     o[i] = *reinterpret_cast<const uint32_t*>(&x);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
@@ -144,10 +152,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
   if (tid == 0) {
     for (int i = 0; i < NC; ++i) {
       mbar_init(&c_full[i], 1);
-      mbar_init(&c_empty[i], 4);
+      mbar_init(&c_empty[i], NDEQ);
     }
     for (int i = 0; i < NM; ++i) {
-      mbar_init(&m_full[i], 4);
+      mbar_init(&m_full[i], NDEQ);
       mbar_init(&m_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -255,12 +263,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
         mbar_wait_bounded(drain, 0, nullptr);
       }
     }
-  } else if (warp < 8) {
-    // ---------------- dequantize: thread r holds key r of the tile ----------------
+  } else if (warp < SOFT0) {
+    // ---------------- dequantize: a thread holds one half of one key of the tile ----------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_DEQ));
-    const int r = tid - 128, blk = r >> p.pb_log2, at = r & (p.pb - 1);
-    const uint32_t off = blk * p.pb * (D + 8) + at * (D / 2), noff = blk * p.pb * (D + 8) + p.pb * D + at * 8;
-    const uint32_t sb = smem_u32(smem), row = r * 128, sw = r & 7;
+    constexpr int NW = D / 16;                                       // words of half a row
+    const int r = (tid - 32 * DEQ0) & 127, half = (tid - 32 * DEQ0) >> 7, blk = r >> p.pb_log2, at = r & (p.pb - 1);
+    const uint32_t off = blk * p.pb * (D + 8) + at * (D / 2) + half * (D / 4), noff = blk * p.pb * (D + 8) + p.pb * D + at * 8;
+    const uint32_t sb = smem_u32(smem), sw = r & 7;
     uint32_t n = 0, mat = 0;
     while (ok && line.next(p, it, err)) {
       for (int i = 0; i < it.nt; ++i, ++n) {
@@ -274,12 +283,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
         const float2 vn = __half22float2(*reinterpret_cast<const __half2*>(&num[1]));
         const float any = kn.x + kn.y + vn.x + vn.y;                 // finite numbers, or a NaN among them
         if (any != any) { num[0] = 0x7FFF7FFFu; num[1] = 0u; }
-#pragma unroll
+#pragma unroll 1
         for (int kv = 0; kv < 2; ++kv, ++mat) {
           const uint32_t slot = mat % NM;
-          uint32_t w[D / 8];
+          uint32_t w[NW];
 #pragma unroll
-          for (int c = 0; c < D / 8; c += 4)
+          for (int c = 0; c < NW; c += 4)
             asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                          : "=r"(w[c]), "=r"(w[c + 1]), "=r"(w[c + 2]), "=r"(w[c + 3])
                          : "r"(base + off + kv * p.pb * (D / 2) + 4 * c));
@@ -288,21 +297,18 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
             if (lane == 0) mbar_arrive(&c_empty[st]);
           }
           if (!mbar_wait_bounded(&m_empty[slot], (mat / NM & 1u) ^ 1u, abort_flag)) { give_up(); break; }
-          const __half2 s = __half2half2(__ushort_as_half((unsigned short)num[kv]));
-          const __half2 l = __half2half2(__ushort_as_half((unsigned short)(num[kv] >> 16)));
-          const uint32_t dst = sb + C::MATS + slot * C::MAT + row;
-          auto all = [&](auto clamp) {
+          const uint32_t nn = kv ? num[1] : num[0];
+          const __half2 s = __half2half2(__ushort_as_half((unsigned short)nn));
+          const __half2 l = __half2half2(__ushort_as_half((unsigned short)(nn >> 16)));
+          const uint32_t dst = sb + C::MATS + slot * C::MAT + r * 128;
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-              const uint4 v = dequant8<decltype(clamp)::value>(w[c], s, l);
-              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + (c >> 3) * C::BOX + (((c & 7) ^ sw) << 4)), "r"(v.x),
-                           "r"(v.y), "r"(v.z), "r"(v.w)
-                           : "memory");
-            }
-          };
-          const float2 nf = kv ? vn : kn;
-          if (__any_sync(0xffffffffu, fmaf(15.0f, nf.x, nf.y) > 65504.0f)) all(std::true_type{});
-          else all(std::false_type{});
+          for (int c = 0; c < NW; ++c) {
+            const int cc = half * NW + c;                            // the row's 16-byte piece
+            const uint4 v = dequant8(w[c], s, l);
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + (cc >> 3) * C::BOX + (((cc & 7) ^ sw) << 4)), "r"(v.x),
+                         "r"(v.y), "r"(v.z), "r"(v.w)
+                         : "memory");
+          }
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&m_full[slot]);
@@ -313,7 +319,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
   } else {
     // ---------------- softmax: a query row per thread, group x ----------------
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_SOFT));
-    const int x = (warp - 8) >> 2, r = tid - 256 - 128 * x;          // this group's row
+    const int x = (warp - SOFT0) >> 2, r = tid - 32 * SOFT0 - 128 * x;          // this group's row
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t st = s_tm + 128 * x + lanes, ot = o_tm + D * x + lanes;
     uint32_t ns = 0, no = 0;                                         // tiles whose S, whose P V this group has waited for
@@ -372,21 +378,39 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
         if (!mbar_wait_bounded(&s_full[x], ns & 1u, abort_flag)) { give_up(); break; }
         ++ns;
         tc_fence_after();
-        float s[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(st + 32 * c, reinterpret_cast<uint32_t*>(s) + 32 * c);
-        tmem_ld_wait();
+        // The scores are read twice from tensor memory, 32 at a time, for the maximum and for the
+        // probabilities (128 of them in registers at once spilled: 430 instead of 250 us at 1024
+        // tokens over 8187 keys).
         const int key0 = (it.tl + i) * TILE;
-        if (key0 < lo_max || key0 + TILE > hi_min) {
+        const bool masked = key0 < lo_max || key0 + TILE > hi_min;
+        const int u_lo = lo - key0, u_hi = hi - key0;                // columns the row sees
+        uint32_t s[2][32];
+        float m4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+        auto each = [&](auto&& f) {              // f(32 scores, first column): two chunks an iteration, the next one loading
+          tmem_ld32(st, s[0]);
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 64) {
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (key0 + c > hi || key0 + c < lo) s[c] = -CUDART_INF_F;
-        }
-        float m4[4] = {s[0], s[1], s[2], s[3]};
+            for (int y = 0; y < 2; ++y) {
+              tmem_ld_wait();
+              if (c + 32 * y < 96) tmem_ld32(st + c + 32 * (y + 1), s[1 - y]);
+              uint32_t* v = s[y];
+              if (masked) {
+                // bits of the columns that the row sees
+                const int a = u_lo - c - 32 * y, b = u_hi - c - 32 * y;
+                const uint32_t see = (a > 31 || b < 0) ? 0u : (a > 0 ? 0xFFFFFFFFu << a : 0xFFFFFFFFu) & (b < 31 ? 0xFFFFFFFFu >> (31 - b) : 0xFFFFFFFFu);
 #pragma unroll
-        for (int c = 4; c < 128; c += 4)
+                for (int k = 0; k < 32; ++k)
+                  if (!(see >> k & 1u)) v[k] = 0xFF800000u;          // -infinity
+              }
+              f(v, c + 32 * y);
+            }
+          }
+        };
+        each([&](const uint32_t* v, int) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], s[c + k]);
+          for (int k = 0; k < 32; ++k) m4[k & 3] = fmaxf(m4[k & 3], __uint_as_float(v[k]));
+        });
         const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * rowc;
         float f = 1.0f;
         const bool over = mx > thr;
@@ -402,7 +426,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
           ++no;
           pending = 0;
           tc_fence_after();
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             uint32_t o[32];
             tmem_ld32(ot + c, o);
@@ -419,19 +443,17 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
         }
         const float b = kShift - mrc;
         float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        uint32_t* pw = reinterpret_cast<uint32_t*>(s);
+        each([&](const uint32_t* v, int c) {
+          uint32_t pw[16];
 #pragma unroll
-        for (int c = 0; c < 128; c += 4) {
-          float e[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            e[k] = ex2(fmaf(s[c + k], rowc, b));
-            sum[k] += e[k];
+          for (int k = 0; k < 32; k += 2) {
+            const float e0 = ex2(fmaf(__uint_as_float(v[k]), rowc, b)), e1 = ex2(fmaf(__uint_as_float(v[k + 1]), rowc, b));
+            sum[k & 2] += e0;
+            sum[(k & 2) + 1] += e1;
+            pw[k / 2] = pack_half2(e0, e1);
           }
-          pw[c / 2] = pack_half2(e[0], e[1]);
-          pw[c / 2 + 1] = pack_half2(e[2], e[3]);
-          if (c % 64 == 60) tmem_st32(st + (c / 64) * 32, pw + (c / 64) * 32);
-        }
+          tmem_st16(st + c / 2, pw);             // over columns that have been read: c / 2 + 16 <= c + 32
+        });
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         tmem_st_wait();
         tc_fence_before();
@@ -449,7 +471,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
       const long long at = (it.sq.tok0 + tk) * p.ldo + (long long)hq * D;
       float* out = p.part + (2LL * blockIdx.x + (it.lead ? 0 : 1)) * C::PART;
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
         if (it.nt > 0) {
@@ -478,7 +500,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
       __syncwarp();
       if (lane == 0 && it.nt > 0) mbar_arrive(&o_free[x]);
     }
-    if (tid == 256) p.cut[blockIdx.x] = cut;
+    if (tid == 32 * SOFT0) p.cut[blockIdx.x] = cut;
   }
 
   tc_fence_before();
@@ -515,7 +537,7 @@ static gptq_status tc_launch(kva::Params p, void* ws, cudaStream_t s) {
   tc::kv_tc_kernel<D><<<ctas, tc::THREADS, C::SMEM, s>>>(p, device_error_word());
   count_launch();
   if (gptq_status st = check_launch("kv_tc_kernel")) return st;
-  launch_pdl(kv_join_kernel<D, tc::R>, dim3(ctas, tc::R / 8), dim3(JOIN_WARPS * 32), 0, s, p, device_error_word());
+  launch_pdl(kv_join_kernel<D, tc::R>, dim3(ctas, 8), dim3(JOIN_WARPS * 32), 0, s, p, device_error_word());
   count_launch();
   return check_launch("kv_join_kernel");
 }

@@ -265,63 +265,96 @@ struct Copies {
   }
 };
 
-// Joins the parts of the items that were cut: a CTA per (CTA c of the other kernel, eight rows)
-// takes the item that c began and others ended, two warps per query row. The parts lie in
-// c's second place and the following CTAs' first.
+// Joins the parts of the items that were cut. CTA (c, y) takes the item that CTA c of the other
+// kernel began and others ended; its parts lie in c's second place and the following CTAs' first.
+// A warp takes a row, or, where there are many parts, two warps share one.
 constexpr int JOIN_WARPS = 16;
 template <int D, int R>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) kv_join_kernel(Params p, int* __restrict__ err) {
   constexpr int VPL = D / 32, PART = R * D + 2 * R;
-  __shared__ float sl[JOIN_WARPS], so[JOIN_WARPS / 2][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, half = warp >> 3;
+  using V = typename std::conditional<VPL == 2, float2, float4>::type;       // a lane's values, NV vectors of VW
+  constexpr int NV = VPL == 2 ? 1 : VPL / 4, VW = VPL / NV;
+  __shared__ float sl[JOIN_WARPS / 2], so[JOIN_WARPS / 2][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_dep_wait();
   const int c = blockIdx.x;
   const int4 cut = p.cut[c];
   if (cut.z == 0) return;
   const Seq sq = load_seq(p, cut.x, R, err);
-  const int h = cut.y / sq.nrt, rt = cut.y - h * sq.nrt, r = 8 * blockIdx.y + (warp & 7), rr = rt * R + r;
-  const bool live = rr < (long long)sq.nq * p.G;
-  const int np = cut.z;
+  const int h = cut.y / sq.nrt, rt = cut.y - h * sq.nrt, np = cut.z;
+  const long long all_rows = (long long)sq.nq * p.G;
   auto part_of = [&](int k) { return p.part + (2LL * (c + k) + (k == 0 ? 1 : 0)) * PART; };
-  float mm = -CUDART_INF_F, ll = 0.0f, acc[VPL];
-#pragma unroll
-  for (int k = 0; k < VPL; ++k) acc[k] = 0.0f;
-  if (live) {
+  float mm, ll, acc[VPL];
+  auto largest = [&](int r) {
+    mm = -CUDART_INF_F;
     for (int k = lane; k < np; k += 32) mm = fmaxf(mm, part_of(k)[R * D + r]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+    ll = 0.0f;
+#pragma unroll
+    for (int k = 0; k < VPL; ++k) acc[k] = 0.0f;
+  };
+  auto add = [&](int k, int r) {
+    const float* pt = part_of(k);
+    const float mk = pt[R * D + r], f = mk == -CUDART_INF_F ? 0.0f : ex2(mk - mm);
+    ll = fmaf(f, pt[R * D + R + r], ll);
+#pragma unroll
+    for (int x = 0; x < NV; ++x) {               // lane's values: VW at (32 x + lane) VW
+      const V v = *reinterpret_cast<const V*>(pt + r * D + (32 * x + lane) * VW);
+      const float* vf = reinterpret_cast<const float*>(&v);
+#pragma unroll
+      for (int y = 0; y < VW; ++y) acc[x * VW + y] = fmaf(f, vf[y], acc[x * VW + y]);
+    }
+  };
+  auto write = [&](int rr) {
+    const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+    const int i = rr / p.G, hq = h * p.G + rr - i * p.G;
+    const long long at = (sq.tok0 + i) * p.ldo + (long long)hq * D;
+#pragma unroll
+    for (int x = 0; x < VPL; ++x) {
+      float v = acc[x] * inv;
+      const long long d = at + (32 * (x / VW) + lane) * VW + x % VW;
+      if (p.q_f16) {
+        v = v == v ? fminf(fmaxf(v, -65504.0f), 65504.0f) : v;
+        reinterpret_cast<__half*>(p.O)[d] = __float2half_rn(v);
+      } else {
+        reinterpret_cast<__nv_bfloat16*>(p.O)[d] = __float2bfloat16_rn(v);
+      }
+    }
+    if (p.lse && lane == 0)
+      p.lse[(sq.tok0 + i) * p.Hq + hq] = ll == 0.0f ? -CUDART_INF_F : (mm + log2f(ll)) * 0.6931471805599453f;
+  };
+  if (np <= 4) {
+    for (int r = JOIN_WARPS * blockIdx.y + warp; r < R && (long long)rt * R + r < all_rows; r += JOIN_WARPS * gridDim.y) {
+      largest(r);
+      for (int k = 0; k < np; ++k) add(k, r);
+      write(rt * R + r);
+    }
+    return;
+  }
+  const int half = warp >> 3;
+  for (int r8 = 8 * blockIdx.y; r8 < R && (long long)rt * R + r8 < all_rows; r8 += 8 * gridDim.y) {
+    const int r = r8 + (warp & 7), rr = rt * R + r;
+    const bool live = rr < all_rows;
+    if (live) {
+      largest(r);
 #pragma unroll 8
-    for (int k = half; k < np; k += 2) {
-      const float* pt = part_of(k);
-      const float mk = pt[R * D + r], f = mk == -CUDART_INF_F ? 0.0f : ex2(mk - mm);
-      ll = fmaf(f, pt[R * D + R + r], ll);
-#pragma unroll
-      for (int x = 0; x < VPL; ++x) acc[x] = fmaf(f, pt[r * D + lane * VPL + x], acc[x]);
+      for (int k = half; k < np; k += 2) add(k, r);
     }
-  }
-  if (half) {
-    if (lane == 0) sl[warp & 7] = ll;
+    if (half && live) {
+      if (lane == 0) sl[warp & 7] = ll;
 #pragma unroll
-    for (int x = 0; x < VPL; ++x) so[warp & 7][lane * VPL + x] = acc[x];
-  }
-  __syncthreads();
-  if (half || !live) return;
-  ll += sl[warp];
-  const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
-  const int i = rr / p.G, hq = h * p.G + rr - i * p.G;
-#pragma unroll
-  for (int x = 0; x < VPL; ++x) {
-    float v = (acc[x] + so[warp][lane * VPL + x]) * inv;
-    const long long at = (sq.tok0 + i) * p.ldo + (long long)hq * D + lane * VPL + x;
-    if (p.q_f16) {
-      v = v == v ? fminf(fmaxf(v, -65504.0f), 65504.0f) : v;
-      reinterpret_cast<__half*>(p.O)[at] = __float2half_rn(v);
-    } else {
-      reinterpret_cast<__nv_bfloat16*>(p.O)[at] = __float2bfloat16_rn(v);
+      for (int x = 0; x < VPL; ++x) so[warp & 7][(32 * (x / VW) + lane) * VW + x % VW] = acc[x];
     }
+    __syncthreads();
+    if (!half && live) {
+      ll += sl[warp];
+#pragma unroll
+      for (int x = 0; x < VPL; ++x) acc[x] += so[warp][(32 * (x / VW) + lane) * VW + x % VW];
+      write(rr);
+    }
+    __syncthreads();
   }
-  if (p.lse && lane == 0)
-    p.lse[(sq.tok0 + i) * p.Hq + hq] = ll == 0.0f ? -CUDART_INF_F : (mm + log2f(ll)) * 0.6931471805599453f;
 }
 
 // The page geometry of a call (host).
