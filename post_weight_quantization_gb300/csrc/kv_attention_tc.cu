@@ -127,6 +127,29 @@ __device__ __forceinline__ uint4 dequant8(uint32_t w, __half2 scale, __half2 low
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// The larger of three; two fp32 values in one register pair, a multiply-add or a sum of both at once.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ void halves(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 template <int D>
 __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __restrict__ err) {
   using C = Cfg<D>;
@@ -219,8 +242,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
           if (it.nt == 0) break;
           // matrices in order: K0, K1 before V0 would need a fourth buffer, so V(i - 1) is waited for
           // after K(i) only in the ring's own order K, V, K, V: V(i - 1) is number mat - 1
-          if (i > 0 && !mbar_wait_bounded(&m_full[vslot], (mat - 1) / NM & 1u, abort_flag)) { give_up(); break; }
-          if (i < it.nt && !mbar_wait_bounded(&m_full[kslot], mat / NM & 1u, abort_flag)) { give_up(); break; }
+          if (i > 0 && !mbar_wait_poll(&m_full[vslot], (mat - 1) / NM & 1u, abort_flag)) { give_up(); break; }
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             if (x >= groups) break;
@@ -240,8 +262,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
               for (int kk = 0; kk < 8; ++kk)                         // 16 keys: 16 rows of 128 bytes
                 umma_f16_ts(o_tm + D * x, s_tm + 128 * x + 8 * kk, vd + kk * 128, IDO, i > 1 || kk > 0, leader);
               commit_by(&o_done[x], leader);
+              if (x == groups - 1) commit_by(&m_empty[vslot], leader);   // K(i + 1) is written there while S is computed
             }
             if (i < it.nt) {
+              if (x == 0) {
+                if (!mbar_wait_poll(&m_full[kslot], mat / NM & 1u, abort_flag)) { give_up(); break; }
+                tc_fence_after();
+              }
               const uint64_t kd = k_desc + (uint64_t)(kslot * (C::MAT / 16)), qd = q_desc + (uint64_t)(x * (C::MAT / 16));
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk)
@@ -251,7 +278,6 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
             }
           }
           if (!ok) break;
-          if (i > 0) commit_by(&m_empty[vslot], leader);
           if (i < it.nt) {
             commit_by(&m_empty[kslot], leader);
             mat += 2;                                                // this tile's K and V
@@ -409,7 +435,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
         };
         each([&](const uint32_t* v, int) {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) m4[k & 3] = fmaxf(m4[k & 3], __uint_as_float(v[k]));
+          for (int k = 0; k < 32; k += 2) m4[k / 2 & 3] = max3(m4[k / 2 & 3], __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
         });
         const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * rowc;
         float f = 1.0f;
@@ -442,19 +468,24 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
           pending = 0;
         }
         const float b = kShift - mrc;
-        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const uint64_t b2 = pair(b, b), rowc2 = pair(rowc, rowc);
+        uint64_t sum[2] = {0, 0};
         each([&](const uint32_t* v, int c) {
           uint32_t pw[16];
 #pragma unroll
           for (int k = 0; k < 32; k += 2) {
-            const float e0 = ex2(fmaf(__uint_as_float(v[k]), rowc, b)), e1 = ex2(fmaf(__uint_as_float(v[k + 1]), rowc, b));
-            sum[k & 2] += e0;
-            sum[(k & 2) + 1] += e1;
+            float e0, e1;
+            halves(fma2(pair(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), rowc2, b2), e0, e1);
+            e0 = ex2(e0);
+            e1 = ex2(e1);
+            sum[k / 2 & 1] = add2(sum[k / 2 & 1], pair(e0, e1));
             pw[k / 2] = pack_half2(e0, e1);
           }
           tmem_st16(st + c / 2, pw);             // over columns that have been read: c / 2 + 16 <= c + 32
         });
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        float s0, s1;
+        halves(add2(sum[0], sum[1]), s0, s1);
+        l += s0 + s1;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
