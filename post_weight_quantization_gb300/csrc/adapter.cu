@@ -816,7 +816,7 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
           for (int c = 0; c < NC; c += LD) {
             uint32_t a[LD];
             tmem_ld<LD>(td + (unit_no % ND) * NP + c, a);
-            tmem_ld_wait();
+            tmem_ld_wait<LD>(a);
 #pragma unroll
             for (int i = 0; i < LD; i += 2) run[x][(c + i) / 2] = fma2(pack2u(a[i], a[i + 1]), ss, run[x][(c + i) / 2]);
           }
@@ -840,7 +840,7 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
                   for (int c = 0; c < NC; c += LD) {
                     uint32_t a[LD];
                     tmem_ld<LD>(td + (unit_no % ND) * NP + c, a);
-                    tmem_ld_wait();
+                    tmem_ld_wait<LD>(a);
 #pragma unroll
                     for (int i = 0; i < LD; i += 2) {
                       const bool in0 = base + c + i >= c0 && base + c + i < c1, in1 = base + c + i + 1 >= c0 && base + c + i + 1 < c1;

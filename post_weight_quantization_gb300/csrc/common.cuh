@@ -312,6 +312,13 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16_nowait(uint32_t taddr, uint32
 }
 
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// The same, passing the loaded registers through, so that nothing computed from them can be moved before the wait.
+template <int N>
+__device__ __forceinline__ void tmem_ld_wait(uint32_t* r) {
+  tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
 
 // Copy a PR x PC fp32 tile into shared memory (row stride ldd): element (i, c) is
 // src[i * lds + c] when i < rows and c < cols, else 0. Each thread issues UNROLL

@@ -29,11 +29,11 @@ namespace gptq {
 namespace kva {
 namespace tc {
 
-constexpr int R = 256, DEQ0 = 4, NDEQ = 8, SOFT0 = DEQ0 + NDEQ, THREADS = (SOFT0 + 8) * 32;
+constexpr int R = 256, DEQ0 = 4, NDEQ = 8, SOFT0 = DEQ0 + NDEQ, THREADS = (SOFT0 + 16) * 32;
 constexpr int kItemCost = 1;
 constexpr float kSlack = 4.0f;                  // a row's maximum may lag by 2^4 before it is moved
 constexpr float kShift = 8.0f;                  // probabilities are kept 2^kShift times too large
-constexpr int REG_ISSUE = 72, REG_DEQ = 64, REG_SOFT = 136;       // 128 x 72 + 256 x 64 + 256 x 136, below 640 x 96
+constexpr int REG_ISSUE = 40, REG_DEQ = 56, REG_SOFT = 88;        // 128 x 40 + 256 x 56 + 512 x 88 = 896 x 72
 
 template <int D>
 struct Cfg {
@@ -43,7 +43,8 @@ struct Cfg {
   static constexpr int STAGE = TILE * (D + 8);
   static constexpr int NC = 2, NM = 3;          // ring of packed tiles, ring of dequantized matrices
   static constexpr int CODES = 2 * MAT, MATS = CODES + (NC * STAGE + 1023) / 1024 * 1024, BARS = MATS + NM * MAT;
-  static constexpr int SMEM = BARS + 512 + 1024;
+  static constexpr int ROWS = BARS + 512;       // two floats per row, twice: what the halves of a row tell each other
+  static constexpr int SMEM = ROWS + 4096 + 1024;
   static constexpr int PART = R * D + 2 * R;
 };
 
@@ -91,23 +92,15 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
         "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
-      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
-      "r"(r[30]), "r"(r[31])
-      : "memory");
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -167,9 +160,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
   uint64_t* o_done = p_full + 2;                                     // P V of a tile is done
   uint64_t* o_free = o_done + 2;                                     // the item's O has been read
   uint64_t* drain = o_free + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* told = drain + 1;                                        // 8: both halves of 32 rows have written
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(told + 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  long long* sh = reinterpret_cast<long long*>(smem + C::BARS + 256);        // 14 values
+  long long* sh = reinterpret_cast<long long*>(smem + C::BARS + 384);        // 14 values
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -182,12 +176,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
       mbar_init(&m_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&q_full[i], 4);
+      mbar_init(&q_full[i], 8);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&p_full[i], 8);
       mbar_init(&o_done[i], 1);
-      mbar_init(&o_free[i], 4);
+      mbar_init(&o_free[i], 8);
     }
+    for (int i = 0; i < 8; ++i) mbar_init(&told[i], 2);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -260,8 +255,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
               const uint64_t vd = v_desc + (uint64_t)(vslot * (C::MAT / 16));
 #pragma unroll
               for (int kk = 0; kk < 8; ++kk)                         // 16 keys: 16 rows of 128 bytes
-                umma_f16_ts(o_tm + D * x, s_tm + 128 * x + 8 * kk, vd + kk * 128, IDO, i > 1 || kk > 0, leader);
-              commit_by(&o_done[x], leader);
+                umma_f16_ts(o_tm + D * x, s_tm + 128 * x + 8 * kk + 32 * (kk >> 2), vd + kk * 128, IDO, i > 1 || kk > 0, leader);
+              if (i == it.nt) commit_by(&o_done[x], leader);
               if (x == groups - 1) commit_by(&m_empty[vslot], leader);   // K(i + 1) is written there while S is computed
             }
             if (i < it.nt) {
@@ -343,12 +338,25 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
       }
     }
   } else {
-    // ---------------- softmax: a query row per thread, group x ----------------
+    // ---------------- softmax: half a query row per thread, group x ----------------
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_SOFT));
-    const int x = (warp - SOFT0) >> 2, r = tid - 32 * SOFT0 - 128 * x;          // this group's row
+    const int x = (warp - SOFT0) >> 3, half = (warp >> 2) & 1, r = 32 * (warp & 3) + lane;      // this group's row
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t st = s_tm + 128 * x + lanes, ot = o_tm + D * x + lanes;
-    uint32_t ns = 0, no = 0;                                         // tiles whose S, whose P V this group has waited for
+    const uint32_t st = s_tm + 128 * x + 64 * half + lanes, ot = o_tm + D * x + (D / 2) * half + lanes;
+    uint64_t* both = &told[4 * x + (warp & 3)];
+    const uint32_t mine = smem_u32(smem) + C::ROWS + 8 * (128 * x + r) + 4 * half, theirs = mine ^ 4u;
+    uint32_t nt = 0;                                                 // times the halves have told each other something
+    auto tell = [&](float v, float& w) {                             // v to the other half of the row, w from it
+      const uint32_t at = nt & 1u ? 2048u : 0u;
+      asm volatile("st.shared.f32 [%0], %1;" ::"r"(mine + at), "f"(v) : "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(both);
+      if (!mbar_wait_poll(both, nt & 1u, abort_flag)) return false;
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(w) : "r"(theirs + at) : "memory");
+      ++nt;
+      return true;
+    };
+    uint32_t ns = 0, no = 0;                                         // tiles whose S, items whose O this group has waited for
     int4 cut = make_int4(0, 0, 0, 0);
     while (ok && line.next(p, it, err)) {
       if (it.more) cut = make_int4(it.b, it.item, 1 + it.more, 0);
@@ -384,7 +392,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
         rowc = p.scale_log2 * pow2(-e);
         const uint32_t dst = smem_u32(smem) + x * C::MAT + r * 128;
 #pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
+        for (int c = half * (D / 16); c < (half + 1) * (D / 16); ++c) {
           uint4 w = make_uint4(0u, 0u, 0u, 0u);
           if (row_ok) w = *reinterpret_cast<const uint4*>(qp + 8 * c);
           float v[8];
@@ -399,45 +407,43 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
         if (lane == 0 && it.nt > 0) mbar_arrive(&q_full[x]);
       }
       float mrc = 0.0f, thr = -CUDART_INF_F, l = 0.0f;               // maximum in log2 units (0: none yet), its limit, the sum
-      uint32_t pending = 0;                                          // P V of this item not waited for yet
       for (int i = 0; i < it.nt; ++i) {
         if (!mbar_wait_bounded(&s_full[x], ns & 1u, abort_flag)) { give_up(); break; }
         ++ns;
         tc_fence_after();
-        // The scores are read twice from tensor memory, 32 at a time, for the maximum and for the
-        // probabilities (128 of them in registers at once spilled: 430 instead of 250 us at 1024
-        // tokens over 8187 keys).
         const int key0 = (it.tl + i) * TILE;
+        // The scores are read twice from tensor memory, for the maximum and for the probabilities: all of
+        // them in registers at once spilled, and what is spilled does not stay in the little cache that
+        // the shared memory leaves.
         const bool masked = key0 < lo_max || key0 + TILE > hi_min;
-        const int u_lo = lo - key0, u_hi = hi - key0;                // columns the row sees
-        uint32_t s[2][32];
-        float m4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-        auto each = [&](auto&& f) {              // f(32 scores, first column): two chunks an iteration, the next one loading
-          tmem_ld32(st, s[0]);
-#pragma unroll 1
-          for (int c = 0; c < 128; c += 64) {
+        const int u_lo = lo - key0 - 64 * half, u_hi = hi - key0 - 64 * half;          // columns the row sees
+        uint32_t s[2][16];
+        auto each = [&](auto&& f) {              // f(16 scores, first column), the next ones loading
+          tmem_ld_32x32b_x16_nowait(st, s[0]);
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              tmem_ld_wait();
-              if (c + 32 * y < 96) tmem_ld32(st + c + 32 * (y + 1), s[1 - y]);
-              uint32_t* v = s[y];
-              if (masked) {
-                // bits of the columns that the row sees
-                const int a = u_lo - c - 32 * y, b = u_hi - c - 32 * y;
-                const uint32_t see = (a > 31 || b < 0) ? 0u : (a > 0 ? 0xFFFFFFFFu << a : 0xFFFFFFFFu) & (b < 31 ? 0xFFFFFFFFu >> (31 - b) : 0xFFFFFFFFu);
+          for (int c = 0; c < 64; c += 16) {
+            uint32_t* v = s[c / 16 & 1];
+            tmem_ld_wait<16>(v);
+            if (c < 48) tmem_ld_32x32b_x16_nowait(st + c + 16, s[1 - (c / 16 & 1)]);
+            if (masked) {
+              const int a = u_lo - c, b = u_hi - c;
+              const uint32_t see = (a > 15 || b < 0) ? 0u : (a > 0 ? 0xFFFFu << a : 0xFFFFu) & (b < 15 ? 0xFFFFu >> (15 - b) : 0xFFFFu);
 #pragma unroll
-                for (int k = 0; k < 32; ++k)
-                  if (!(see >> k & 1u)) v[k] = 0xFF800000u;          // -infinity
-              }
-              f(v, c + 32 * y);
+              for (int k = 0; k < 16; ++k)
+                if (!(see >> k & 1u)) v[k] = 0xFF800000u;            // -infinity
             }
+            f(v, c);
           }
         };
+        float m4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
         each([&](const uint32_t* v, int) {
 #pragma unroll
-          for (int k = 0; k < 32; k += 2) m4[k / 2 & 3] = max3(m4[k / 2 & 3], __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+          for (int k = 0; k < 16; k += 2) m4[k / 2 & 3] = max3(m4[k / 2 & 3], __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
         });
-        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * rowc;
+        const float mh = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
+        float mx;
+        if (!tell(mh, mx)) { give_up(); break; }
+        mx = fmaxf(mx, mh) * rowc;
         float f = 1.0f;
         const bool over = mx > thr;
         if (over) {
@@ -446,34 +452,25 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
           thr = mx + kSlack;
           l *= f;
         }
-        // O is this group's own; its last P V must be done before it is read or rescaled
+        // O is this group's own: the last P V was issued before this S, so it is done
         if (__any_sync(0xffffffffu, over) && i > 0) {
-          if (!mbar_wait_bounded(&o_done[x], no & 1u, abort_flag)) { give_up(); break; }
-          ++no;
-          pending = 0;
-          tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tmem_ld32(ot + c, o);
-            tmem_ld_wait();
+          for (int c = 0; c < D / 2; c += 8) {
+            uint32_t o[8];
+            tmem_ld8(ot + c, o);
+            tmem_ld_wait<8>(o);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-            tmem_st32(ot + c, o);
+            for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+            tmem_st8(ot + c, o);
           }
-        } else if (pending) {
-          // nothing to do to O: the barrier's phase is taken all the same, so that phases stay in step
-          if (!mbar_wait_bounded(&o_done[x], no & 1u, abort_flag)) { give_up(); break; }
-          ++no;
-          pending = 0;
         }
         const float b = kShift - mrc;
         const uint64_t b2 = pair(b, b), rowc2 = pair(rowc, rowc);
         uint64_t sum[2] = {0, 0};
         each([&](const uint32_t* v, int c) {
-          uint32_t pw[16];
+          uint32_t pw[8];
 #pragma unroll
-          for (int k = 0; k < 32; k += 2) {
+          for (int k = 0; k < 16; k += 2) {
             float e0, e1;
             halves(fma2(pair(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), rowc2, b2), e0, e1);
             e0 = ex2(e0);
@@ -481,7 +478,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
             sum[k / 2 & 1] = add2(sum[k / 2 & 1], pair(e0, e1));
             pw[k / 2] = pack_half2(e0, e1);
           }
-          tmem_st16(st + c / 2, pw);             // over columns that have been read: c / 2 + 16 <= c + 32
+          tmem_st8(st + c / 2, pw);              // over columns that have been read
         });
         float s0, s1;
         halves(add2(sum[0], sum[1]), s0, s1);
@@ -490,36 +487,39 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[x]);
-        pending = 1;
       }
       if (!ok) break;
       // ---- the item's output
       if (it.nt > 0) {
-        if (!mbar_wait_bounded(&o_done[x], no & 1u, abort_flag)) { give_up(); break; }
+        float lh;
+        if (!mbar_wait_bounded(&o_done[x], no & 1u, abort_flag) || !tell(l, lh)) { give_up(); break; }
         ++no;
+        l += lh;
         tc_fence_after();
       }
       const long long at = (it.sq.tok0 + tk) * p.ldo + (long long)hq * D;
       float* out = p.part + (2LL * blockIdx.x + (it.lead ? 0 : 1)) * C::PART;
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        uint32_t o[32];
+      for (int c = 0; c < D / 2; c += 16) {
+        uint32_t o[16];
         if (it.nt > 0) {
-          tmem_ld32(ot + c, o);
-          tmem_ld_wait();
+          tmem_ld8(ot + c, o);
+          tmem_ld8(ot + c + 8, o + 8);
+          tmem_ld_wait<16>(o);
         }
         __syncwarp();
 #pragma unroll
-        for (int k = 0; k < 32; k += 4) {
+        for (int k = 0; k < 16; k += 4) {
           if (!row_ok) break;
-          float4 v = make_float4(__uint_as_float(o[k]), __uint_as_float(o[k + 1]), __uint_as_float(o[k + 2]), __uint_as_float(o[k + 3]));
-          if (l == 0.0f) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);    // no key seen: O may never have been written
-          if (it.whole) store_out(p, at + c + k, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
-          else *reinterpret_cast<float4*>(out + (128 * x + r) * D + c + k) = v;
+          float4 w = make_float4(__uint_as_float(o[k]), __uint_as_float(o[k + 1]), __uint_as_float(o[k + 2]), __uint_as_float(o[k + 3]));
+          if (l == 0.0f) w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);    // no key seen: O may never have been written
+          const int col = half * (D / 2) + c + k;
+          if (it.whole) store_out(p, at + col, make_float4(w.x * inv, w.y * inv, w.z * inv, w.w * inv));
+          else *reinterpret_cast<float4*>(out + (128 * x + r) * D + col) = w;
         }
       }
-      if (row_ok) {
+      if (row_ok && half == 0) {
         if (it.whole) {
           if (p.lse) p.lse[(it.sq.tok0 + tk) * p.Hq + hq] = l == 0.0f ? -CUDART_INF_F : (mrc - kShift + log2f(l)) * 0.6931471805599453f;
         } else {
