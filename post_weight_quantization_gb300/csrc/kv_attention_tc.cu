@@ -31,7 +31,8 @@ namespace tc {
 
 constexpr int R = 256, DEQ0 = 4, NDEQ = 8, SOFT0 = DEQ0 + NDEQ, THREADS = (SOFT0 + 16) * 32;
 constexpr int kItemCost = 1;
-constexpr float kSlack = 4.0f;                  // a row's maximum may lag by 2^4 before it is moved
+constexpr int CH = 16;                          // scores a thread takes from tensor memory at once
+constexpr float kSlack = 7.0f;                  // a row's maximum may lag by 2^7 before it is moved: probabilities stay below 2^15
 constexpr float kShift = 8.0f;                  // probabilities are kept 2^kShift times too large
 constexpr int REG_ISSUE = 40, REG_DEQ = 56, REG_SOFT = 88;        // 128 x 40 + 256 x 56 + 512 x 88 = 896 x 72
 
@@ -97,6 +98,17 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(taddr));
 }
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
                "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
@@ -104,20 +116,24 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Eight codes of a word as four fp16 pairs code * scale + low, one rounding each: 0x6400 | c is
-// 1024 + c, less 1024 exactly c. 15 * scale + low can round past fp16's largest number: it is kept
-// at that number.
+// Eight codes of a word as four fp16 pairs code * scale + low, one rounding each. 0x6400 | c is
+// 1024 + c, less 1024 exactly c; codes in bits 4 to 7 come as 16 c. Pair i holds codes i and i + 4:
+// queries are laid out alike, and the output's columns are put back at its end.
 __device__ __forceinline__ uint4 dequant8(uint32_t w, __half2 scale, __half2 low) {
-  const uint32_t e = w & 0x0F0F0F0Fu, d = (w >> 4) & 0x0F0F0F0Fu;
   uint32_t o[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {                 // bytes i of both; a selector's top bit repeats a byte's sign bit: 0
-    const uint32_t c = prmt(e, d, (uint32_t)(i | ((8 + i) << 4) | ((4 + i) << 8) | ((12 + i) << 12))) | 0x64006400u;
-    __half2 x = __hfma2(__hsub2(*reinterpret_cast<const __half2*>(&c), __float2half2_rn(1024.0f)), scale, low);
-    x = __hmin2_nan(x, __float2half2_rn(65504.0f));
-    o[i] = *reinterpret_cast<const uint32_t*>(&x);
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t c = ((i < 2 ? w : w >> 8) & (i & 1 ? 0x00F000F0u : 0x000F000Fu)) | 0x64006400u;
+    const __half2 a = *reinterpret_cast<const __half2*>(&c);
+    const __half2 n = i & 1 ? __hfma2(a, __float2half2_rn(0.0625f), __float2half2_rn(-64.0f)) : __hsub2(a, __float2half2_rn(1024.0f));
+    const __half2 v = __hfma2(n, scale, low);
+    o[i] = *reinterpret_cast<const uint32_t*>(&v);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
+}
+__device__ __forceinline__ uint32_t at_most_65504(uint32_t v) {
+  const __half2 x = __hmin2_nan(*reinterpret_cast<const __half2*>(&v), __float2half2_rn(65504.0f));
+  return *reinterpret_cast<const uint32_t*>(&x);
 }
 
 // The larger of three; two fp32 values in one register pair, a multiply-add or a sum of both at once.
@@ -313,26 +329,28 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
             asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                          : "=r"(w[c]), "=r"(w[c + 1]), "=r"(w[c + 2]), "=r"(w[c + 3])
                          : "r"(base + off + kv * p.pb * (D / 2) + 4 * c));
-          if (kv == 1) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&c_empty[st]);
-          }
           if (!mbar_wait_bounded(&m_empty[slot], (mat / NM & 1u) ^ 1u, abort_flag)) { give_up(); break; }
           const uint32_t nn = kv ? num[1] : num[0];
           const __half2 s = __half2half2(__ushort_as_half((unsigned short)nn));
           const __half2 l = __half2half2(__ushort_as_half((unsigned short)(nn >> 16)));
+          // 15 * scale + low can round past fp16's largest number: such values are kept at that number
+          const bool past = __any_sync(0xffffffffu, fmaf(15.0f, __low2float(s), __low2float(l)) > 65504.0f);
           const uint32_t dst = sb + C::MATS + slot * C::MAT + r * 128;
 #pragma unroll
           for (int c = 0; c < NW; ++c) {
             const int cc = half * NW + c;                            // the row's 16-byte piece
-            const uint4 v = dequant8(w[c], s, l);
+            uint4 v = dequant8(w[c], s, l);
+            if (past) v = make_uint4(at_most_65504(v.x), at_most_65504(v.y), at_most_65504(v.z), at_most_65504(v.w));
             asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + (cc >> 3) * C::BOX + (((cc & 7) ^ sw) << 4)), "r"(v.x),
                          "r"(v.y), "r"(v.z), "r"(v.w)
                          : "memory");
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&m_full[slot]);
+          if (lane == 0) {
+            mbar_arrive(&m_full[slot]);
+            if (kv == 1) mbar_arrive(&c_empty[st]);
+          }
         }
         if (!ok) break;
       }
@@ -398,8 +416,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
           float v[8];
           if (p.q_f16) unpack8<F16>(&w, v); else unpack8<BF16>(&w, v);
           asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + (c >> 3) * C::BOX + (((c & 7) ^ (r & 7)) << 4)),
-                       "r"(pack_half2(v[0] * f, v[1] * f)), "r"(pack_half2(v[2] * f, v[3] * f)), "r"(pack_half2(v[4] * f, v[5] * f)),
-                       "r"(pack_half2(v[6] * f, v[7] * f))
+                       "r"(pack_half2(v[0] * f, v[4] * f)), "r"(pack_half2(v[1] * f, v[5] * f)), "r"(pack_half2(v[2] * f, v[6] * f)),
+                       "r"(pack_half2(v[3] * f, v[7] * f))
                        : "memory");
         }
         fence_proxy_async_smem();
@@ -412,77 +430,75 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
         ++ns;
         tc_fence_after();
         const int key0 = (it.tl + i) * TILE;
-        // The scores are read twice from tensor memory, for the maximum and for the probabilities: all of
-        // them in registers at once spilled, and what is spilled does not stay in the little cache that
-        // the shared memory leaves.
         const bool masked = key0 < lo_max || key0 + TILE > hi_min;
         const int u_lo = lo - key0 - 64 * half, u_hi = hi - key0 - 64 * half;          // columns the row sees
-        uint32_t s[2][16];
-        auto each = [&](auto&& f) {              // f(16 scores, first column), the next ones loading
+        // One pass computes the probabilities from the maximum so far and this tile's maximum. Only
+        // where that is more than 2^kSlack above (an item's first tile, seldom later) the row moves
+        // its maximum and the pass is done again.
+        uint32_t pw[32];
+        float s0, s1;
+#pragma unroll 1
+        for (;;) {
+          const float b = kShift - mrc;
+          const uint64_t b2 = pair(b, b), rowc2 = pair(rowc, rowc);
+          uint64_t sum[2] = {0, 0};
+          float m4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+          uint32_t s[2][CH];
           tmem_ld_32x32b_x16_nowait(st, s[0]);
 #pragma unroll
-          for (int c = 0; c < 64; c += 16) {
-            uint32_t* v = s[c / 16 & 1];
-            tmem_ld_wait<16>(v);
-            if (c < 48) tmem_ld_32x32b_x16_nowait(st + c + 16, s[1 - (c / 16 & 1)]);
+          for (int c = 0; c < 64; c += CH) {
+            uint32_t* v = s[c / CH & 1];
+            tmem_ld_wait<CH>(v);
+            if (c + CH < 64) tmem_ld_32x32b_x16_nowait(st + c + CH, s[1 - (c / CH & 1)]);
             if (masked) {
-              const int a = u_lo - c, b = u_hi - c;
-              const uint32_t see = (a > 15 || b < 0) ? 0u : (a > 0 ? 0xFFFFu << a : 0xFFFFu) & (b < 15 ? 0xFFFFu >> (15 - b) : 0xFFFFu);
+              const int a = u_lo - c, z = u_hi - c;
+              constexpr uint32_t all = (1u << CH) - 1u;
+              const uint32_t see = (a >= CH || z < 0) ? 0u : (a > 0 ? all << a : all) & (z < CH - 1 ? all >> (CH - 1 - z) : all);
 #pragma unroll
-              for (int k = 0; k < 16; ++k)
+              for (int k = 0; k < CH; ++k)
                 if (!(see >> k & 1u)) v[k] = 0xFF800000u;            // -infinity
             }
-            f(v, c);
-          }
-        };
-        float m4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-        each([&](const uint32_t* v, int) {
 #pragma unroll
-          for (int k = 0; k < 16; k += 2) m4[k / 2 & 3] = max3(m4[k / 2 & 3], __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
-        });
-        const float mh = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
-        float mx;
-        if (!tell(mh, mx)) { give_up(); break; }
-        mx = fmaxf(mx, mh) * rowc;
-        float f = 1.0f;
-        const bool over = mx > thr;
-        if (over) {
-          f = thr == -CUDART_INF_F ? 0.0f : ex2(mrc - mx);
-          mrc = mx;
-          thr = mx + kSlack;
-          l *= f;
-        }
-        // O is this group's own: the last P V was issued before this S, so it is done
-        if (__any_sync(0xffffffffu, over) && i > 0) {
+            for (int k = 0; k < CH; k += 2) {
+              m4[k / 2 & 3] = max3(m4[k / 2 & 3], __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+              float e0, e1;
+              halves(fma2(pair(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), rowc2, b2), e0, e1);
+              e0 = ex2(e0);
+              e1 = ex2(e1);
+              sum[k / 2 & 1] = add2(sum[k / 2 & 1], pair(e0, e1));
+              pw[(c + k) / 2] = pack_half2(e0, e1);
+            }
+          }
+          halves(add2(sum[0], sum[1]), s0, s1);
+          const float mh = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
+          float mx;
+          if (!tell(mh, mx)) { ok = false; break; }
+          mx = fmaxf(mx, mh) * rowc;
+          const bool over = mx > thr;
+          if (!__any_sync(0xffffffffu, over)) break;
+          float f = 1.0f;
+          if (over) {
+            f = thr == -CUDART_INF_F ? 0.0f : ex2(mrc - mx);
+            mrc = mx;
+            thr = mx + kSlack;
+            l *= f;
+          }
+          if (i > 0) {
+            // O is this group's own: the last P V was issued before this S, so it is done
 #pragma unroll 1
-          for (int c = 0; c < D / 2; c += 8) {
-            uint32_t o[8];
-            tmem_ld8(ot + c, o);
-            tmem_ld_wait<8>(o);
+            for (int c = 0; c < D / 2; c += 8) {
+              uint32_t o[8];
+              tmem_ld8(ot + c, o);
+              tmem_ld_wait<8>(o);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-            tmem_st8(ot + c, o);
+              for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tmem_st8(ot + c, o);
+            }
           }
         }
-        const float b = kShift - mrc;
-        const uint64_t b2 = pair(b, b), rowc2 = pair(rowc, rowc);
-        uint64_t sum[2] = {0, 0};
-        each([&](const uint32_t* v, int c) {
-          uint32_t pw[8];
-#pragma unroll
-          for (int k = 0; k < 16; k += 2) {
-            float e0, e1;
-            halves(fma2(pair(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), rowc2, b2), e0, e1);
-            e0 = ex2(e0);
-            e1 = ex2(e1);
-            sum[k / 2 & 1] = add2(sum[k / 2 & 1], pair(e0, e1));
-            pw[k / 2] = pack_half2(e0, e1);
-          }
-          tmem_st8(st + c / 2, pw);              // over columns that have been read
-        });
-        float s0, s1;
-        halves(add2(sum[0], sum[1]), s0, s1);
+        if (!ok) { give_up(); break; }
         l += s0 + s1;
+        tmem_st32(st, pw);                       // over this half's own scores
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -512,7 +528,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
 #pragma unroll
         for (int k = 0; k < 16; k += 4) {
           if (!row_ok) break;
-          float4 w = make_float4(__uint_as_float(o[k]), __uint_as_float(o[k + 1]), __uint_as_float(o[k + 2]), __uint_as_float(o[k + 3]));
+          const int e = (k & ~7) + (k >> 2 & 1);                     // column j of eight lies at 2 (j mod 4) + j / 4
+          float4 w = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 2]), __uint_as_float(o[e + 4]), __uint_as_float(o[e + 6]));
           if (l == 0.0f) w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);    // no key seen: O may never have been written
           const int col = half * (D / 2) + c + k;
           if (it.whole) store_out(p, at + col, make_float4(w.x * inv, w.y * inv, w.z * inv, w.w * inv));
