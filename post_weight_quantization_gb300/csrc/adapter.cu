@@ -703,6 +703,10 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
           const uint32_t sc = smem_u32(codes) + st * C::C_BYTES;
 #pragma unroll
           for (int i = 0; i < BITS; ++i) lds_piece<BITS>(sc, row_l, i, w + 4 * i);
+          // without the fence the next copy could overwrite words that a lane's load had not read yet
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&c_empty[st]);
         } else {
 #pragma unroll
           for (int c = 0; c < 4; ++c)
@@ -722,8 +726,6 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
           }
         }
         publish();
-        // Only now: released straight after the loads, the stage could be overwritten before they had read it.
-        if (p.codes_tma && lane == 0) mbar_arrive(&c_empty[(cb0 + (uint32_t)(b - blk0)) % SLOTS]);
       }
       cb0 += (uint32_t)(blk1 - blk0);
       ab = ab0 + (uint32_t)(blk1 - blk0);

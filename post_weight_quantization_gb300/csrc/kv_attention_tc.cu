@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(&m_full[slot]);
-            if (kv == 1) mbar_arrive(&c_empty[st]);
+            if (kv == 1) mbar_arrive(&c_empty[st]);      // here its words have been read: loads alone may still be on their way
           }
         }
         if (!ok) break;
