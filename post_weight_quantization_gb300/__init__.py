@@ -7,10 +7,10 @@ built library raises ImportError: there is no CPU fallback.
 """
 import importlib
 
-__all__ = ["gptq", "build"]
+__all__ = ["gptq", "build", "decoder"]
 
 
 def __getattr__(name):
-    if name in ("gptq", "build"):
+    if name in ("gptq", "build", "decoder"):
         return importlib.import_module(f"{__name__}.{name}")
     raise AttributeError(name)

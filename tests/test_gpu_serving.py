@@ -521,3 +521,21 @@ def test_serving_on_another_stream(g):
     O = g.gptq_kv_attention(cache, late, cu, lens, table, 1, stream=s)
     s.synchronize()
     t.check(O)
+
+
+@pytest.mark.parametrize("hq,h,D,page", [(8, 2, 128, 64), (16, 2, 64, 32)])
+def test_attention_piece_with_cold_caches(g, hq, h, D, page):
+    """The same call with everything evicted in between gives the same bits: what a warp reads of a
+    tile is read before the next tile takes its place, however late the warp comes."""
+    t = Batch([331, 140], [150, 140], hq, h, D, page, torch.bfloat16, seed=7 * D)
+    args = t.gpu(g)
+    evict = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    want = None
+    for i in range(40):
+        evict.fill_(i)
+        O = g.gptq_kv_attention(*args, 150)
+        if want is None:
+            want = O
+        assert torch.equal(O, want), i
+    done(g)
+    t.check(want, heads=(0, hq - 1))
