@@ -34,9 +34,9 @@ class Batch:
         self.free += self.tables[b][::-1]
         self.lens[b], self.tables[b] = 0, []
 
-    def extend(self, new: List[int]) -> "Step":
-        """Places for new[b] more tokens of each sequence b. Raises MemoryError, with nothing changed,
-        when there are not enough free pages."""
+    def extend(self, new: List[int], width: int = 0) -> "Step":
+        """Places for new[b] more tokens of each sequence b; the table of pages has at least `width`
+        columns. Raises MemoryError, with nothing changed, when there are not enough free pages."""
         if len(new) != len(self.lens) or min(new, default=0) < 0:
             raise ValueError(f"one count per sequence, none negative: {len(self.lens)} sequences, got {new}")
         p = self.page_size
@@ -51,24 +51,31 @@ class Batch:
             slots += [self.tables[b][j // p] * p + j % p for j in places]
             self.lens[b] += k
             cu.append(cu[-1] + k)
-        width = max([len(t) for t in self.tables] + [1])
+        width = max([len(t) for t in self.tables] + [1, width])
         table = [t + [0] * (width - len(t)) for t in self.tables]
         # one copy for the 32-bit numbers of a step
         ints = torch.tensor(positions + cu + self.lens + sum(table, []), dtype=torch.int32).to(self.device)
-        positions, cu_q, kv_lens, table = ints.split([len(positions), len(cu), len(new), len(new) * width])
-        return Step(torch.tensor(slots, dtype=torch.int64).to(self.device), positions, cu_q, kv_lens,
-                    table.view(len(new), width), max(new, default=0))
+        return Step(torch.tensor(slots, dtype=torch.int64).to(self.device), ints, len(new), max(new, default=0))
 
 
-@dataclass
 class Step:
-    """What a step's operators read beside the tokens (device tensors, and the longest count)."""
-    slots: torch.Tensor          # (T,) int64: the new tokens' places in the cache
-    positions: torch.Tensor      # (T,) int32
-    cu_q: torch.Tensor           # (batch + 1,) int32
-    kv_lens: torch.Tensor        # (batch,) int32, the new tokens included
-    block_table: torch.Tensor    # (batch, pages) int32
-    max_q: int
+    """What a step's operators read beside the tokens: slots (T,) int64, the new tokens' places in the
+    cache; positions (T,), cu_q (batch + 1,), kv_lens (batch,), the new tokens included, and
+    block_table (batch, pages), all int32; max_q, the most new tokens of a sequence."""
+
+    def __init__(self, slots: torch.Tensor, ints: torch.Tensor, batch: int, max_q: int):
+        T = slots.shape[0]
+        self.slots, self.ints, self.max_q = slots, ints, max_q
+        self.positions, self.cu_q, self.kv_lens, table = ints.split([T, batch + 1, batch, ints.shape[0] - T - 2 * batch - 1])
+        self.block_table = table.view(batch, table.shape[0] // max(batch, 1))
+
+    def copy_(self, other: "Step") -> "Step":
+        """Take over a step of the same shape in place, for a captured graph that reads this one."""
+        if (self.max_q, self.block_table.shape) != (other.max_q, other.block_table.shape):
+            raise ValueError("the steps have different shapes")
+        self.slots.copy_(other.slots)
+        self.ints.copy_(other.ints)
+        return self
 
 
 @dataclass
@@ -160,15 +167,30 @@ def main() -> None:
     print(f"prompts {lens}: {start.elapsed_time(end) * 1e3:.0f} us, mean |y| {Y.float().abs().mean().item():.4f}")
     last = (step.cu_q[1:] - 1).long()
     X = Y[last]
-    plans = [batch.extend([1] * len(lens)) for _ in range(steps)]
+    width = len(batch.free) // len(lens)
+    plans = [batch.extend([1] * len(lens), width) for _ in range(2 * steps)]
     torch.cuda.synchronize()
     start.record()
-    for plan in plans:
+    for plan in plans[:steps]:
         X = block.forward(X, plan, which)
     end.record()
     torch.cuda.synchronize()
+    calls = start.elapsed_time(end) * 1e3 / steps
+    # the same as one captured graph, whose tokens, places and lengths are copied into it
+    at = plans[steps]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        Y = block.forward(X, at, which)
+    start.record()
+    for plan in plans[steps:]:
+        at.copy_(plan)
+        graph.replay()
+        X.copy_(Y)
+    end.record()
+    torch.cuda.synchronize()
+    replays = start.elapsed_time(end) * 1e3 / steps
     gptq.gptq_device_check()
-    print(f"{steps} tokens of each sequence, one by one: {start.elapsed_time(end) * 1e3 / steps:.0f} us a step, "
+    print(f"{2 * steps} tokens of each sequence, one by one: {calls:.0f} us a step by calls, {replays:.0f} us by a graph, "
           f"mean |y| {X.float().abs().mean().item():.4f}")
 
 

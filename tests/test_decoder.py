@@ -122,6 +122,36 @@ def test_block_prompts_then_tokens(dec, hidden, heads, kv_heads, dim, page, wind
 
 
 @pytest.mark.gpu
+def test_block_in_a_graph(dec):
+    """Single tokens through a captured graph: the bits of the calls, step after step."""
+    block = dec.random_block(256, 8, 2, 64, num_pages=24, page_size=16, positions=100, adapters=2, rank=8)
+    which = torch.tensor([1, -1, 0], dtype=torch.int32).cuda()
+    gen = torch.Generator().manual_seed(2)
+    prompt = torch.randn((60, 256), generator=gen).bfloat16().cuda()
+    tokens = [torch.randn((3, 256), generator=gen).bfloat16().cuda() for _ in range(20)]
+    def start():
+        batch = dec.Batch(24, 16)
+        for _ in which:
+            batch.add()
+        step = batch.extend([40, 17, 3])
+        block.forward(prompt, step, torch.repeat_interleave(which, torch.tensor([40, 17, 3]).cuda()))
+        return [batch.extend([1, 1, 1], 6) for _ in tokens]
+    want = [block.forward(X, step, which) for X, step in zip(tokens, start())]
+    steps = start()
+    X, at = tokens[0].clone(), dec.Step(steps[0].slots.clone(), steps[0].ints.clone(), 3, 1)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        Y = block.forward(X, at, which)
+    for x, step, ref in zip(tokens, steps, want):
+        X.copy_(x)
+        at.copy_(step)
+        graph.replay()
+        assert torch.equal(Y, ref)
+    with pytest.raises(ValueError):
+        at.copy_(dec.Step(at.slots, at.ints, 3, 2))
+
+
+@pytest.mark.gpu
 def test_example_runs(dec, capsys):
     dec.main()
     out = capsys.readouterr().out
