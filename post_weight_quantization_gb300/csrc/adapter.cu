@@ -137,16 +137,17 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Many tokens: a CTA per 16 tokens, its warps over d; for each adapter among the tokens NT groups
+// Many tokens: a cluster per 16 tokens, its CTAs' warps over d; for each adapter among the tokens NT groups
 // of eight of its rows at a time on mma.sync, so neighbours that share an adapter share the
-// reads of its rows. A batch of UN 32-column blocks is loaded before the first is multiplied.
+// reads of its rows. A batch of UN 32-column blocks is loaded before the first is multiplied. The
+// CTAs add up each other's sums, each a share of them, in a fixed order.
 template <int NT>
 __global__ void __launch_bounds__(SH_WARPS * 32) adapter_shrink_kernel(ShrinkParams p, int* __restrict__ err) {
   constexpr int UN = 4;
-  __shared__ float red[SH_WARPS][SH_TOK][8 * NT + 1];
+  __shared__ float red[SH_WARPS][SH_TOK][8 * NT + 1], sums[SH_TOK * 8 * NT];
   grid_dep_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int t0 = blockIdx.x * SH_TOK;
+  const int t0 = blockIdx.y * SH_TOK, part = blockIdx.x, parts = gridDim.x;
   int id = -1;
   if (lane < SH_TOK && t0 + lane < p.T) {
     id = p.ids[t0 + lane];
@@ -158,7 +159,8 @@ __global__ void __launch_bounds__(SH_WARPS * 32) adapter_shrink_kernel(ShrinkPar
   const int ida = __shfl_sync(0xffffffffu, id, g), idb = __shfl_sync(0xffffffffu, id, g + 8);
   // lane (g, t) holds columns 8 t ... 8 t + 7 of a block: two MMAs' k in a fixed order, the
   // same for both operands. Tokens past the end repeat the last one.
-  const int nb = p.d / 32, b0 = nb * warp / SH_WARPS, b1 = nb * (warp + 1) / SH_WARPS;   // this warp's blocks
+  const int nb = p.d / 32, w0 = SH_WARPS * part + warp, nw = SH_WARPS * parts;
+  const int b0 = (int)((long long)nb * w0 / nw), b1 = (int)((long long)nb * (w0 + 1) / nw);     // this warp's blocks
   const uint16_t* xa = p.X + (long long)min(t0 + g, p.T - 1) * p.ldx + 8 * t;
   const uint16_t* xb = p.X + (long long)min(t0 + g + 8, p.T - 1) * p.ldx + 8 * t;
   for (int r0 = 0; r0 < p.rank; r0 += 8 * NT) {
@@ -225,6 +227,15 @@ __global__ void __launch_bounds__(SH_WARPS * 32) adapter_shrink_kernel(ShrinkPar
       float s = 0.0f;
 #pragma unroll
       for (int w = 0; w < SH_WARPS; ++w) s += red[w][i][r];
+      sums[x] = s;
+    }
+    if (parts > 1) cluster_sync();
+    for (int x = SH_WARPS * 32 * part + threadIdx.x; x < SH_TOK * nr; x += SH_WARPS * 32 * parts) {
+      const int i = x / nr, r = x - i * nr;
+      float s = 0.0f;
+      if (parts == 1) s = sums[x];
+      else
+        for (int k = 0; k < parts; ++k) s += ld_cluster(smem_u32(&sums[x]), (uint32_t)k);
       if (t0 + i < p.T && p.part) {
         p.part[(long long)(t0 + i) * p.rank + r0 + r] = s;
       } else if (t0 + i < p.T) {
@@ -233,7 +244,8 @@ __global__ void __launch_bounds__(SH_WARPS * 32) adapter_shrink_kernel(ShrinkPar
         p.hl[(long long)(t0 + i) * (2 * p.rank) + p.rank + r0 + r] = __float2bfloat16_rn(s - __bfloat162float(h));
       }
     }
-    __syncthreads();
+    if (parts > 1) cluster_sync();                         // also: nobody leaves while its sums are read
+    else __syncthreads();
   }
 }
 
@@ -983,8 +995,10 @@ bool make_code_map(CUtensorMap* m, const void* base, long long rows, long long r
 
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// How a call of T tokens is cut. Tiles of 256 tokens where they give at least half the SMs one
-// each; else tiles of up to 64 tokens with clusters that split d so that about every SM has a CTA.
+// How a call of T tokens is cut. Tiles of up to 64 tokens while every SM has at most one, with
+// clusters that split d so that about every SM has a CTA; above that tiles of 256 tokens. (Measured
+// at 4 bits, d = 8192, m = 8192, in us, 64 / 256: 192 tokens 92 / 76, 512 tokens 172 / 80; m = 4096, d = 4096, 768
+// tokens 90 / 49.)
 struct Plan {
   int N, mt, nt, S, splits;
 };
@@ -992,20 +1006,31 @@ Plan plan_of(long long m, long long d, long long T) {
   Plan p;
   const int sms = sm_count();
   p.mt = (int)((m + BM - 1) / BM);
-  const long long tiles = (long long)p.mt * ((T + 255) / 256);
   p.S = 1;
   p.splits = 1;
-  if (T > 64 && 2 * tiles >= sms) {
+  if (T > 64 && p.mt * ((T + 63) / 64) > sms) {
     p.N = 256;
   } else {
     p.N = T <= 16 ? 16 : (T <= 32 ? 32 : 64);
     const long long few = (long long)p.mt * ((T + p.N - 1) / p.N);
     while (p.S < 8 && 2 * p.S * few <= sms && 2 * p.S * KB <= d) p.S *= 2;
-    // slices of d for U, a cluster's CTAs: at least 256 columns, while there are few CTAs
-    if (T <= SH_FEW)
-      while (p.splits < 8 && p.splits * 512 <= d && T * p.splits < 2 * sms) p.splits *= 2;
   }
   p.nt = (int)((T + p.N - 1) / p.N);
+  // slices of d for U, a cluster's CTAs, of at least 256 columns each
+  if (T <= SH_FEW) {
+    while (p.splits < 8 && p.splits * 512 <= d && T * p.splits < 2 * sms) p.splits *= 2;
+  } else {
+    // U's CTAs on SMs that the product leaves free run beside it; on the others they hold it up. So
+    // as many slices as fit there when they are done before the product (a slice of U takes about
+    // as long as a tile of 64 tokens over as many columns), else as many as make U itself quick.
+    // Measured at 4 bits, d = 8192, rank 16, in us, free SMs only / all: m = 8192, 128 tokens 47 / 53, 384
+    // tokens 74 / 82; m = 1024, 192 tokens 25 / 29. Too few are free: m = 1024, 256 tokens 49 / 29,
+    // 1024 tokens 72 / 55; m = 8192, 1024 tokens 156 / 139.
+    const long long groups = (T + SH_TOK - 1) / SH_TOK, room = sms - (long long)p.mt * p.nt * p.S;
+    while (p.splits < 8 && p.splits * 512 <= d && 2 * p.splits * groups <= room) p.splits *= 2;
+    if (groups > room || p.splits < p.S)
+      while (p.splits < 8 && p.splits * 512 <= d && 2 * p.splits * groups <= 4 * sms) p.splits *= 2;
+  }
   return p;
 }
 
@@ -1083,23 +1108,20 @@ gptq_status adapter_linear_launch(const uint32_t* qweight, const float* scales, 
     q.T = (int)T; q.d = (int)d; q.rank = rank; q.splits = pl.splits;
     if (pl.N == 256) q.hl = reinterpret_cast<__nv_bfloat16*>(ws);
     else q.part = reinterpret_cast<float*>(ws);
-    const unsigned grid = (unsigned)((T + SH_TOK - 1) / SH_TOK);
-    if (T <= SH_FEW) {
-      cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3((unsigned)pl.splits, (unsigned)T);
-      cfg.blockDim = dim3(SH_WARPS * 32);
-      cfg.stream = s;
-      cudaLaunchAttribute attr[1];
-      attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim.x = (unsigned)pl.splits;
-      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-      cfg.attrs = attr;
-      cfg.numAttrs = 1;
-      cudaLaunchKernelEx(&cfg, adapter_shrink_few_kernel, q, device_error_word());
-    }
-    else if (rank == 8) adapter_shrink_kernel<1><<<grid, SH_WARPS * 32, 0, s>>>(q, device_error_word());
-    else if (rank == 16) adapter_shrink_kernel<2><<<grid, SH_WARPS * 32, 0, s>>>(q, device_error_word());
-    else adapter_shrink_kernel<4><<<grid, SH_WARPS * 32, 0, s>>>(q, device_error_word());
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)pl.splits, (unsigned)(T <= SH_FEW ? T : (T + SH_TOK - 1) / SH_TOK));
+    cfg.blockDim = dim3(SH_WARPS * 32);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)pl.splits;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (T <= SH_FEW) cudaLaunchKernelEx(&cfg, adapter_shrink_few_kernel, q, device_error_word());
+    else if (rank == 8) cudaLaunchKernelEx(&cfg, adapter_shrink_kernel<1>, q, device_error_word());
+    else if (rank == 16) cudaLaunchKernelEx(&cfg, adapter_shrink_kernel<2>, q, device_error_word());
+    else cudaLaunchKernelEx(&cfg, adapter_shrink_kernel<4>, q, device_error_word());
     count_launch();
     if (gptq_status st = check_launch("adapter_shrink_kernel")) return st;
   }
