@@ -28,9 +28,9 @@
 //   warps 4 ...  unpack: sets of four (a warp per 32 tensor-memory lanes), 128-column blocks in turn
 //   last eight   epilogue: per unit N / 2 accumulators a thread
 //
-// Few tokens (N <= 64): a cluster of CTAs splits d for one tile, and the members sum their parts
+// Up to 256 tokens (N <= 64): a cluster of CTAs splits d for one tile, and the members sum their parts
 // from each other's shared memory, each a share of the rows, adding B[a] U there (one dot
-// product of `rank` values per output). Many tokens (N = 128): a persistent CTA per SM; the
+// product of `rank` values per output). Many tokens (N = 256): a persistent CTA per SM; the
 // adapters are further units of the same product, A = B[a]'s rows, B = U as two bf16 parts
 // (high and low, so the sum keeps 16 bits of U), one unit per run of tokens with one adapter,
 // which the epilogue adds to that run's columns only.
@@ -50,7 +50,10 @@ namespace adp {
 // ---------------------------------------------------------------------------------
 // U = alpha A X
 constexpr int SH_WARPS = 8, SH_TOK = 16;
-constexpr int SH_FEW = 64;                               // tokens up to which each reads its adapter by itself
+// Tokens up to which each reads its adapter by itself: the other kernel reads an adapter once for up to
+// 16 tokens that share it, but a group's adapters one after another. m = d = 8192, 128 tokens, the whole
+// call, in us: 64 adapters in any order 61 / 227, sorted 66 / 170, 4 adapters sorted 59 / 47.
+constexpr int SH_FEW = 256;
 
 struct ShrinkParams {
   const uint16_t* X;
@@ -995,10 +998,13 @@ bool make_code_map(CUtensorMap* m, const void* base, long long rows, long long r
 
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// How a call of T tokens is cut. Tiles of up to 64 tokens while every SM has at most one, with
-// clusters that split d so that about every SM has a CTA; above that tiles of 256 tokens. (Measured
-// at 4 bits, d = 8192, m = 8192, in us, 64 / 256: 192 tokens 92 / 76, 512 tokens 172 / 80; m = 4096, d = 4096, 768
-// tokens 90 / 49.)
+// How a call of T tokens is cut. Up to 256 tokens: tiles of up to 64, with clusters that split d so
+// that about every SM has a CTA. More: tiles of 256 once there are more tiles of 64 than SMs.
+// Measured at 4 bits, in us, 64 / 256: m = d = 8192, 512 tokens 172 / 80; m = d = 4096, 768 tokens 90 / 49.
+// In tiles of 256 every run of tokens with one adapter is a unit of the product: for prompts a few, for
+// a decoding batch up to one per token. So up to 256 tokens, which may be such a batch, stay with tiles
+// of 64: of 64 adapters in any order, m = d = 8192, 256 tokens take 104 / 575 (sorted, of 4: 102 / 78). (512
+// tokens of 64 adapters in any order take 597, sorted 160: the caller of long batches sorts them.)
 struct Plan {
   int N, mt, nt, S, splits;
 };
@@ -1008,7 +1014,7 @@ Plan plan_of(long long m, long long d, long long T) {
   p.mt = (int)((m + BM - 1) / BM);
   p.S = 1;
   p.splits = 1;
-  if (T > 64 && p.mt * ((T + 63) / 64) > sms) {
+  if (T > 256 && p.mt * ((T + 63) / 64) > sms) {
     p.N = 256;
   } else {
     p.N = T <= 16 ? 16 : (T <= 32 ? 32 : 64);
@@ -1023,9 +1029,9 @@ Plan plan_of(long long m, long long d, long long T) {
     // U's CTAs on SMs that the product leaves free run beside it; on the others they hold it up. So
     // as many slices as fit there when they are done before the product (a slice of U takes about
     // as long as a tile of 64 tokens over as many columns), else as many as make U itself quick.
-    // Measured at 4 bits, d = 8192, rank 16, in us, free SMs only / all: m = 8192, 128 tokens 47 / 53, 384
-    // tokens 74 / 82; m = 1024, 192 tokens 25 / 29. Too few are free: m = 1024, 256 tokens 49 / 29,
-    // 1024 tokens 72 / 55; m = 8192, 1024 tokens 156 / 139.
+    // Measured at 4 bits, d = 8192, rank 16, in us, free SMs only / all: m = 8192, 384 tokens 74 / 82;
+    // m = 1024, 768 tokens 47 / 53. Too few are free: m = 1024, 1024 tokens 72 / 55; m = 8192, 1024 tokens
+    // 156 / 139.
     const long long groups = (T + SH_TOK - 1) / SH_TOK, room = sms - (long long)p.mt * p.nt * p.S;
     while (p.splits < 8 && p.splits * 512 <= d && 2 * p.splits * groups <= room) p.splits *= 2;
     if (groups > room || p.splits < p.S)
