@@ -95,6 +95,11 @@ def _load() -> ctypes.CDLL:
 
 
 _lib = _load()
+try:
+    from . import serving_calls as _calls
+except ImportError as e:
+    raise ImportError("serving_calls.so is missing or does not fit this torch: build it with "
+                      "`python -m post_weight_quantization_gb300.build`") from e
 
 
 def library() -> ctypes.CDLL:
@@ -430,9 +435,11 @@ def gptq_gemm_f32(A: torch.Tensor, B: torch.Tensor, C: torch.Tensor, a_kmajor: b
 _DTYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _ALL = tuple(_DTYPE)
 
-# These calls are made for every token of a decoding loop, so their checks cost as little as
-# they can: the common case by attribute comparisons, the full check (which says what is
-# wrong) only where one of them fails.
+# These calls are made for every token of a decoding loop. The common case (everything right, on
+# the current device and stream) is checked, allocated and launched by the module of
+# csrc/serving_calls.cpp, which declines (None) anything else; then the checks below say what is
+# wrong, or allow what is unusual. Measured for 33 tokens of gptq_qk_norm_rope on the host: 18 us
+# this way, 5 us by the module.
 
 
 def _dense(t, name: str, shape, dtype) -> None:
@@ -483,6 +490,11 @@ def gptq_adapter_linear(q: "QuantizedLayer", X: torch.Tensor, m: int, A: Optiona
     adapter), from the packed layer q and bf16 tokens X (T x d). A: (n, rank, d), B: (n, m,
     rank) bf16, ids: (T,) int32, alpha: (n,) float32 or None for 1. fp32 output, or bf16 with
     out_bf16. Without A, B and ids it is the packed layer alone."""
+    if stream is None:
+        got = _calls.adapter_linear(q.qweight, q.scales, q.zeros, q.d, q.bits, q.group_size, X, m, A, B, ids, alpha, Y,
+                                    out_bf16, ws)
+        if got is not None:
+            return got
     _need_cuda(X, "X", (torch.bfloat16, torch.int16))
     d, bits, gs = q.d, q.bits, q.group_size
     if X.dim() != 2 or X.shape[1] != d or X.stride(1) != 1:
@@ -545,6 +557,10 @@ def gptq_qk_norm_rope(Q: torch.Tensor, K: Optional[torch.Tensor], positions: Opt
     None for no rotation), in one pass. Q, K: (T, heads, head_dim) float32, bfloat16 or
     float16; K may be None. Returns (Q_out, K_out) of out_dtype (default: Q's type); Q_out and
     K_out may be Q and K themselves."""
+    if stream is None:
+        got = _calls.qk_norm_rope(Q, K, positions, cos, sin, wq, wk, eps, interleaved, Q_out, K_out, out_dtype)
+        if got is not None:
+            return got
     ldq = _heads(Q, "Q", _ALL)
     T, hq, dim = Q.shape
     dtype, dev = Q.dtype, Q.device
@@ -617,6 +633,8 @@ class KVCache:
 def gptq_kv_append(cache: KVCache, K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
     """Quantize K and V rows (T, n_kv_heads, head_dim; float32, bfloat16 or float16) to 4 bits
     into the cache at slots (T,) int64 = page * page_size + place; negative slots are skipped."""
+    if stream is None and _calls.kv_append(cache.pool, cache.page_size, cache.n_kv_heads, cache.head_dim, K, V, slots):
+        return
     pages, pool, h, dim = cache.check(), cache.pool, cache.n_kv_heads, cache.head_dim
     ldk = _heads(K, "K", _ALL, -1, h, dim)
     T, dtype = K.shape[0], K.dtype
@@ -633,6 +651,10 @@ def gptq_kv_read(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torch
                  K: Optional[torch.Tensor] = None, V: Optional[torch.Tensor] = None, stream=None):
     """The cached values at slots (T,) int64 as (K, V), each (T, n_kv_heads, head_dim) of
     dtype; zeros for negative slots."""
+    if stream is None:
+        got = _calls.kv_read(cache.pool, cache.page_size, cache.n_kv_heads, cache.head_dim, slots, dtype, K, V)
+        if got is not None:
+            return got
     pages, pool, h, dim = cache.check(), cache.pool, cache.n_kv_heads, cache.head_dim
     T = slots.shape[0]
     _dense(slots, "slots", (T,), torch.int64)
@@ -667,6 +689,11 @@ def gptq_kv_attention(cache: KVCache, Q: torch.Tensor, cu_q: torch.Tensor, kv_le
     tokens are the last ones of those kv_lens[b]. max_q: the most query tokens of a sequence.
     sm_scale defaults to head_dim ** -0.5; window > 0 sees only the last `window` keys up to
     the query's own. lse, when given, is (total_q, n_q_heads) float32. Returns O."""
+    if stream is None:
+        got = _calls.kv_attention(cache.pool, cache.page_size, cache.n_kv_heads, cache.head_dim, Q, cu_q, kv_lens,
+                                  block_table, max_q, sm_scale, causal, window, O, lse, ws)
+        if got is not None:
+            return got
     pages, pool, h, dim = cache.check(), cache.pool, cache.n_kv_heads, cache.head_dim
     ldq = _heads(Q, "Q", (torch.bfloat16, torch.float16), -1, -1, dim)
     total, hq, _ = Q.shape
