@@ -896,8 +896,7 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
     // ---- few tokens: the cluster's sums, each member its share of the rows. The adapters' dot
     // products come first: they wait for no other CTA.
     const int t0 = (tile0 / p.mt) * N, r0 = (tile0 % p.mt) * BM;
-    __syncthreads();                                       // U is in shared memory (warp 3)
-    const int rows = BM / S, nout = rows * min(N, p.T - t0);
+    const int rows = BM / S, rows_lg = 31 - __clz(rows), nout = rows * min(N, p.T - t0);
     // 2^lg lanes share an output: each takes every 2^lg-th 16 bytes of the adapter's row and member
     // of the cluster, so an output's loads are in flight together
     // (as many as leave one pass over the outputs: 48 tokens, 8192 x 8192, rank 16: 28.5 us with two, 27.2 with one)
@@ -908,57 +907,70 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
     bool met = false;
     for (int x0 = threadIdx.x; x0 - lane < nout << lg || !met; x0 += OUT * THREADS) {
       float sum[OUT];
-      int col[OUT], rl[OUT];                               // token of the tile, row of the tile
+      int col[OUT], rl[OUT];                               // token of the tile (-1: none), row of the tile
+      const uint16_t* br[OUT];                             // the adapter's row
 #pragma unroll
       for (int o = 0; o < OUT; ++o) {
         const int x = (x0 + o * THREADS) >> lg;
-        col[o] = x < nout ? x / rows : -1;
-        rl[o] = rank_c * rows + (x - x / rows * rows);
+        col[o] = x < nout ? x >> rows_lg : -1;
+        rl[o] = (rank_c << rows_lg) + (x & (rows - 1));
         if (r0 + rl[o] >= p.m) col[o] = -1;
         sum[o] = 0.0f;
+        br[o] = nullptr;
+        if (p.ids && col[o] >= 0) {
+          const int id = p.ids[t0 + col[o]];
+          if (id >= 0 && id < p.n_adapters) br[o] = p.B + ((long long)id * p.m + r0 + rl[o]) * p.rank;
+        }
       }
-      if (p.ids) {
-        int id[OUT];
+      auto load = [&](uint4 (&v)[OUT], int r) {
 #pragma unroll
         for (int o = 0; o < OUT; ++o) {
-          id[o] = col[o] >= 0 ? p.ids[t0 + col[o]] : -1;
-          if (id[o] >= p.n_adapters) id[o] = -1;
+          v[o] = make_uint4(0u, 0u, 0u, 0u);
+          if (br[o] && r < p.rank) v[o] = __ldg(reinterpret_cast<const uint4*>(br[o] + r));
         }
+      };
+      uint4 bv[OUT];
+      load(bv, 8 * part);
+      // the first rows are on their way while the others finish; then U is in shared memory (warp 3)
+      if (!met) __syncthreads();
+      if (p.ids) {
         for (int r = 8 * part; r < p.rank; r += 8 << lg) {
-          uint4 bv[OUT];
+          uint4 next[OUT];
+          load(next, r + (8 << lg));
 #pragma unroll
           for (int o = 0; o < OUT; ++o) {
-            bv[o] = make_uint4(0u, 0u, 0u, 0u);
-            if (id[o] >= 0) bv[o] = __ldg(reinterpret_cast<const uint4*>(p.B + ((long long)id[o] * p.m + r0 + rl[o]) * p.rank + r));
-          }
-#pragma unroll
-          for (int o = 0; o < OUT; ++o) {
-            if (id[o] < 0) continue;
-            float v[8];
-            unpack8<BF16>(&bv[o], v);
-            const float* u = Us + col[o] * p.rank + r;
-            const float4 ua = *reinterpret_cast<const float4*>(u), ub = *reinterpret_cast<const float4*>(u + 4);
-            sum[o] = fmaf(v[0], ua.x, sum[o]); sum[o] = fmaf(v[1], ua.y, sum[o]);
-            sum[o] = fmaf(v[2], ua.z, sum[o]); sum[o] = fmaf(v[3], ua.w, sum[o]);
-            sum[o] = fmaf(v[4], ub.x, sum[o]); sum[o] = fmaf(v[5], ub.y, sum[o]);
-            sum[o] = fmaf(v[6], ub.z, sum[o]); sum[o] = fmaf(v[7], ub.w, sum[o]);
+            if (br[o]) {
+              float v[8];
+              unpack8<BF16>(&bv[o], v);
+              const float* u = Us + col[o] * p.rank + r;
+              const float4 ua = *reinterpret_cast<const float4*>(u), ub = *reinterpret_cast<const float4*>(u + 4);
+              sum[o] = fmaf(v[0], ua.x, sum[o]); sum[o] = fmaf(v[1], ua.y, sum[o]);
+              sum[o] = fmaf(v[2], ua.z, sum[o]); sum[o] = fmaf(v[3], ua.w, sum[o]);
+              sum[o] = fmaf(v[4], ub.x, sum[o]); sum[o] = fmaf(v[5], ub.y, sum[o]);
+              sum[o] = fmaf(v[6], ub.z, sum[o]); sum[o] = fmaf(v[7], ub.w, sum[o]);
+            }
+            bv[o] = next[o];
           }
         }
       }
-      if (!met) {
-        __syncwarp();
-        if (S > 1) cluster_sync();
-        met = true;
+      __syncwarp();
+      if (!met && S > 1) cluster_sync();
+      met = true;
+      for (int k = part; k < S; k += 1 << lg) {
+        float v[OUT];
+#pragma unroll
+        for (int o = 0; o < OUT; ++o) {
+          v[o] = 0.0f;
+          if (col[o] < 0) continue;
+          const float* at = &P[col[o] * C::P_LD + rl[o]];
+          v[o] = S > 1 ? ld_cluster(smem_u32(at), (uint32_t)k) : *at;
+        }
+#pragma unroll
+        for (int o = 0; o < OUT; ++o) sum[o] += v[o];
       }
+      __syncwarp();
 #pragma unroll
       for (int o = 0; o < OUT; ++o) {
-        if (col[o] >= 0) {
-          if (S > 1) {
-            for (int k = part; k < S; k += 1 << lg) sum[o] += ld_cluster(smem_u32(&P[col[o] * C::P_LD + rl[o]]), (uint32_t)k);
-          } else if (part == 0) {
-            sum[o] += P[col[o] * C::P_LD + rl[o]];
-          }
-        }
         for (int k = 0; k < lg; ++k) sum[o] += __shfl_xor_sync(0xffffffffu, sum[o], 1 << k);
         if (col[o] < 0 || part) continue;
         const long long at = (long long)(t0 + col[o]) * p.ldy + r0 + rl[o];
