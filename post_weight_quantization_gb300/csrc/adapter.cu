@@ -28,8 +28,8 @@
 //   warps 4 ...  unpack: sets of four (a warp per 32 tensor-memory lanes), 128-column blocks in turn
 //   last eight   epilogue: per unit N / 2 accumulators a thread
 //
-// Up to 256 tokens (N <= 64): a cluster of CTAs splits d for one tile, and the members sum their parts
-// from each other's shared memory, each a share of the rows, adding B[a] U there (one dot
+// Up to 256 tokens (N <= 64): a cluster of CTAs splits d for one tile; each member ends with a share
+// of the rows, whose sums the others write into its shared memory, and adds B[a] U there (one dot
 // product of `rank` values per output). Many tokens (N = 256): a persistent CTA per SM; the
 // adapters are further units of the same product, A = B[a]'s rows, B = U as two bf16 parts
 // (high and low, so the sum keeps 16 bits of U), one unit per run of tokens with one adapter,
@@ -72,6 +72,15 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
                : "=f"(v)
                : "r"(addr), "r"(rank));
   return v;
+}
+
+__device__ __forceinline__ uint32_t map_cluster(uint32_t addr, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 // Few tokens: a cluster per token and 16 rows of its adapter, a slice of d per CTA, its warps over
@@ -294,8 +303,7 @@ struct Cfg {
   static constexpr int X_BOX = N * XK * 2, X_BYTES = 2 * X_BOX;
   static constexpr int TMEM_A = ND * NP;                   // columns: the accumulators, then the A blocks of 64
   static constexpr uint32_t TMEM_COLS = 512;
-  static constexpr int P_LD = BM + 4;
-  static constexpr int P_BYTES = MANY ? 0 : N * P_LD * 4;  // the tile's sums, token-major, for the cluster
+  static constexpr int P_BYTES = MANY ? 0 : N * BM * 4;    // the cluster's sums of this member's rows
   static constexpr int SMEM_FIX = SLOTS * (X_BYTES + C_BYTES) + 1024 + 256 + P_BYTES;
 };
 
@@ -546,6 +554,9 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
   grid_dep_launch();
 
   const int S = MANY ? 1 : p.S, rank_c = MANY ? 0 : (int)(blockIdx.x % S);
+  const int rows = BM / S, rows_lg = 31 - __clz(rows);     // few tokens: the rows that a member of the cluster ends with
+  if (S > 1) cluster_arrive();                             // waited for before anything is written to another member
+  bool all_here = false;                                   // this warp has
   const int ntiles = p.mt * p.nt, step = MANY ? (int)gridDim.x : ntiles;       // few tokens: one tile per cluster
   const int tile0 = MANY ? (int)blockIdx.x : (int)(blockIdx.x / S);
   const int nblk = (p.d + KB - 1) / KB, blk0 = (int)((long long)nblk * rank_c / S), blk1 = (int)((long long)nblk * (rank_c + 1) / S);
@@ -886,8 +897,21 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
             }
         }
       } else {
+        // each row's sums to the member that ends with it: [member][token][row]
+        const int own = (32 * q + lane) >> rows_lg;
+        uint32_t to = smem_u32(P) + 4 * (((rank_c * N) << rows_lg) + ((32 * q + lane) & (rows - 1)));
+        if (S > 1) {
+          __syncwarp();
+          cluster_wait();
+          all_here = true;
+          to = map_cluster(to, (uint32_t)own);
+        }
 #pragma unroll
-        for (int c = 0; c < NC; ++c) P[(h * NC + c) * C::P_LD + 32 * q + lane] = half2f(run[0][c / 2], c & 1);
+        for (int c = 0; c < NC; ++c) {
+          const float v = half2f(run[0][c / 2], c & 1);
+          const uint32_t at = to + 4 * ((h * NC + c) << rows_lg);
+          if (S > 1) st_cluster(at, v); else asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
+        }
       }
     }
   }
@@ -896,7 +920,12 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
     // ---- few tokens: the cluster's sums, each member its share of the rows. The adapters' dot
     // products come first: they wait for no other CTA.
     const int t0 = (tile0 / p.mt) * N, r0 = (tile0 % p.mt) * BM;
-    const int rows = BM / S, rows_lg = 31 - __clz(rows), nout = rows * min(N, p.T - t0);
+    const int nout = rows * min(N, p.T - t0);
+    if (S > 1) {                                           // the members' sums are written
+      __syncwarp();
+      if (!all_here) cluster_wait();
+      cluster_arrive();
+    }
     // 2^lg lanes share an output: each takes every 2^lg-th 16 bytes of the adapter's row and member
     // of the cluster, so an output's loads are in flight together
     // (as many as leave one pass over the outputs: 48 tokens, 8192 x 8192, rank 16: 28.5 us with two, 27.2 with one)
@@ -954,7 +983,7 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
         }
       }
       __syncwarp();
-      if (!met && S > 1) cluster_sync();
+      if (!met && S > 1) cluster_wait();
       met = true;
       for (int k = part; k < S; k += 1 << lg) {
         float v[OUT];
@@ -962,8 +991,7 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
         for (int o = 0; o < OUT; ++o) {
           v[o] = 0.0f;
           if (col[o] < 0) continue;
-          const float* at = &P[col[o] * C::P_LD + rl[o]];
-          v[o] = S > 1 ? ld_cluster(smem_u32(at), (uint32_t)k) : *at;
+          v[o] = P[((k * N + col[o]) << rows_lg) + (rl[o] & (rows - 1))];
         }
 #pragma unroll
         for (int o = 0; o < OUT; ++o) sum[o] += v[o];
@@ -979,8 +1007,6 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
       }
       __syncwarp();
     }
-    __syncwarp();
-    if (S > 1) cluster_sync();                             // nobody leaves while its sums are read
   }
 
   tc_fence_before();

@@ -197,6 +197,10 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// The two halves of it, for other work in between (whole warps).
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 // Make this thread's ordinary shared-memory writes visible to the async proxy (TMA,
 // tensor-core operand reads) before signalling the consumer.
 __device__ __forceinline__ void fence_proxy_async_smem() {
