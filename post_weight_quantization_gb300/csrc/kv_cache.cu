@@ -98,14 +98,50 @@ __device__ __forceinline__ void row_range(const Row16<E>& r, float& lo, float& h
   }
 }
 
-// The code of x in fp32: round((x - low) / s) limited to [0, 15], ties to even. The limit from
-// above is put on the numerator (15 s / s is 15 exactly, and an infinity stays out of the
-// correction); the conversion to an unsigned integer limits from below.
-__device__ __forceinline__ uint32_t code_of(float x, float low, float s, float inv, float top) {
-  const float q = divide(fminf(__fsub_rn(x, low), top), s, inv);
-  uint32_t c;
-  asm("cvt.rni.u32.f32 %0, %1;" : "=r"(c) : "f"(q));
-  return c;
+// Two fp32 values in one register pair: sum, product, multiply-add of both at once.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float2 halves(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+// The codes of eight values as a word: round((x - low) / s) limited to [0, 15], ties to even, in
+// fp32. The limits are put on the numerator (15 s / s is 15 exactly, and an infinity stays out of
+// the correction). Adding 1.5 * 2^23 rounds the quotient to an integer, which lies in the sum's low
+// bits; the eight sums' other bits leave the word as one constant (mod 2^32).
+__device__ __forceinline__ uint32_t codes_of(const float (&v)[8], float low, float s, float inv, float top) {
+  const uint64_t low2 = pair(-low, -low), s2 = pair(-s, -s), inv2 = pair(inv, inv), magic = pair(12582912.0f, 12582912.0f);
+  uint32_t word = 0u - 0x4B400000u * 0x11111111u;
+#pragma unroll
+  for (int k = 0; k < 8; k += 2) {
+    const float2 a = halves(add2(pair(v[k], v[k + 1]), low2));
+    const uint64_t n = pair(fmaxf(fminf(a.x, top), 0.0f), fmaxf(fminf(a.y, top), 0.0f));
+    const uint64_t q = mul2(n, inv2);                   // the two steps of divide()
+    const float2 c = halves(add2(fma2(fma2(q, s2, n), inv2, q), magic));
+    word += __float_as_uint(c.x) << (4 * k);
+    word += __float_as_uint(c.y) << (4 * k + 4);
+  }
+  return word;
 }
 
 // A warp takes one token and NB * RPW / 2 heads of it (RPW rows at once): NB rows per lane
@@ -190,9 +226,7 @@ __global__ void __launch_bounds__(WARPS * 32) kv_append_kernel(Params p, int* __
     for (int x = 0; x < 2; ++x) {
       float v[8];
       unpack8<E>(&raw[i].r[x], v);
-      word[x] = 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) word[x] += code_of(v[k], low, sc, inv, top) << (4 * k);
+      word[x] = codes_of(v, low, sc, inv, top);
     }
     if (h >= p.H) continue;
     uint8_t* b = page + (long long)h * p.page * (D + 8);
@@ -235,13 +269,24 @@ __global__ void __launch_bounds__(WARPS * 32) kv_read_kernel(Params p, int* __re
     if (h >= p.H) continue;
     const float sc = __half2float(__ushort_as_half((unsigned short)num[i]));
     const float low = __half2float(__ushort_as_half((unsigned short)(num[i] >> 16)));
+    // A code masked out of its place k and put under the exponent of 2^23 is 2^23 + 16^k code as a float;
+    // less 2^23 it is 16^k code exactly, and times scale 16^-k the same product as code times scale.
+    const uint64_t low2 = pair(low, low), magic = pair(-8388608.0f, -8388608.0f);
+    const uint64_t s01 = pair(sc, sc * 0.0625f), s23 = pair(sc * 0.00390625f, sc * 0.000244140625f);
     float v[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      // 2^23 + code - 2^23: the code as a float without an integer conversion
-      const float c = __uint_as_float(((word[i] >> (4 * k)) & 15u) | 0x4B000000u) - 8388608.0f;
-      v[k] = fmaf(c, sc, low);
-      if (std::is_same<E, F16>::value && v[k] == v[k]) v[k] = fminf(fmaxf(v[k], -kHalfMax), kHalfMax);   // 15 scale + low can round past it
+    for (int k = 0; k < 8; k += 2) {
+      const uint32_t w = word[i] >> (k < 4 ? 0 : 16);
+      const uint64_t c = pair(__uint_as_float((w & (15u << (4 * (k & 2)))) | 0x4B000000u),
+                              __uint_as_float((w & (240u << (4 * (k & 2)))) | 0x4B000000u));
+      const float2 f = halves(fma2(add2(c, magic), k & 2 ? s23 : s01, low2));
+      v[k] = f.x;
+      v[k + 1] = f.y;
+    }
+    if (std::is_same<E, F16>::value) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (v[k] == v[k]) v[k] = fminf(fmaxf(v[k], -kHalfMax), kHalfMax);      // 15 scale + low can round past it
     }
     pack8<E>(reinterpret_cast<typename E::T*>(kv ? p.y[1] : p.y[0]) + t * (kv ? p.ldy[1] : p.ldy[0]) + h * D + 8 * l, v);
   }
