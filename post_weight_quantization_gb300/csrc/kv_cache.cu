@@ -147,11 +147,10 @@ __device__ __forceinline__ uint32_t codes_of(const float (&v)[8], float low, flo
 // A warp takes one token and NB * RPW / 2 heads of it (RPW rows at once): NB rows per lane
 // group, whose loads are all in flight before the first is used (the token's slot and its
 // page, a 64-bit multiply by a host-computed reciprocal instead of a division, are the same
-// for all of them). Appending, a lane holds 16 values of a row, so that a row's statistics,
-// which all its lanes compute, cost half as much as with eight: the kernel is bound by
-// instruction issue before bandwidth.
-constexpr int NB_APPEND = 2, NB_READ = 4;
-template <int D> constexpr int append_lanes() { return D / 16; }
+// for all of them). A lane holds 16 values of a row, and always of K or always of V, so that what is
+// computed per row costs half as much as with eight and addresses are steps: the kernels are bound
+// by instruction issue before bandwidth. NB is 4 where the heads fill it, else 2.
+template <int D> constexpr int row_lanes() { return D / 16; }
 
 struct Params {
   const void* x[2];            // K, V
@@ -182,24 +181,24 @@ __device__ __forceinline__ uint8_t* page_of(const Params& p, long long slot, int
   return p.pool + page * p.H * ((long long)p.page * (D + 8));
 }
 
-template <typename E, int D>
+template <typename E, int D, int NB>
 __global__ void __launch_bounds__(WARPS * 32) kv_append_kernel(Params p, int* __restrict__ err) {
-  constexpr int NB = NB_APPEND, LANES = append_lanes<D>(), RPW = 32 / LANES;
-  const int lane = threadIdx.x & 31, l = lane % LANES, sub = lane / LANES;
+  constexpr int LANES = row_lanes<D>(), RPW = 32 / LANES;
+  const int lane = threadIdx.x & 31, l = lane % LANES, sub = lane / LANES, kv = sub & 1;
   uint32_t t;
   int h0;
   if (!unit_of<NB * RPW / 2>(p, t, h0)) return;
   const long long slot = p.slots[t];
+  h0 += sub >> 1;                                       // this lane's heads: h0, h0 + RPW / 2, ...
+  const typename E::T* x = reinterpret_cast<const typename E::T*>(kv ? p.x[1] : p.x[0]) + t * (kv ? p.ldx[1] : p.ldx[0]) +
+                           h0 * D + 8 * l;
   Row16<E> raw[NB];
 #pragma unroll
-  for (int i = 0; i < NB; ++i) {                        // row i * RPW + sub: K and V of a head in turn
-    const int row = i * RPW + sub, h = h0 + (row >> 1), kv = row & 1;
+  for (int i = 0; i < NB; ++i) {
     raw[i] = Row16<E>{};
-    if (h < p.H) {
-      const typename E::T* x = reinterpret_cast<const typename E::T*>(kv ? p.x[1] : p.x[0]) +
-                               t * (kv ? p.ldx[1] : p.ldx[0]) + h * D + 8 * l;
-      raw[i].r[0] = *reinterpret_cast<const Row8<E>*>(x);
-      raw[i].r[1] = *reinterpret_cast<const Row8<E>*>(x + D / 2);
+    if (h0 + i * (RPW / 2) < p.H) {
+      raw[i].r[0] = *reinterpret_cast<const Row8<E>*>(x + i * (RPW / 2) * D);
+      raw[i].r[1] = *reinterpret_cast<const Row8<E>*>(x + i * (RPW / 2) * D + D / 2);
     }
   }
   if (slot < 0) return;
@@ -209,9 +208,11 @@ __global__ void __launch_bounds__(WARPS * 32) kv_append_kernel(Params p, int* __
   }
   int at;
   uint8_t* page = page_of<D>(p, slot, at);
+  const long long block = (long long)p.page * (D + 8);
+  uint8_t* codes = page + h0 * block + (kv * p.page + at) * (D / 2) + 4 * l;
+  uint8_t* nums = page + h0 * block + p.page * D + 8 * at + 4 * kv;
 #pragma unroll
   for (int i = 0; i < NB; ++i) {
-    const int row = i * RPW + sub, h = h0 + (row >> 1), kv = row & 1;
     float lo, hi;
     row_range<E, LANES>(raw[i], lo, hi);
     const bool bad = lo != lo;
@@ -223,72 +224,83 @@ __global__ void __launch_bounds__(WARPS * 32) kv_append_kernel(Params p, int* __
     const float inv = sc > 0.0f ? reciprocal(sc) : 0.0f, top = 15.0f * sc;
     uint32_t word[2];
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
+    for (int y = 0; y < 2; ++y) {
       float v[8];
-      unpack8<E>(&raw[i].r[x], v);
-      word[x] = codes_of(v, low, sc, inv, top);
+      unpack8<E>(&raw[i].r[y], v);
+      word[y] = codes_of(v, low, sc, inv, top);
     }
-    if (h >= p.H) continue;
-    uint8_t* b = page + (long long)h * p.page * (D + 8);
-    uint32_t* c = reinterpret_cast<uint32_t*>(b + (kv * p.page + at) * (D / 2));
-    c[l] = word[0];
-    c[D / 16 + l] = word[1];
+    if (h0 + i * (RPW / 2) >= p.H) continue;
+    uint32_t* c = reinterpret_cast<uint32_t*>(codes + i * (RPW / 2) * block);
+    c[0] = word[0];
+    c[D / 16] = word[1];
     if (l == 0) {
       const uint32_t s16 = bad ? 0x7FFFu : (uint32_t)__half_as_ushort(hs);
-      reinterpret_cast<uint32_t*>(b + p.page * D)[2 * at + kv] = s16 | ((uint32_t)__half_as_ushort(hl) << 16);
+      *reinterpret_cast<uint32_t*>(nums + i * (RPW / 2) * block) = s16 | ((uint32_t)__half_as_ushort(hl) << 16);
     }
   }
 }
 
-template <typename E, int D>
+// Eight codes of a word times scale plus low, one rounding each. A code masked out of its place k
+// and put under the exponent of 2^23 is 2^23 + 16^k code as a float; less 2^23 it is 16^k code exactly,
+// and times scale 16^-k the same product as code times scale.
+__device__ __forceinline__ void values_of(uint32_t word, uint64_t s01, uint64_t s23, uint64_t low2, float (&v)[8]) {
+  const uint64_t magic = pair(-8388608.0f, -8388608.0f);
+#pragma unroll
+  for (int k = 0; k < 8; k += 2) {
+    const uint32_t w = word >> (k < 4 ? 0 : 16);
+    const uint64_t c = pair(__uint_as_float((w & (15u << (4 * (k & 2)))) | 0x4B000000u),
+                            __uint_as_float((w & (240u << (4 * (k & 2)))) | 0x4B000000u));
+    const float2 f = halves(fma2(add2(c, magic), k & 2 ? s23 : s01, low2));
+    v[k] = f.x;
+    v[k + 1] = f.y;
+  }
+}
+
+template <typename E, int D, int NB>
 __global__ void __launch_bounds__(WARPS * 32) kv_read_kernel(Params p, int* __restrict__ err) {
-  constexpr int NB = NB_READ, LPR = D / 8, RPW = 32 / LPR;
-  const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
+  constexpr int LANES = row_lanes<D>(), RPW = 32 / LANES;
+  const int lane = threadIdx.x & 31, l = lane % LANES, sub = lane / LANES, kv = sub & 1;
   uint32_t t;
   int h0;
   if (!unit_of<NB * RPW / 2>(p, t, h0)) return;
   const long long slot = p.slots[t];
-  uint32_t word[NB], num[NB];
+  h0 += sub >> 1;
   const bool live = slot >= 0 && slot < p.n_slots;
   if (slot >= p.n_slots && lane == 0) report_device_error(err, DEVERR_INDEX);
   int at = 0;
   const uint8_t* page = live ? page_of<D>(p, slot, at) : nullptr;
+  const long long block = (long long)p.page * (D + 8);
+  const uint8_t* codes = page + h0 * block + (kv * p.page + at) * (D / 2) + 4 * l;
+  const uint8_t* nums = page + h0 * block + p.page * D + 8 * at + 4 * kv;
+  uint32_t word[NB][2], num[NB];
 #pragma unroll
   for (int i = 0; i < NB; ++i) {
-    const int row = i * RPW + sub, h = h0 + (row >> 1), kv = row & 1;
-    word[i] = num[i] = 0u;
-    if (live && h < p.H) {
-      const uint8_t* b = page + (long long)h * p.page * (D + 8);
-      word[i] = reinterpret_cast<const uint32_t*>(b + (kv * p.page + at) * (D / 2))[l];
-      num[i] = reinterpret_cast<const uint32_t*>(b + p.page * D)[2 * at + kv];
+    word[i][0] = word[i][1] = num[i] = 0u;
+    if (live && h0 + i * (RPW / 2) < p.H) {
+      const uint32_t* c = reinterpret_cast<const uint32_t*>(codes + i * (RPW / 2) * block);
+      word[i][0] = c[0];
+      word[i][1] = c[D / 16];
+      num[i] = *reinterpret_cast<const uint32_t*>(nums + i * (RPW / 2) * block);
     }
   }
+  typename E::T* y = reinterpret_cast<typename E::T*>(kv ? p.y[1] : p.y[0]) + t * (kv ? p.ldy[1] : p.ldy[0]) + h0 * D + 8 * l;
 #pragma unroll
   for (int i = 0; i < NB; ++i) {
-    const int row = i * RPW + sub, h = h0 + (row >> 1), kv = row & 1;
-    if (h >= p.H) continue;
+    if (h0 + i * (RPW / 2) >= p.H) continue;
     const float sc = __half2float(__ushort_as_half((unsigned short)num[i]));
     const float low = __half2float(__ushort_as_half((unsigned short)(num[i] >> 16)));
-    // A code masked out of its place k and put under the exponent of 2^23 is 2^23 + 16^k code as a float;
-    // less 2^23 it is 16^k code exactly, and times scale 16^-k the same product as code times scale.
-    const uint64_t low2 = pair(low, low), magic = pair(-8388608.0f, -8388608.0f);
-    const uint64_t s01 = pair(sc, sc * 0.0625f), s23 = pair(sc * 0.00390625f, sc * 0.000244140625f);
-    float v[8];
+    const uint64_t low2 = pair(low, low), s01 = pair(sc, sc * 0.0625f), s23 = mul2(s01, pair(0.00390625f, 0.00390625f));
 #pragma unroll
-    for (int k = 0; k < 8; k += 2) {
-      const uint32_t w = word[i] >> (k < 4 ? 0 : 16);
-      const uint64_t c = pair(__uint_as_float((w & (15u << (4 * (k & 2)))) | 0x4B000000u),
-                              __uint_as_float((w & (240u << (4 * (k & 2)))) | 0x4B000000u));
-      const float2 f = halves(fma2(add2(c, magic), k & 2 ? s23 : s01, low2));
-      v[k] = f.x;
-      v[k + 1] = f.y;
-    }
-    if (std::is_same<E, F16>::value) {
+    for (int z = 0; z < 2; ++z) {
+      float v[8];
+      values_of(word[i][z], s01, s23, low2, v);
+      if (std::is_same<E, F16>::value) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (v[k] == v[k]) v[k] = fminf(fmaxf(v[k], -kHalfMax), kHalfMax);      // 15 scale + low can round past it
+        for (int k = 0; k < 8; ++k)
+          if (v[k] == v[k]) v[k] = fminf(fmaxf(v[k], -kHalfMax), kHalfMax);    // 15 scale + low can round past it
+      }
+      pack8<E>(y + i * (RPW / 2) * D + z * (D / 2), v);
     }
-    pack8<E>(reinterpret_cast<typename E::T*>(kv ? p.y[1] : p.y[0]) + t * (kv ? p.ldy[1] : p.ldy[0]) + h * D + 8 * l, v);
   }
 }
 
@@ -298,6 +310,9 @@ void with_width(int D, F&& f) {
   else if (D == 128) f(std::integral_constant<int, 128>{});
   else f(std::integral_constant<int, 256>{});
 }
+
+// Rows per lane group of a warp: four where the token's 2 H rows fill them.
+int rows_of(int H, int D) { return 2 * H >= 4 * (32 / (D / 16)) ? 4 : 2; }
 
 // Fills in the sizes for warps of `heads` heads; returns the grid (0: too large).
 unsigned set_sizes(Params& p, long long T, int H, int heads, long long num_pages, int page, const long long* slots,
@@ -322,11 +337,13 @@ gptq_status kv_append_launch(const void* K, const void* V, int dtype, long long 
   using namespace kvc;
   Params p{};
   p.x[0] = K; p.x[1] = V; p.ldx[0] = ldk; p.ldx[1] = ldv;
-  const unsigned grid = set_sizes(p, T, H, NB_APPEND * (32 / (D / 16)) / 2, num_pages, page, slots, pool);
+  const int nb = rows_of(H, D);
+  const unsigned grid = set_sizes(p, T, H, nb * (32 / (D / 16)) / 2, num_pages, page, slots, pool);
   if (!grid) return set_error(GPTQ_ERR_INVALID_ARG, "too many rows for one launch");
   with_dtype(dtype, [&](auto e) {
     with_width(D, [&](auto d) {
-      kv_append_kernel<decltype(e), decltype(d)::value><<<grid, WARPS * 32, 0, s>>>(p, device_error_word());
+      if (nb == 4) kv_append_kernel<decltype(e), decltype(d)::value, 4><<<grid, WARPS * 32, 0, s>>>(p, device_error_word());
+      else kv_append_kernel<decltype(e), decltype(d)::value, 2><<<grid, WARPS * 32, 0, s>>>(p, device_error_word());
     });
   });
   count_launch();
@@ -338,11 +355,13 @@ gptq_status kv_read_launch(const void* pool, long long num_pages, int page, int 
   using namespace kvc;
   Params p{};
   p.y[0] = K; p.y[1] = V; p.ldy[0] = ldk; p.ldy[1] = ldv;
-  const unsigned grid = set_sizes(p, T, H, NB_READ * (32 / (D / 8)) / 2, num_pages, page, slots, const_cast<void*>(pool));
+  const int nb = rows_of(H, D);
+  const unsigned grid = set_sizes(p, T, H, nb * (32 / (D / 16)) / 2, num_pages, page, slots, const_cast<void*>(pool));
   if (!grid) return set_error(GPTQ_ERR_INVALID_ARG, "too many rows for one launch");
   with_dtype(dtype, [&](auto e) {
     with_width(D, [&](auto d) {
-      kv_read_kernel<decltype(e), decltype(d)::value><<<grid, WARPS * 32, 0, s>>>(p, device_error_word());
+      if (nb == 4) kv_read_kernel<decltype(e), decltype(d)::value, 4><<<grid, WARPS * 32, 0, s>>>(p, device_error_word());
+      else kv_read_kernel<decltype(e), decltype(d)::value, 2><<<grid, WARPS * 32, 0, s>>>(p, device_error_word());
     });
   });
   count_launch();
