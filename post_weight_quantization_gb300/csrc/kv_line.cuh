@@ -267,14 +267,15 @@ struct Copies {
 
 // Joins the parts of the items that were cut. CTA (c, y) takes the item that CTA c of the other
 // kernel began and others ended; its parts lie in c's second place and the following CTAs' first.
-// A warp takes a row, or, where there are many parts, two warps share one.
+// A warp takes a row, all its parts in flight together; where there are many parts, two to eight
+// warps share a row.
 constexpr int JOIN_WARPS = 16;
 template <int D, int R>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) kv_join_kernel(Params p, int* __restrict__ err) {
   constexpr int VPL = D / 32, PART = R * D + 2 * R;
   using V = typename std::conditional<VPL == 2, float2, float4>::type;       // a lane's values, NV vectors of VW
   constexpr int NV = VPL == 2 ? 1 : VPL / 4, VW = VPL / NV;
-  __shared__ float sl[JOIN_WARPS / 2], so[JOIN_WARPS / 2][D];
+  __shared__ float sl[JOIN_WARPS], so[JOIN_WARPS][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_dep_wait();
   const int c = blockIdx.x;
@@ -326,32 +327,58 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) kv_join_kernel(Params p, int*
   };
   if (np <= 4) {
     for (int r = JOIN_WARPS * blockIdx.y + warp; r < R && (long long)rt * R + r < all_rows; r += JOIN_WARPS * gridDim.y) {
-      largest(r);
-      for (int k = 0; k < np; ++k) add(k, r);
+      float mk[4], lk[4];
+      V vk[4][NV];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        mk[k] = -CUDART_INF_F;
+        if (k < np) {
+          const float* pt = part_of(k);
+          mk[k] = pt[R * D + r];
+          lk[k] = pt[R * D + R + r];
+#pragma unroll
+          for (int x = 0; x < NV; ++x) vk[k][x] = *reinterpret_cast<const V*>(pt + r * D + (32 * x + lane) * VW);
+        }
+      }
+      mm = fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3]));
+      ll = 0.0f;
+#pragma unroll
+      for (int k = 0; k < VPL; ++k) acc[k] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (mk[k] == -CUDART_INF_F) continue;
+        const float f = ex2(mk[k] - mm);
+        ll = fmaf(f, lk[k], ll);
+#pragma unroll
+        for (int x = 0; x < VPL; ++x) acc[x] = fmaf(f, reinterpret_cast<const float*>(vk[k])[x], acc[x]);
+      }
       write(rt * R + r);
     }
     return;
   }
-  const int half = warp >> 3;
-  for (int r8 = 8 * blockIdx.y; r8 < R && (long long)rt * R + r8 < all_rows; r8 += 8 * gridDim.y) {
-    const int r = r8 + (warp & 7), rr = rt * R + r;
-    const bool live = rr < all_rows;
+  const long long rows = all_rows - (long long)rt * R;
+  const int rp = rows <= 2 ? 2 : rows <= 4 ? 4 : 8, share = JOIN_WARPS / rp, slot = warp & (rp - 1), s0 = warp / rp;
+  for (int r0 = rp * blockIdx.y; r0 < R && r0 < rows; r0 += rp * gridDim.y) {
+    const int r = r0 + slot;
+    const bool live = r < rows;
     if (live) {
       largest(r);
 #pragma unroll 8
-      for (int k = half; k < np; k += 2) add(k, r);
+      for (int k = s0; k < np; k += share) add(k, r);
     }
-    if (half && live) {
-      if (lane == 0) sl[warp & 7] = ll;
+    if (s0 && live) {
+      if (lane == 0) sl[warp] = ll;
 #pragma unroll
-      for (int x = 0; x < VPL; ++x) so[warp & 7][(32 * (x / VW) + lane) * VW + x % VW] = acc[x];
+      for (int x = 0; x < VPL; ++x) so[warp][(32 * (x / VW) + lane) * VW + x % VW] = acc[x];
     }
     __syncthreads();
-    if (!half && live) {
-      ll += sl[warp];
+    if (!s0 && live) {
+      for (int w = slot + rp; w < JOIN_WARPS; w += rp) {
+        ll += sl[w];
 #pragma unroll
-      for (int x = 0; x < VPL; ++x) acc[x] += so[warp][(32 * (x / VW) + lane) * VW + x % VW];
-      write(rr);
+        for (int x = 0; x < VPL; ++x) acc[x] += so[w][(32 * (x / VW) + lane) * VW + x % VW];
+      }
+      write(rt * R + r);
     }
     __syncthreads();
   }
