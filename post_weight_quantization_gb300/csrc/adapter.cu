@@ -34,6 +34,11 @@
 // adapters are further units of the same product, A = B[a]'s rows, B = U as two bf16 parts
 // (high and low, so the sum keeps 16 bits of U), one unit per run of tokens with one adapter,
 // which the epilogue adds to that run's columns only.
+//
+// Bound: HBM bandwidth for few tokens (the codes), the tensor cores for many. Measured at 4 bits, rank
+// 16: 4096 x 4096, 1 token 12.3 us, 3001 tokens 130 us (780 TFLOP/s, 40 % of the library GEMM's rate: an
+// accumulator leaves tensor memory per 128 columns); 8192 x 8192, 48 tokens 31 us (2.1 TB/s; unpacking:
+// instruction issue 61 % busy).
 #include <cudaTypedefs.h>
 
 #include <algorithm>

@@ -12,7 +12,8 @@
 // Bound: HBM bandwidth (every value read once and written once). A warp takes one token and a
 // strided set of its head blocks, NB rows per lane group each: the token's angles and the
 // weights are read once for all of them, and a block's loads are in flight while the block
-// before is computed.
+// before is computed. Measured, 16381 tokens of 64 + 8 heads of 128, bf16: 106 us, 5.75 TB/s, 85 % of
+// a plain copy's rate.
 #include <algorithm>
 #include <type_traits>
 
