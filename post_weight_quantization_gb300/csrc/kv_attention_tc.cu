@@ -16,16 +16,17 @@
 // row sees the NaN in its score exactly when it sees the key.
 //
 //   warp 0        copies of the packed tiles (bulk copies into a ring of two)
-//   warp 1        MMA issuer: S_A, S_B of the first tile; then per tile and group P V, next S
+//   warp 1        MMA issuer: the first tile's S; then per half tile and group P V, S of the next but one
 //   warps 4-11    dequantize: half a key per thread, K then V, into a ring of three 128 x D buffers
-//   warps 12-27   softmax: two threads per query row, half a tile's keys each, which tell each other
-//                 their maxima through shared memory; at the item's end O
-// One pass over the scores: they are read from tensor memory 16 at a time and leave as probabilities
-// from the maximum so far (all of a tile's scores in registers at once spilled, and so little cache is
-// left beside the shared memory that spills go to L2: 412 instead of 288 us).
+//   warps 12-19   softmax: a query row per thread (four warps per group); at the item's end O
+// Scores come by half tiles of 64 keys into the two halves of a group's columns: while the softmax
+// works on one half, the MMAs bring the other (whole tiles, whose P lies over all of S, made the two
+// take turns: 288 instead of 269 us). One pass over the scores: they are read from tensor memory 32 at
+// a time and leave as probabilities from the maximum so far. (Two threads per row, which tell each
+// other their maxima, took 341 us with half tiles: what is done per half tile then counts twice.)
 // Bound: the tensor cores' 4 rows keys D operations; measured, 1024 tokens over 8187 keys, 64 + 8 heads of
-// 128: 288 us, 45 % of the measured bf16 rate. A group's MMAs and its softmax take turns (P lies over S);
-// the other group works meanwhile. Per 256 rows and 128 keys 4200 cycles, of which 2048 are MMAs.
+// 128: 269 us, 47 % of the measured bf16 rate with the join's launch. Per 256 rows and 128 keys it takes 3900
+// cycles, of which 2048 are MMAs; the softmax warps' own latency is the rest.
 // The tiles of all items form a line that is cut evenly over one CTA per SM, as in the other
 // kernel, and cut items are joined afterwards.
 #include "kv_line.cuh"
@@ -34,12 +35,12 @@ namespace gptq {
 namespace kva {
 namespace tc {
 
-constexpr int R = 256, DEQ0 = 4, NDEQ = 8, SOFT0 = DEQ0 + NDEQ, THREADS = (SOFT0 + 16) * 32;
+constexpr int R = 256, DEQ0 = 4, NDEQ = 8, SOFT0 = DEQ0 + NDEQ, THREADS = (SOFT0 + 8) * 32;
 constexpr int kItemCost = 1;
-constexpr int CH = 16;                          // scores a thread takes from tensor memory at once
+constexpr int CH = 32;                          // scores a thread takes from tensor memory at once
 constexpr float kSlack = 7.0f;                  // a row's maximum may lag by 2^7 before it is moved: probabilities stay below 2^15
 constexpr float kShift = 8.0f;                  // probabilities are kept 2^kShift times too large
-constexpr int REG_ISSUE = 40, REG_DEQ = 56, REG_SOFT = 88;        // 128 x 40 + 256 x 56 + 512 x 88 = 896 x 72
+constexpr int REG_ISSUE = 72, REG_DEQ = 64, REG_SOFT = 136;       // 128 x 72 + 256 x 64 + 256 x 136, below 640 x 96
 
 template <int D>
 struct Cfg {
@@ -49,8 +50,7 @@ struct Cfg {
   static constexpr int STAGE = TILE * (D + 8);
   static constexpr int NC = 2, NM = 3;          // ring of packed tiles, ring of dequantized matrices
   static constexpr int CODES = 2 * MAT, MATS = CODES + (NC * STAGE + 1023) / 1024 * 1024, BARS = MATS + NM * MAT;
-  static constexpr int ROWS = BARS + 512;       // two floats per row, twice: what the halves of a row tell each other
-  static constexpr int SMEM = ROWS + 4096 + 1024;
+  static constexpr int SMEM = BARS + 512 + 1024;
   static constexpr int PART = R * D + 2 * R;
 };
 
@@ -176,13 +176,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
   uint64_t* m_full = c_empty + NC;                                   // dequantized matrices: K, V, K, V, ...
   uint64_t* m_empty = m_full + NM;
   uint64_t* q_full = m_empty + NM;                                   // per group from here on
-  uint64_t* s_full = q_full + 2;
-  uint64_t* p_full = s_full + 2;
-  uint64_t* o_done = p_full + 2;                                     // P V of a tile is done
-  uint64_t* o_free = o_done + 2;                                     // the item's O has been read
+  uint64_t* s_full = q_full + 2;                                     // per group and half of a tile
+  uint64_t* p_full = s_full + 4;
+  uint64_t* o_done = p_full + 4;                                     // P V of a half tile is done
+  uint64_t* o_last = o_done + 2;                                     // the item's last P V is
+  uint64_t* o_free = o_last + 2;                                     // the item's O has been read
   uint64_t* drain = o_free + 2;
-  uint64_t* told = drain + 1;                                        // 8: both halves of 32 rows have written
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(told + 8);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   long long* sh = reinterpret_cast<long long*>(smem + C::BARS + 384);        // 14 values
 
@@ -197,13 +197,15 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
       mbar_init(&m_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&q_full[i], 8);
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 8);
+      mbar_init(&q_full[i], 4);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&s_full[2 * i + b], 1);
+        mbar_init(&p_full[2 * i + b], 4);
+      }
       mbar_init(&o_done[i], 1);
-      mbar_init(&o_free[i], 8);
+      mbar_init(&o_last[i], 1);
+      mbar_init(&o_free[i], 4);
     }
-    for (int i = 0; i < 8; ++i) mbar_init(&told[i], 2);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -245,60 +247,69 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
     } else if (warp == 1) {
       // ---------------- MMA issuer ----------------
       const uint32_t leader = elect_leader();
-      constexpr uint32_t IDS = umma_idesc(/*f16*/ 0, false, false, 128, 128), IDO = umma_idesc(0, false, /*B MN-major*/ true, 128, D);
+      constexpr uint32_t IDS = umma_idesc(/*f16*/ 0, false, false, 128, 64), IDO = umma_idesc(0, false, /*B MN-major*/ true, 128, D);
       const uint32_t sb = smem_u32(smem);
       const uint64_t q_desc = umma_sdesc_sw128(sb, 16, 1024), k_desc = umma_sdesc_sw128(sb + C::MATS, 16, 1024);
       const uint64_t v_desc = umma_sdesc_sw128(sb + C::MATS, C::BOX, 1024);
-      uint32_t mat = 0, np[2] = {0, 0}, items[2] = {0, 0};           // matrices, tiles and items so far, per group
+      uint32_t mat = 0, np[4] = {0, 0, 0, 0}, items[2] = {0, 0};     // matrices; waits per group and half; items per group
       bool issued = false;
+      // S of half tile j into its half of the group's columns
+      auto scores = [&](int x, int j, uint32_t kslot) {
+        const uint64_t kd = k_desc + (uint64_t)(kslot * (C::MAT / 16) + (j & 1) * (64 * 128 / 16)), qd = q_desc + (uint64_t)(x * (C::MAT / 16));
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_f16_ss(s_tm + 128 * x + 64 * (j & 1), qd + (kk >> 2) * (C::BOX / 16) + 2 * (kk & 3),
+                      kd + (kk >> 2) * (C::BOX / 16) + 2 * (kk & 3), IDS, kk > 0, leader);
+        commit_by(&s_full[2 * x + (j & 1)], leader);
+      };
       while (ok && line.next(p, it, err)) {
-        const int groups = it.rows > 128 ? 2 : 1;
-        for (int i = 0; ok && i <= it.nt; ++i) {                     // P V of tile i - 1, S of tile i
-          const uint32_t kslot = mat % NM, vslot = (mat + NM - 1) % NM;
-          if (it.nt == 0) break;
-          // matrices in order: K0, K1 before V0 would need a fourth buffer, so V(i - 1) is waited for
-          // after K(i) only in the ring's own order K, V, K, V: V(i - 1) is number mat - 1
-          if (i > 0 && !mbar_wait_poll(&m_full[vslot], (mat - 1) / NM & 1u, abort_flag)) { give_up(); break; }
+        const int groups = it.rows > 128 ? 2 : 1, nh = 2 * it.nt;    // half tiles
+        if (nh == 0) continue;
+        // the first tile's scores; K is number mat, V number mat + 1 of the ring's matrices
+        if (!mbar_wait_poll(&m_full[mat % NM], mat / NM & 1u, abort_flag)) { give_up(); break; }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (x >= groups) break;
+          if (!mbar_wait_poll(&q_full[x], items[x] & 1u, abort_flag) ||
+              !mbar_wait_poll(&o_free[x], (items[x] & 1u) ^ 1u, abort_flag)) { give_up(); break; }
+          ++items[x];
+          tc_fence_after();
+          issued = true;
+          scores(x, 0, mat % NM);
+          scores(x, 1, mat % NM);
+        }
+        if (!ok) break;
+        commit_by(&m_empty[mat % NM], leader);
+        // P V of half tile j, then S of half tile j + 2 over that P
+        for (int j = 0; ok && j < nh; ++j) {
+          const uint32_t vn = mat + 1 + (j & ~1), kn = vn + 1, vslot = vn % NM, kslot = kn % NM;
+          if (!(j & 1) && !mbar_wait_poll(&m_full[vslot], vn / NM & 1u, abort_flag)) { give_up(); break; }
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             if (x >= groups) break;
-            if (i == 0) {
-              if (!mbar_wait_poll(&q_full[x], items[x] & 1u, abort_flag) ||
-                  !mbar_wait_poll(&o_free[x], (items[x] & 1u) ^ 1u, abort_flag)) { give_up(); break; }
-              ++items[x];
-            } else {
-              if (!mbar_wait_poll(&p_full[x], np[x] & 1u, abort_flag)) { give_up(); break; }
-              ++np[x];
-            }
+            const int b = 2 * x + (j & 1);
+            if (!mbar_wait_poll(&p_full[b], (j & 1 ? np[2 * x + 1] : np[2 * x]) & 1u, abort_flag)) { give_up(); break; }
+            if (j & 1) ++np[2 * x + 1]; else ++np[2 * x];
             tc_fence_after();
-            issued = true;
-            if (i > 0) {
-              const uint64_t vd = v_desc + (uint64_t)(vslot * (C::MAT / 16));
+            const uint64_t vd = v_desc + (uint64_t)(vslot * (C::MAT / 16) + (j & 1) * (64 * 128 / 16));
 #pragma unroll
-              for (int kk = 0; kk < 8; ++kk)                         // 16 keys: 16 rows of 128 bytes
-                umma_f16_ts(o_tm + D * x, s_tm + 128 * x + 8 * kk + 32 * (kk >> 2), vd + kk * 128, IDO, i > 1 || kk > 0, leader);
-              if (i == it.nt) commit_by(&o_done[x], leader);
-              if (x == groups - 1) commit_by(&m_empty[vslot], leader);   // K(i + 1) is written there while S is computed
-            }
-            if (i < it.nt) {
-              if (x == 0) {
-                if (!mbar_wait_poll(&m_full[kslot], mat / NM & 1u, abort_flag)) { give_up(); break; }
+            for (int kk = 0; kk < 4; ++kk)                           // 16 keys: 16 rows of 128 bytes
+              umma_f16_ts(o_tm + D * x, s_tm + 128 * x + 64 * (j & 1) + 8 * kk, vd + kk * 128, IDO, j > 0 || kk > 0,
+                          leader);
+            commit_by(&o_done[x], leader);
+            if (j == nh - 1) commit_by(&o_last[x], leader);
+            if ((j & 1) && x == groups - 1) commit_by(&m_empty[vslot], leader);
+            if (j + 2 < nh) {
+              if (x == 0 && !(j & 1)) {
+                if (!mbar_wait_poll(&m_full[kslot], kn / NM & 1u, abort_flag)) { give_up(); break; }
                 tc_fence_after();
               }
-              const uint64_t kd = k_desc + (uint64_t)(kslot * (C::MAT / 16)), qd = q_desc + (uint64_t)(x * (C::MAT / 16));
-#pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk)
-                umma_f16_ss(s_tm + 128 * x, qd + (kk >> 2) * (C::BOX / 16) + 2 * (kk & 3), kd + (kk >> 2) * (C::BOX / 16) + 2 * (kk & 3),
-                            IDS, kk > 0, leader);
-              commit_by(&s_full[x], leader);
+              scores(x, j, kslot);
+              if ((j & 1) && x == groups - 1) commit_by(&m_empty[kslot], leader);
             }
           }
-          if (!ok) break;
-          if (i < it.nt) {
-            commit_by(&m_empty[kslot], leader);
-            mat += 2;                                                // this tile's K and V
-          }
         }
+        mat += 2 * (uint32_t)it.nt;
       }
       if (issued) {
         commit_by(drain, leader);
@@ -361,25 +372,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
       }
     }
   } else {
-    // ---------------- softmax: half a query row per thread, group x ----------------
+    // ---------------- softmax: a query row per thread, group x ----------------
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_SOFT));
-    const int x = (warp - SOFT0) >> 3, half = (warp >> 2) & 1, r = 32 * (warp & 3) + lane;      // this group's row
+    const int x = (warp - SOFT0) >> 2, r = tid - 32 * SOFT0 - 128 * x;          // this group's row
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t st = s_tm + 128 * x + 64 * half + lanes, ot = o_tm + D * x + (D / 2) * half + lanes;
-    uint64_t* both = &told[4 * x + (warp & 3)];
-    const uint32_t mine = smem_u32(smem) + C::ROWS + 8 * (128 * x + r) + 4 * half, theirs = mine ^ 4u;
-    uint32_t nt = 0;                                                 // times the halves have told each other something
-    auto tell = [&](float v, float& w) {                             // v to the other half of the row, w from it
-      const uint32_t at = nt & 1u ? 2048u : 0u;
-      asm volatile("st.shared.f32 [%0], %1;" ::"r"(mine + at), "f"(v) : "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(both);
-      if (!mbar_wait_poll(both, nt & 1u, abort_flag)) return false;
-      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(w) : "r"(theirs + at) : "memory");
-      ++nt;
-      return true;
-    };
-    uint32_t ns = 0, no = 0;                                         // tiles whose S, items whose O this group has waited for
+    const uint32_t st0 = s_tm + 128 * x + lanes, ot = o_tm + D * x + lanes;
+    uint32_t ns[2] = {0, 0}, npv = 0, no = 0;                        // waits for S by half tile; half tiles whose P V was asked for; items
     int4 cut = make_int4(0, 0, 0, 0);
     while (ok && line.next(p, it, err)) {
       if (it.more) cut = make_int4(it.b, it.item, 1 + it.more, 0);
@@ -415,7 +413,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
         rowc = p.scale_log2 * pow2(-e);
         const uint32_t dst = smem_u32(smem) + x * C::MAT + r * 128;
 #pragma unroll 4
-        for (int c = half * (D / 16); c < (half + 1) * (D / 16); ++c) {
+        for (int c = 0; c < D / 8; ++c) {
           uint4 w = make_uint4(0u, 0u, 0u, 0u);
           if (row_ok) w = *reinterpret_cast<const uint4*>(qp + 8 * c);
           float v[8];
@@ -430,13 +428,15 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
         if (lane == 0 && it.nt > 0) mbar_arrive(&q_full[x]);
       }
       float mrc = 0.0f, thr = -CUDART_INF_F, l = 0.0f;               // maximum in log2 units (0: none yet), its limit, the sum
-      for (int i = 0; i < it.nt; ++i) {
-        if (!mbar_wait_bounded(&s_full[x], ns & 1u, abort_flag)) { give_up(); break; }
-        ++ns;
+      for (int j = 0; j < 2 * it.nt; ++j) {
+        const int b = j & 1;
+        if (!mbar_wait_bounded(&s_full[2 * x + b], (b ? ns[1] : ns[0]) & 1u, abort_flag)) { give_up(); break; }
+        if (b) ++ns[1]; else ++ns[0];
         tc_fence_after();
-        const int key0 = (it.tl + i) * TILE;
-        const bool masked = key0 < lo_max || key0 + TILE > hi_min;
-        const int u_lo = lo - key0 - 64 * half, u_hi = hi - key0 - 64 * half;          // columns the row sees
+        const uint32_t st = st0 + 64 * b;
+        const int key0 = it.tl * TILE + 64 * j;
+        const bool masked = key0 < lo_max || key0 + 64 > hi_min;
+        const int u_lo = lo - key0, u_hi = hi - key0;                // columns the row sees
         // One pass computes the probabilities from the maximum so far and this tile's maximum. Only
         // where that is more than 2^kSlack above (an item's first tile, seldom later) the row moves
         // its maximum and the pass is done again.
@@ -444,20 +444,20 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
         float s0, s1;
 #pragma unroll 1
         for (;;) {
-          const float b = kShift - mrc;
-          const uint64_t b2 = pair(b, b), rowc2 = pair(rowc, rowc);
+          const float sh = kShift - mrc;
+          const uint64_t b2 = pair(sh, sh), rowc2 = pair(rowc, rowc);
           uint64_t sum[2] = {0, 0};
           float m4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
           uint32_t s[2][CH];
-          tmem_ld_32x32b_x16_nowait(st, s[0]);
+          tmem_ld32(st, s[0]);
 #pragma unroll
           for (int c = 0; c < 64; c += CH) {
             uint32_t* v = s[c / CH & 1];
             tmem_ld_wait<CH>(v);
-            if (c + CH < 64) tmem_ld_32x32b_x16_nowait(st + c + CH, s[1 - (c / CH & 1)]);
+            if (c + CH < 64) tmem_ld32(st + c + CH, s[1 - (c / CH & 1)]);
             if (masked) {
               const int a = u_lo - c, z = u_hi - c;
-              constexpr uint32_t all = (1u << CH) - 1u;
+              constexpr uint32_t all = 0xFFFFFFFFu >> (32 - CH);
               const uint32_t see = (a >= CH || z < 0) ? 0u : (a > 0 ? all << a : all) & (z < CH - 1 ? all >> (CH - 1 - z) : all);
 #pragma unroll
               for (int k = 0; k < CH; ++k)
@@ -475,10 +475,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
             }
           }
           halves(add2(sum[0], sum[1]), s0, s1);
-          const float mh = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
-          float mx;
-          if (!tell(mh, mx)) { ok = false; break; }
-          mx = fmaxf(mx, mh) * rowc;
+          const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * rowc;
           const bool over = mx > thr;
           if (!__any_sync(0xffffffffu, over)) break;
           float f = 1.0f;
@@ -488,10 +485,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
             thr = mx + kSlack;
             l *= f;
           }
-          if (i > 0) {
-            // O is this group's own: the last P V was issued before this S, so it is done
+          if (j > 0) {
+            // O is this group's own; the P V before has to be done (the one before that is: this S was
+            // issued after it, so the barrier is at this phase or past it)
+            if (!mbar_wait_bounded(&o_done[x], (npv - 1) & 1u, abort_flag)) { ok = false; break; }
+            tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < D / 2; c += 8) {
+            for (int c = 0; c < D; c += 8) {
               uint32_t o[8];
               tmem_ld8(ot + c, o);
               tmem_ld_wait<8>(o);
@@ -503,26 +503,25 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
         }
         if (!ok) { give_up(); break; }
         l += s0 + s1;
-        tmem_st32(st, pw);                       // over this half's own scores
+        tmem_st32(st, pw);                       // over scores that have been read
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[x]);
+        if (lane == 0) mbar_arrive(&p_full[2 * x + b]);
+        ++npv;
       }
       if (!ok) break;
       // ---- the item's output
       if (it.nt > 0) {
-        float lh;
-        if (!mbar_wait_bounded(&o_done[x], no & 1u, abort_flag) || !tell(l, lh)) { give_up(); break; }
+        if (!mbar_wait_bounded(&o_last[x], no & 1u, abort_flag)) { give_up(); break; }
         ++no;
-        l += lh;
         tc_fence_after();
       }
       const long long at = (it.sq.tok0 + tk) * p.ldo + (long long)hq * D;
       float* out = p.part + (2LL * blockIdx.x + (it.lead ? 0 : 1)) * C::PART;
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll 1
-      for (int c = 0; c < D / 2; c += 16) {
+      for (int c = 0; c < D; c += 16) {
         uint32_t o[16];
         if (it.nt > 0) {
           tmem_ld8(ot + c, o);
@@ -536,12 +535,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
           const int e = (k & ~7) + (k >> 2 & 1);                     // column j of eight lies at 2 (j mod 4) + j / 4
           float4 w = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 2]), __uint_as_float(o[e + 4]), __uint_as_float(o[e + 6]));
           if (l == 0.0f) w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);    // no key seen: O may never have been written
-          const int col = half * (D / 2) + c + k;
+          const int col = c + k;
           if (it.whole) store_out(p, at + col, make_float4(w.x * inv, w.y * inv, w.z * inv, w.w * inv));
           else *reinterpret_cast<float4*>(out + (128 * x + r) * D + col) = w;
         }
       }
-      if (row_ok && half == 0) {
+      if (row_ok) {
         if (it.whole) {
           if (p.lse) p.lse[(it.sq.tok0 + tk) * p.Hq + hq] = l == 0.0f ? -CUDART_INF_F : (mrc - kShift + log2f(l)) * 0.6931471805599453f;
         } else {
