@@ -20,7 +20,7 @@
 //     brought to the top of fp16's range by a power of two that follows the largest V scale
 //     seen, so small probabilities keep their bits down to 2^-24 of the largest.
 //   Why mma.sync and not tcgen05: the product is bound by HBM bandwidth (one pass over the
-//   cache for at most 32 rows), and tcgen05 would need the codes unpacked to 16 bits in
+//   cache for at most 16 or 32 rows), and tcgen05 would need the codes unpacked to 16 bits in
 //   shared memory, four times the bytes that come from HBM, where here they go from the
 //   packed words to the tensor core through registers.
 //
@@ -525,15 +525,15 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, NT>::OCC) kv_split_kernel(Para
 }
 
 // Query rows of one head that a CTA takes at once: the eight columns of an n-tile times NT.
-int row_tiles(int D, long long rows) { return rows <= 8 ? 1 : (rows <= 16 || D == 256 ? 2 : 4); }
+int row_tiles(int D, long long rows) { return rows <= 8 ? 1 : (rows <= 16 || D != 64 ? 2 : 4); }
 
 template <typename F>
 void with_shape(int D, int nt, F&& f) {
   auto go = [&](auto d) {
     constexpr int DD = decltype(d)::value;
     if (nt == 1) f(d, std::integral_constant<int, 1>{});
-    else if (nt == 2 || DD == 256) f(d, std::integral_constant<int, 2>{});
-    else if constexpr (DD != 256) f(d, std::integral_constant<int, 4>{});
+    else if (nt == 2 || DD != 64) f(d, std::integral_constant<int, 2>{});
+    else if constexpr (DD == 64) f(d, std::integral_constant<int, 4>{});
   };
   if (D == 64) go(std::integral_constant<int, 64>{});
   else if (D == 128) go(std::integral_constant<int, 128>{});
@@ -543,12 +543,12 @@ void with_shape(int D, int nt, F&& f) {
 }  // namespace kva
 
 // Which kernel: many rows of a head at once are worth dequantizing a tile into shared memory for the
-// large tensor-core tiles; this one streams the cache again for every 32 rows. (Heads of 256 do
-// not fit the other's tensor memory.) Measured at D = 128, in us, this one / the other: 32 sequences of
-// 1024 tokens and 8 kv heads, 32 rows a head 57 / 68, 48 rows 123 / 70, 128 rows 213 / 80; one sequence of
-// 8192, 32 rows 47 / 39, 64 rows 47 / 41, 128 rows 68 / 51. At D = 64: 32 rows 31 / 51, 48 rows 70 / 53.
-constexpr long long kManyRows = 32;
-static bool many_rows(int D, long long rows) { return D != 256 && rows > kManyRows; }
+// large tensor-core tiles; this one streams the cache again for its most rows each. (Heads of 256
+// do not fit the other's tensor memory.) Measured over 8 kv heads, in us, this one / the other: D = 128, 32
+// sequences of 1024 tokens, 16 rows a head 25 / 57, 32 rows 57 / 57, 64 rows 129 / 59; 8 of 2048, 16 rows
+// 23 / 37, 32 rows 47 / 37; one of 8192, 16 rows 23 / 31, 32 rows 45 / 31. D = 64, 32 of 1024: 32 rows 31 / 45, 48
+// rows 70 / 45; one of 8192: 32 rows 30 / 27.
+static bool many_rows(int D, long long rows) { return D != 256 && rows > (D == 64 ? 32 : 16); }
 
 size_t kv_attention_tc_workspace_bytes(int D);
 gptq_status kv_attention_tc_launch(const kva::Params& p, int D, void* ws, cudaStream_t s);
