@@ -163,6 +163,11 @@ __device__ __forceinline__ void find_start(const Params& p, long long* sh, long 
   off = sh[13];
 }
 
+// A head's row tiles are taken from both ends in turn: under a causal mask the first rows see the fewest
+// keys and the last the most, while the line counts every item's tiles alike. (A prompt of 4096 tokens, 64 + 8
+// heads of 128: 543 us in order, 381 this way; 1024 tokens over 8187 keys 281, 268.)
+__device__ __forceinline__ int row_tile(int k, int nrt) { return k & 1 ? nrt - 1 - (k >> 1) : k >> 1; }
+
 // One item, or the part of it that a CTA takes.
 struct Item {
   Seq sq;
@@ -204,7 +209,7 @@ struct Line {
       it.b = b;
       it.item = (int)item;
       it.h = it.item / q.nrt;
-      it.rt = it.item - it.h * q.nrt;
+      it.rt = row_tile(it.item - it.h * q.nrt, q.nrt);
       const long long rest = (long long)q.nq * p.G - (long long)it.rt * R;
       it.rows = (int)(rest < R ? rest : R);
       it.i0 = it.rt * R / p.G;
@@ -282,7 +287,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) kv_join_kernel(Params p, int*
   const int4 cut = p.cut[c];
   if (cut.z == 0) return;
   const Seq sq = load_seq(p, cut.x, R, err);
-  const int h = cut.y / sq.nrt, rt = cut.y - h * sq.nrt, np = cut.z;
+  const int h = cut.y / sq.nrt, rt = row_tile(cut.y - h * sq.nrt, sq.nrt), np = cut.z;
   const long long all_rows = (long long)sq.nq * p.G;
   auto part_of = [&](int k) { return p.part + (2LL * (c + k) + (k == 0 ? 1 : 0)) * PART; };
   float mm, ll, acc[VPL];
