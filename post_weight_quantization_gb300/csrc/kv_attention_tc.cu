@@ -25,8 +25,9 @@
 // a time and leave as probabilities from the maximum so far. (Two threads per row, which tell each
 // other their maxima, took 341 us with half tiles: what is done per half tile then counts twice.)
 // Bound: the tensor cores' 4 rows keys D operations; measured, 1024 tokens over 8187 keys, 64 + 8 heads of
-// 128: 269 us, 47 % of the measured bf16 rate with the join's launch. Per 256 rows and 128 keys it takes 3900
-// cycles, of which 2048 are MMAs; the softmax warps' own latency is the rest.
+// 128: 257 us, the call with the join 267 us, 49 % of the measured bf16 rate (with row tiles in order: 269
+// and 279). Per 256 rows and 128 keys it takes 3700 cycles, of which 2048 are MMAs; the softmax warps' own
+// latency is the rest.
 // The tiles of all items form a line that is cut evenly over one CTA per SM, as in the other
 // kernel, and cut items are joined afterwards.
 #include "kv_line.cuh"
