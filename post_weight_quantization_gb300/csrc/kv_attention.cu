@@ -431,7 +431,10 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, NT>::OCC) kv_split_kernel(Para
         chunk<D, NT, false>(st, base + koff[0], base + koff[1], base + noff[0], base + noff[1], p.pb, key0, g, t);
       else if (key0 < it.hi_all && key0 + KC > it.lo_all)
         chunk<D, NT, true>(st, base + koff[0], base + koff[1], base + noff[0], base + noff[1], p.pb, key0, g, t);
-      __syncwarp();                              // every lane has read its part of the stage
+      // the stage's words have been read: without the fence nothing keeps the next copy, which is
+      // another proxy's write, behind loads that are still on their way to the MMAs
+      fence_proxy_async_smem();
+      __syncwarp();
       if (lane == 0) mbar_arrive(&empty[slot]);
       ++use;
       if (++slot == NS) {

@@ -539,3 +539,82 @@ def test_attention_piece_with_cold_caches(g, hq, h, D, page):
         assert torch.equal(O, want), i
     done(g)
     t.check(want, heads=(0, hq - 1))
+
+
+# ------------------------------------------------------------------ attention over long caches
+class Long:
+    """One long sequence's cache, which all sequences of a batch share through their tables (sequence b
+    sees its first lens[b] tokens), and attention over it in float64 on the GPU. The cached values
+    are those that gptq_kv_read gives; the bounds are the ones above. Values of V move with their tile of
+    128 keys, so that a tile that is lost or counted twice moves the output, and lse moves by the tile's
+    share of the softmax."""
+
+    def __init__(self, g, n, h, D, page, seed=0):
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        self.n, self.h, self.D, self.page = n, h, D, page
+        pages = -(-n // page)
+        self.order = torch.randperm(pages, device="cuda", generator=gen)
+        self.cache = g.KVCache(torch.full((pages, h, page * (D + 8)), 0xFF, dtype=torch.uint8, device="cuda"), page, h, D)
+        at = torch.arange(n, device="cuda")
+        slots = self.order[at // page] * page + at % page
+        K = torch.randn((n, h, D), device="cuda", generator=gen)
+        V = torch.randn((n, h, D), device="cuda", generator=gen) + 3 * torch.randn((n // 128 + 1, 1, D), device="cuda",
+                                                                                   generator=gen)[at // 128]
+        g.gptq_kv_append(self.cache, K, V, slots)
+        self.k, self.v = (x.double() for x in g.gptq_kv_read(self.cache, slots, dtype=torch.float32))
+        num = self.cache.pool[..., page * D:].contiguous().view(torch.float16).view(pages, h, page, 4).double()
+        self.num = num[slots // page, :, slots % page]                       # (n, h, 4)
+        self.gen = gen
+
+    def batch(self, lens, new, hq, dtype=torch.bfloat16):
+        """Queries of a batch and what the call reads beside them."""
+        self.lens, self.hq, self.cu = lens, hq, [0]
+        for x in new:
+            self.cu.append(self.cu[-1] + x)
+        self.Q = torch.randn((self.cu[-1], hq, self.D), device="cuda", generator=self.gen).to(dtype)
+        self.Q[::3] *= 4                                                    # some rows are peaked
+        ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+        return self.cache, self.Q, ints(self.cu), ints(lens), self.order.int()[None].repeat(len(lens), 1)
+
+    def check(self, O, lse, seqs, heads, causal=True, window=0):
+        sm, G = self.D ** -0.5, self.hq // self.h
+        for b in seqs:
+            n, a, z = self.lens[b], self.cu[b], self.cu[b + 1]
+            pos = torch.arange(n - (z - a), n, device="cuda")[:, None]
+            key = torch.arange(n, device="cuda")[None]
+            see = (key <= pos if causal else key >= 0) & ((key > pos - window) if window else (key >= 0))
+            for y in heads:
+                k, v, num = self.k[:n, y // G], self.v[:n, y // G], self.num[:n, y // G]
+                q = self.Q[a:z, y].double()
+                s = (sm * (q @ k.T)).masked_fill(~see, -float("inf"))
+                l = torch.logsumexp(s, 1)
+                p = torch.where(see, torch.exp(s - l[:, None]), 0.0)
+                ref, mag = p @ v, p @ (v.abs() + 2 * num[:, 3:].abs())
+                d_s = (self.D + 8) * 2.0 ** -22 * sm * q.abs().sum(1, keepdim=True) * (15 * num[:, 0] + num[:, 1].abs()).max()
+                bound = ((2.0 ** -11 + 2 * d_s + 2.0 ** -18) * mag + HALF_ULP[O.dtype] * ref.abs() * (1 + 2.0 ** -6)
+                         + TINY[O.dtype])
+                err = (O[a:z, y].double() - ref).abs()
+                assert (err <= bound).all(), (b, y, float((err / bound).max()))
+                dl = (lse[a:z, y].double() - l).abs()
+                assert (dl <= d_s[:, 0] + 2.0 ** -18 + 2.0 ** -22 * l.abs()).all(), (b, y, float(dl.max()))
+
+
+@pytest.mark.parametrize("hq,h,D,page,new", [(4, 4, 64, 16, 1), (32, 4, 64, 32, 1), (4, 4, 128, 16, 1), (32, 4, 128, 64, 1),
+                                             (4, 4, 256, 32, 1), (32, 4, 256, 16, 1), (16, 4, 64, 64, 8), (12, 4, 256, 64, 5)])
+def test_attention_few_rows_with_cold_caches(g, hq, h, D, page, new):
+    """The kernel of few rows a head, whose ring of tiles is filled anew several times by every CTA, with
+    everything evicted in between: the same bits each time, one row a head and more."""
+    t = Long(g, 9001, h, D, page, seed=D + hq)
+    lens = [9001 - 61 * i for i in range(24)]
+    args = t.batch(lens, [new] * 24, hq)
+    evict = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    lse = torch.empty((24 * new, hq), device="cuda")
+    want = None
+    for i in range(30):
+        evict.fill_(i)
+        O = g.gptq_kv_attention(*args, new, lse=lse)
+        if want is None:
+            want = O
+        assert torch.equal(O, want), i
+    done(g)
+    t.check(want, lse, (0, 9, 23), (0, hq - 1))
