@@ -209,9 +209,24 @@ def gptq_workspace_size(which: int, m: int, d: int, bits: int = 4, group_size: i
     return int(_lib.gptq_workspace_size(which, m, d, bits, group_size, blocksize))
 
 
-def _workspace(nbytes: int, device) -> torch.Tensor:
+def _empty(shape, dtype, device, stream=None, keep: bool = True) -> torch.Tensor:
+    """torch.empty for work on `stream`. A block that the current stream's pool hands out may still be
+    in use by what that stream has queued, which another stream does not wait for: so the memory is
+    taken from the pool of the stream that works on it. With `keep` the caller gets the tensor, and its
+    memory is not given out again before the current stream's work at that time is done either."""
+    if stream is None or _stream(stream) == _stream(None):
+        return torch.empty(shape, dtype=dtype, device=device)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(s):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if keep:
+        t.record_stream(torch.cuda.current_stream())
+    return t
+
+
+def _workspace(nbytes: int, device, stream=None) -> torch.Tensor:
     # torch's allocator returns 512-byte aligned blocks, above the 256 bytes the ABI needs
-    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    return _empty(max(nbytes, 256), torch.uint8, device, stream, keep=False)
 
 
 def gptq_hessian_accumulate(X: torch.Tensor, H: torch.Tensor, alpha: float = 2.0, zero_first: bool = False,
@@ -473,15 +488,6 @@ def _same_device(dev: int, *tensors) -> None:
         _one_device(*tensors)
 
 
-def _keep(stream, *tensors) -> None:
-    """Tensors allocated here for work on a stream other than the current one: their memory is
-    not given out again before that work is done."""
-    if stream is not None and _stream(stream) != _stream(None):
-        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
-        for t in tensors:
-            t.record_stream(s)
-
-
 def gptq_adapter_linear(q: "QuantizedLayer", X: torch.Tensor, m: int, A: Optional[torch.Tensor] = None,
                         B: Optional[torch.Tensor] = None, ids: Optional[torch.Tensor] = None,
                         alpha: Optional[torch.Tensor] = None, Y: Optional[torch.Tensor] = None, out_bf16: bool = False,
@@ -525,18 +531,15 @@ def gptq_adapter_linear(q: "QuantizedLayer", X: torch.Tensor, m: int, A: Optiona
     dev = X.device
     ydt = torch.bfloat16 if out_bf16 else torch.float32
     if Y is None:
-        Y = torch.empty((T, m), dtype=ydt, device=dev)
-        _keep(stream, Y)
+        Y = _empty((T, m), ydt, dev, stream)
     else:
         _need_cuda(Y, "Y", (ydt,))
         if Y.dim() != 2 or tuple(Y.shape) != (T, m) or Y.stride(1) != 1:
             raise ValueError(f"Y must be ({T}, {m}) with unit column stride, got {tuple(Y.shape)}")
     need = _lib.gptq_adapter_workspace_size(m, d, bits, gs, T, rank)
     if ws is None:
-        ws, ws_bytes = torch.empty(max(need, 256), dtype=torch.uint8, device=dev), max(need, 256)
-        _keep(stream, ws)
-    else:
-        ws_bytes = _need_workspace(ws, need)
+        ws = _workspace(need, dev, stream)
+    ws_bytes = _need_workspace(ws, need)
     _same_device(X.get_device(), qweight, scales, zeros, X, A, B, ids, alpha, Y, ws)
     st = _lib.gptq_adapter_linear(qweight.data_ptr(), scales.data_ptr(), zeros.data_ptr(), m, d, bits, gs, X.data_ptr(), T,
                                   X.stride(0) if T > 1 else d, _ptr(A), _ptr(B), _ptr(alpha), n, rank, _ptr(ids),
@@ -574,14 +577,12 @@ def gptq_qk_norm_rope(Q: torch.Tensor, K: Optional[torch.Tensor], positions: Opt
     if odt not in _DTYPE:
         raise TypeError(f"out_dtype must be one of {_ALL}, got {odt}")
     if Q_out is None:
-        Q_out, ldqo = torch.empty((T, hq, dim), dtype=odt, device=dev), hq * dim
-        _keep(stream, Q_out)
+        Q_out, ldqo = _empty((T, hq, dim), odt, dev, stream), hq * dim
     else:
         ldqo = _heads(Q_out, "Q_out", (odt,), T, hq, dim)
     if K is not None:
         if K_out is None:
-            K_out, ldko = torch.empty((T, hk, dim), dtype=odt, device=dev), hk * dim
-            _keep(stream, K_out)
+            K_out, ldko = _empty((T, hk, dim), odt, dev, stream), hk * dim
         else:
             ldko = _heads(K_out, "K_out", (odt,), T, hk, dim)
     rot = n_pos = 0
@@ -662,13 +663,11 @@ def gptq_kv_read(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torch
         raise TypeError(f"dtype must be one of {_ALL}, got {dtype}")
     dev = pool.device
     if K is None:
-        K, ldk = torch.empty((T, h, dim), dtype=dtype, device=dev), h * dim
-        _keep(stream, K)
+        K, ldk = _empty((T, h, dim), dtype, dev, stream), h * dim
     else:
         ldk = _heads(K, "K", (dtype,), T, h, dim)
     if V is None:
-        V, ldv = torch.empty((T, h, dim), dtype=dtype, device=dev), h * dim
-        _keep(stream, V)
+        V, ldv = _empty((T, h, dim), dtype, dev, stream), h * dim
     else:
         ldv = _heads(V, "V", (dtype,), T, h, dim)
     _same_device(pool.get_device(), pool, slots, K, V)
@@ -708,18 +707,15 @@ def gptq_kv_attention(cache: KVCache, Q: torch.Tensor, cu_q: torch.Tensor, kv_le
     _dense(kv_lens, "kv_lens", (batch,), torch.int32)
     dtype, dev = Q.dtype, Q.device
     if O is None:
-        O, ldo = torch.empty((total, hq, dim), dtype=dtype, device=dev), hq * dim
-        _keep(stream, O)
+        O, ldo = _empty((total, hq, dim), dtype, dev, stream), hq * dim
     else:
         ldo = _heads(O, "O", (dtype,), total, hq, dim)
     if lse is not None:
         _dense(lse, "lse", (total, hq), torch.float32)
     need = _lib.gptq_kv_attention_workspace_size(total, hq, h, dim, batch, max_q)
     if ws is None:
-        ws, ws_bytes = torch.empty(max(need, 256), dtype=torch.uint8, device=dev), max(need, 256)
-        _keep(stream, ws)
-    else:
-        ws_bytes = _need_workspace(ws, need)
+        ws = _workspace(need, dev, stream)
+    ws_bytes = _need_workspace(ws, need)
     _same_device(Q.get_device(), pool, Q, cu_q, kv_lens, block_table, O, lse, ws)
     st = _lib.gptq_kv_attention(Q.data_ptr(), _DTYPE[dtype], total, hq, h, dim, ldq, cu_q.data_ptr(), kv_lens.data_ptr(),
                                 block_table.data_ptr(), ldt if batch > 1 else width, width, batch, max_q, pool.data_ptr(),

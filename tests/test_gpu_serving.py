@@ -618,3 +618,53 @@ def test_attention_few_rows_with_cold_caches(g, hq, h, D, page, new):
         assert torch.equal(O, want), i
     done(g)
     t.check(want, lse, (0, 9, 23), (0, hq - 1))
+
+
+# ------------------------------------------------------------------ memory of calls on another stream
+def _on_another_stream(call, sizes):
+    """call(stream) while the current stream is still to write blocks of the sizes that the call
+    allocates, blocks that have been given back already. Returns call's result."""
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    blocks = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(2)]
+    torch.cuda._sleep(200_000_000)
+    for b in blocks:
+        b.fill_(0x55)
+    del blocks, b
+    out = call(side)
+    side.synchronize()
+    assert not torch.cuda.current_stream().query()              # what it queued is still to come
+    torch.cuda.synchronize()
+    return out
+
+
+def test_serving_memory_of_another_stream(g):
+    """Outputs and workspaces of calls on another stream than the current one are not memory that
+    the current stream has yet to write."""
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    rnd = lambda *s: torch.randn(s, generator=gen, device="cuda").bfloat16()
+    T, hq, hk, D, page, m, d, rank = 300, 8, 2, 64, 16, 256, 512, 16
+    Q, K, V, X = rnd(T, hq, D), rnd(T, hk, D), rnd(T, hk, D), rnd(T, d)
+    w = torch.rand(D, generator=gen, device="cuda")
+    cache = g.KVCache.empty(20, page, hk, D)
+    slots = torch.arange(T, device="cuda")
+    g.gptq_kv_append(cache, K, V, slots)
+    cu, lens = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([0, T], [T]))
+    table = torch.arange(20, dtype=torch.int32, device="cuda")[None]
+    q = g.QuantizedLayer(torch.randint(-2 ** 31, 2 ** 31 - 1, (m, d // 8), generator=gen, dtype=torch.int32, device="cuda"),
+                         torch.rand((m, 4), generator=gen, device="cuda"), torch.full((m, 4), 8.0, device="cuda"), None, 4, 128, d)
+    A, B, ids = rnd(3, rank, d), rnd(3, m, rank), torch.arange(T, dtype=torch.int32, device="cuda") // 100
+    lib = g.library()
+    calls = {
+        "norm": (lambda s: g.gptq_qk_norm_rope(Q, K, wq=w, wk=w, stream=s), [2 * T * hq * D, 2 * T * hk * D]),
+        "read": (lambda s: g.gptq_kv_read(cache, slots, stream=s), [2 * T * hk * D]),
+        "attention": (lambda s: (g.gptq_kv_attention(cache, Q, cu, lens, table, T, stream=s),),
+                      [2 * T * hq * D, lib.gptq_kv_attention_workspace_size(T, hq, hk, D, 1, T)]),
+        "adapter": (lambda s: (g.gptq_adapter_linear(q, X, m, A, B, ids, stream=s),),
+                    [4 * T * m, lib.gptq_adapter_workspace_size(m, d, 4, 128, T, rank)]),
+    }
+    for name, (call, sizes) in calls.items():
+        want = call(None)
+        for a, b in zip(want, _on_another_stream(call, sizes)):
+            assert torch.equal(a, b), name
+    done(g)
