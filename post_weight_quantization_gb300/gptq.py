@@ -263,15 +263,15 @@ def gptq_factor(H: torch.Tensor, percdamp: float = 0.01, act_order: bool = False
         raise ValueError("H must be a contiguous d x d tensor")
     dev = H.device
     if Hinv1 is None:
-        Hinv1 = torch.empty((d, d), dtype=torch.float32, device=dev)
+        Hinv1 = _empty((d, d), torch.float32, dev, stream)
     _need_buffer(Hinv1, "Hinv1", (d, d), (torch.float32,))
     if act_order:
         if perm_out is None:
-            perm_out = torch.empty(d, dtype=torch.int32, device=dev)
+            perm_out = _empty((d,), torch.int32, dev, stream)
         _need_buffer(perm_out, "perm_out", (d,), (torch.int32,))
     need = gptq_workspace_size(GPTQ_WS_FACTOR, 0, d)
     if ws is None:
-        ws = _workspace(need, dev)
+        ws = _workspace(need, dev, stream)
     ws_bytes = _need_workspace(ws, need)
     _one_device(H, Hinv1, perm_out if act_order else None, ws)
     info = _c_i64(-1)
@@ -331,10 +331,10 @@ def gptq_quantize_layer(W: torch.Tensor, Hinv1: torch.Tensor, perm: Optional[tor
     G = 1 if group_size == -1 else (d // group_size if group_size > 0 else 1)
     if out is None:
         out = QuantizedLayer(
-            qweight=torch.empty((m, (d * bits + 31) // 32), dtype=torch.int32, device=dev),
-            scales=torch.empty((m, G), dtype=torch.float32, device=dev),
-            zeros=torch.empty((m, G), dtype=torch.float32, device=dev),
-            col_losses=torch.empty(d, dtype=torch.float32, device=dev),
+            qweight=_empty((m, (d * bits + 31) // 32), torch.int32, dev, stream),
+            scales=_empty((m, G), torch.float32, dev, stream),
+            zeros=_empty((m, G), torch.float32, dev, stream),
+            col_losses=_empty((d,), torch.float32, dev, stream),
             bits=bits, group_size=group_size, d=d)
     if (out.bits, out.group_size, out.d) != (bits, group_size, d):
         raise ValueError(f"out describes bits={out.bits}, group_size={out.group_size}, d={out.d}; "
@@ -345,7 +345,7 @@ def gptq_quantize_layer(W: torch.Tensor, Hinv1: torch.Tensor, perm: Optional[tor
     _need_buffer(out.col_losses, "out.col_losses", (d,), (torch.float32,))
     need = gptq_workspace_size(GPTQ_WS_QUANTIZE, m, d, bits, group_size, blocksize)
     if ws is None:
-        ws = _workspace(need, dev)
+        ws = _workspace(need, dev, stream)
     ws_bytes = _need_workspace(ws, need)
     _one_device(W, Hinv1, perm, out.qweight, out.scales, out.zeros, out.col_losses, ws)
     info = _c_i64(0)
@@ -360,7 +360,7 @@ def gptq_quantize_layer(W: torch.Tensor, Hinv1: torch.Tensor, perm: Optional[tor
 def gptq_unpack_codes(qweight: torch.Tensor, m: int, d: int, bits: int, stream=None) -> torch.Tensor:
     _need_rows(qweight, "qweight", m, (d * bits + 31) // 32, (torch.int32,))
     _one_device(qweight)
-    codes = torch.empty((m, d), dtype=torch.uint8, device=qweight.device)
+    codes = _empty((m, d), torch.uint8, qweight.device, stream)
     _check(_lib.gptq_unpack_codes(_ptr(qweight), m, d, bits, _ptr(codes), _stream(stream)), "gptq_unpack_codes")
     return codes
 
@@ -379,7 +379,7 @@ def gptq_dequant_gemv(q: "QuantizedLayer", X: torch.Tensor, m: int, g_idx: Optio
         _need_buffer(g_idx, "g_idx", (q.d,), (torch.int32,))
     T = X.shape[0]
     if Y is None:
-        Y = torch.empty((T, m), dtype=torch.float32, device=X.device)
+        Y = _empty((T, m), torch.float32, X.device, stream)
     _need_cuda(Y, "Y", (torch.float32,))
     if Y.dim() != 2 or tuple(Y.shape) != (T, m) or Y.stride(1) != 1:
         raise ValueError(f"Y must be ({T}, {m}) with unit column stride, got {tuple(Y.shape)}")
@@ -404,13 +404,13 @@ def gptq_dequant_gemm(q: "QuantizedLayer", X: torch.Tensor, m: int, Y: Optional[
     T = X.shape[0]
     ydt = torch.bfloat16 if out_bf16 else torch.float32
     if Y is None:
-        Y = torch.empty((T, m), dtype=ydt, device=X.device)
+        Y = _empty((T, m), ydt, X.device, stream)
     _need_cuda(Y, "Y", (ydt,))
     if Y.dim() != 2 or tuple(Y.shape) != (T, m) or Y.stride(1) != 1:
         raise ValueError(f"Y must be ({T}, {m}) with unit column stride, got {tuple(Y.shape)}")
     need = gptq_workspace_size(GPTQ_WS_DEQUANT_GEMM, m, q.d)
     if ws is None:
-        ws = _workspace(need, X.device)
+        ws = _workspace(need, X.device, stream)
     ws_bytes = _need_workspace(ws, need)
     _one_device(q.qweight, q.scales, q.zeros, X, Y, ws)
     st = _lib.gptq_dequant_gemm(_ptr(q.qweight), _ptr(q.scales), _ptr(q.zeros), m, q.d, q.bits, q.group_size,
@@ -734,7 +734,7 @@ def quantize_layer(W: torch.Tensor, X_batches, bits: int = 4, group_size: int = 
     Returns (QuantizedLayer, H, Hinv1, perm).
     """
     d = W.shape[1]
-    H = torch.empty((d, d), dtype=torch.float32, device=W.device)
+    H = _empty((d, d), torch.float32, W.device, stream)
     first = True
     for X in X_batches:
         gptq_hessian_accumulate(X, H, alpha=alpha, zero_first=first, stream=stream)

@@ -623,18 +623,21 @@ def test_attention_few_rows_with_cold_caches(g, hq, h, D, page, new):
 # ------------------------------------------------------------------ memory of calls on another stream
 def _on_another_stream(call, sizes):
     """call(stream) while the current stream is still to write blocks of the sizes that the call
-    allocates, blocks that have been given back already. Returns call's result."""
+    allocates, blocks that have been given back already. Returns call's result. (A first round loads
+    the kernels and gets the memory, which can wait for the device.)"""
     side = torch.cuda.Stream()
-    torch.cuda.synchronize()
-    blocks = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(2)]
-    torch.cuda._sleep(200_000_000)
-    for b in blocks:
-        b.fill_(0x55)
-    del blocks, b
-    out = call(side)
-    side.synchronize()
-    assert not torch.cuda.current_stream().query()              # what it queued is still to come
-    torch.cuda.synchronize()
+    for cycles in (1000, 400_000_000):
+        torch.cuda.synchronize()
+        blocks = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(2)]
+        torch.cuda._sleep(cycles)
+        for b in blocks:
+            b.fill_(0x55)
+        del blocks, b
+        out = call(side)
+        side.synchronize()
+        early = not torch.cuda.current_stream().query()         # what it queued is still to come
+        torch.cuda.synchronize()
+    assert early
     return out
 
 
@@ -662,6 +665,32 @@ def test_serving_memory_of_another_stream(g):
                       [2 * T * hq * D, lib.gptq_kv_attention_workspace_size(T, hq, hk, D, 1, T)]),
         "adapter": (lambda s: (g.gptq_adapter_linear(q, X, m, A, B, ids, stream=s),),
                     [4 * T * m, lib.gptq_adapter_workspace_size(m, d, 4, 128, T, rank)]),
+    }
+    for name, (call, sizes) in calls.items():
+        want = call(None)
+        for a, b in zip(want, _on_another_stream(call, sizes)):
+            assert torch.equal(a, b), name
+    done(g)
+
+
+def test_layer_memory_of_another_stream(g):
+    """The same for the calls that make a packed layer and use it alone."""
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    T, m, d = 300, 256, 512
+    X = torch.randn((T, d), generator=gen, device="cuda").bfloat16()
+    W = torch.randn((m, d), generator=gen, device="cuda")
+    q, H, Hinv1, _ = g.quantize_layer(W, [X])
+    fields = lambda q: (q.qweight, q.scales, q.zeros, q.col_losses)
+    size = g.gptq_workspace_size
+    calls = {
+        "factor": (lambda s: g.gptq_factor(H, act_order=True, sync=False, stream=s)[:2],
+                   [4 * d * d, 4 * d, size(g.GPTQ_WS_FACTOR, 0, d)]),
+        "layer": (lambda s: fields(g.gptq_quantize_layer(W, Hinv1, stream=s)),
+                  [m * d // 2, 4 * m * d // 128, 4 * d, size(g.GPTQ_WS_QUANTIZE, m, d)]),
+        "codes": (lambda s: (g.gptq_unpack_codes(q.qweight, m, d, 4, stream=s),), [m * d]),
+        "gemv": (lambda s: (g.gptq_dequant_gemv(q, X[:4], m, stream=s),), [4 * 4 * m]),
+        "gemm": (lambda s: (g.gptq_dequant_gemm(q, X, m, out_bf16=True, stream=s),),
+                 [2 * T * m, size(g.GPTQ_WS_DEQUANT_GEMM, m, d)]),
     }
     for name, (call, sizes) in calls.items():
         want = call(None)
