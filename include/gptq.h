@@ -540,8 +540,9 @@ gptq_status gptq_kv_read(const void* pool, int64_t num_pages, int page_size, int
  *
  *   Q, O       device, total_q x n_q_heads x head_dim of q_dtype (GPTQ_BF16 or GPTQ_F16),
  *              heads dense, token strides ldq / ldo elements, rows 16-byte aligned.
- *   cu_q       device int32[batch + 1], non-decreasing, within [0, total_q]; query tokens
- *              outside every sequence get no output.
+ *   cu_q       device int32[batch + 1], non-decreasing, within [0, total_q], steps of at most
+ *              max_q (a longer sequence gets its first max_q tokens' output, as if it had no
+ *              more, and is reported); query tokens outside every sequence get no output.
  *   kv_lens    device int32[batch], in [0, table_width * page_size].
  *   block_table device int32, batch x table_width, row stride ldt; entries that hold keys
  *              are pages in [0, num_pages), later ones are not read.

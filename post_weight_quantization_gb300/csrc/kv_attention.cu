@@ -581,6 +581,7 @@ gptq_status kv_attention_launch(const void* Q, int dtype, long long total_q, int
   p.Q = Q; p.O = O; p.lse = lse; p.cu_q = cu_q; p.kv_lens = kv_lens; p.table = table;
   p.pool = reinterpret_cast<const uint8_t*>(pool);
   p.ldq = ldq; p.ldo = ldo; p.ldt = ldt; p.total_q = total_q; p.table_width = table_width; p.num_pages = num_pages;
+  p.max_q = max_q;
   p.Hq = Hq; p.H = H; p.G = Hq / H; p.batch = (int)batch; p.causal = causal; p.q_f16 = dtype == GPTQ_F16;
   set_pages(p, page);
   p.window = window;

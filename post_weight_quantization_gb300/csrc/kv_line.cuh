@@ -25,7 +25,7 @@ struct Params {
   const int* kv_lens;
   const int* table;
   const uint8_t* pool;
-  long long ldq, ldo, ldt, total_q, table_width, num_pages;
+  long long ldq, ldo, ldt, total_q, table_width, num_pages, max_q;
   int Hq, H, G, page, batch, causal, q_f16;
   int pb, pb_log2;                              // keys of a block: the largest power of two up to TILE that divides page
   uint32_t page_mul;                            // ceil(2^32 / (page / pb)); 0 when page is pb
@@ -67,10 +67,12 @@ __device__ __forceinline__ Seq load_seq(const Params& p, int b, int R, int* err)
   Seq s;
   long long a = p.cu_q[b], z = p.cu_q[b + 1], len = p.kv_lens[b];
   const long long cap = p.table_width * p.page;
-  if (a < 0 || z > p.total_q || len < 0 || len > cap) {
+  // more tokens than max_q count as max_q: the host has chosen the launches by it
+  if (a < 0 || z > p.total_q || z < a || z - a > p.max_q || len < 0 || len > cap) {
     report_device_error(err, DEVERR_INDEX);
     a = a < 0 ? 0 : a;
     z = z > p.total_q ? p.total_q : z;
+    z = z - a > p.max_q ? a + p.max_q : z;
     len = len < 0 ? 0 : (len > cap ? cap : len);
   }
   s.tok0 = a;

@@ -697,3 +697,34 @@ def test_layer_memory_of_another_stream(g):
         for a, b in zip(want, _on_another_stream(call, sizes)):
             assert torch.equal(a, b), name
     done(g)
+
+
+@pytest.mark.parametrize("hq,h,D,max_q,n,lens", [(4, 2, 64, 1, 40, [200, 64]), (8, 8, 128, 1, 300, [400] * 24),
+                                                 (8, 2, 128, 40, 60, [90, 80])])
+def test_attention_counts_past_max_q_are_reported(g, hq, h, D, max_q, n, lens):
+    """cu_q with more tokens for a sequence than max_q says, or fewer than none: reported, the sequence
+    taken as its first max_q tokens (or none), the others as they are."""
+    t = Long(g, max(lens), h, D, 16, seed=D)
+    new = [max_q] * len(lens)
+    cache, Q, cu, kv, table = t.batch(lens, new, hq)
+    total = Q.shape[0]
+    wide = torch.cat([Q, torch.randn((n, hq, D), device="cuda").bfloat16()])
+    cu = cu.clone()
+    cu[-1] += n                                                  # the last sequence: n tokens too many
+    fill = lambda: (torch.full_like(wide, 5.0), torch.full((total + n, hq), 5.0, device="cuda"))
+    O, lse = fill()
+    g.gptq_kv_attention(cache, wide, cu, kv, table, max_q, O=O, lse=lse)
+    torch.cuda.synchronize()
+    with pytest.raises(g.GPTQError) as e:
+        g.gptq_device_check()
+    assert e.value.status == g.GPTQ_ERR_INVALID_ARG
+    t.check(O, lse, range(len(lens)), (0, hq - 1))
+    assert torch.all(O[total:] == 5) and torch.all(lse[total:] == 5)
+    cu[-1] = cu[-2] - 1                                          # a step below zero: no tokens
+    O, lse = fill()
+    g.gptq_kv_attention(cache, wide, cu, kv, table, max_q, O=O, lse=lse)
+    torch.cuda.synchronize()
+    with pytest.raises(g.GPTQError):
+        g.gptq_device_check()
+    t.check(O, lse, range(len(lens) - 1), (0,))
+    assert torch.all(O[total - max_q:] == 5)
