@@ -1104,13 +1104,9 @@ gptq_status launch(const CUtensorMap& mx, const CUtensorMap& mu, Params p, bool 
   p.codes_tma = make_code_map(&mc, p.qweight, p.m, (long long)p.wpr * 4, BITS) ? 1 : 0;
   using C = Cfg<BITS, N>;
   const size_t smem = C::SMEM_FIX + (C::MANY ? 0 : (size_t)N * p.rank * 4);
-  static bool attr_done = false;
-  if (!attr_done) {
-    const size_t most = C::SMEM_FIX + (C::MANY ? 0 : (size_t)N * 128 * 4);
-    if (cudaFuncSetAttribute(adapter_gemm_kernel<BITS, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess)
-      return set_error(GPTQ_ERR_CUDA, "cudaFuncSetAttribute(adapter_gemm_kernel) failed");
-    attr_done = true;
-  }
+  static PerDevice done;
+  const size_t most = C::SMEM_FIX + (C::MANY ? 0 : (size_t)N * 128 * 4);
+  if (gptq_status st = allow_smem(done, adapter_gemm_kernel<BITS, N>, most, "adapter_gemm_kernel")) return st;
   const long long tiles = (long long)p.mt * p.nt;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(C::MANY ? std::min<long long>(tiles, sm_count()) : tiles * p.S));

@@ -12,6 +12,7 @@
 #include <utility>
 
 #include "../../include/gptq.h"
+#include "per_device.h"
 
 namespace gptq {
 
@@ -50,6 +51,7 @@ struct ProfScope {
 };
 gptq_status check_launch(const char* what);
 int sm_count();
+int current_device();
 int* device_error_word();   // device address of the library's error word
 
 // error bits written by kernels into the device error word
@@ -355,6 +357,17 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
 }
 __device__ __forceinline__ void cp_async_wait_all() {
   asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+}
+
+// A kernel's limit of dynamic shared memory, set once per device; `done` is a static of the caller's,
+// one per kernel.
+template <typename K>
+inline gptq_status allow_smem(PerDevice& done, K* kernel, size_t bytes, const char* name) {
+  if (done.once(current_device(), [&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
+      }))
+    return GPTQ_OK;
+  return set_error(GPTQ_ERR_CUDA, "cudaFuncSetAttribute(%s) failed", name);
 }
 
 // Programmatic dependent launch. A kernel launched with launch_pdl may start while the

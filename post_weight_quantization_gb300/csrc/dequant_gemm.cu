@@ -365,13 +365,8 @@ gptq_status dequant_gemm_launch(const uint32_t* qweight, const float* scales, co
   p.y_bf16 = y_bf16;
   const long long ntiles = (long long)p.mt * p.nt;
   const int grid = (int)std::min<long long>(ntiles, sm_count());
-  static bool attr_done = false;
-  if (!attr_done) {
-    if (cudaFuncSetAttribute(dequant_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) !=
-        cudaSuccess)
-      return set_error(GPTQ_ERR_CUDA, "cudaFuncSetAttribute(dequant_gemm_kernel) failed");
-    attr_done = true;
-  }
+  static PerDevice done;
+  if (gptq_status st = allow_smem(done, dequant_gemm_kernel, SMEM_BYTES, "dequant_gemm_kernel")) return st;
   ProfScope ps("dequant_gemm.gemm", s);
   if (launch_pdl(dequant_gemm_kernel, dim3(grid), dim3(THREADS), SMEM_BYTES, s, mx, mb, p, device_error_word()) !=
       cudaSuccess)

@@ -43,16 +43,10 @@ thread_local char g_last_error[512] = "";
 std::atomic<unsigned long long> g_launches{0};
 __device__ int g_device_error_word = 0;
 
-constexpr int kMaxDevices = 64;
+constexpr int kMaxDevices = PerDevice::kMaxDevices;
 int g_sm_count[kMaxDevices] = {0};
 int* g_err_addr[kMaxDevices] = {nullptr};
 std::mutex g_mu;
-
-int current_device() {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
-  return dev;
-}
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 }  // namespace
@@ -128,6 +122,12 @@ cudaEvent_t profile_event() {
 void profile_record(const char* name, cudaEvent_t start, cudaEvent_t stop) {
   std::lock_guard<std::mutex> lk(g_prof_mu);
   if (g_prof) g_prof->push_back({name, start, stop});
+}
+
+int current_device() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+  return dev;
 }
 
 int sm_count() {

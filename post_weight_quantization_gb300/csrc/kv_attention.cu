@@ -591,14 +591,8 @@ gptq_status kv_attention_launch(const void* Q, int dtype, long long total_q, int
   with_shape(D, row_tiles(D, max_q * p.G), [&](auto d, auto n) {
     constexpr int DD = decltype(d)::value, NT = decltype(n)::value;
     using C = Cfg<DD, NT>;
-    static bool attr_done = false;
-    if (!attr_done) {
-      if (cudaFuncSetAttribute(kv_split_kernel<DD, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) {
-        st = set_error(GPTQ_ERR_CUDA, "cudaFuncSetAttribute(kv_split_kernel) failed");
-        return;
-      }
-      attr_done = true;
-    }
+    static PerDevice done;
+    if ((st = allow_smem(done, kv_split_kernel<DD, NT>, C::SMEM, "kv_split_kernel"))) return;
     const long long ctas = (long long)sm_count() * C::OCC;
     p.cut = reinterpret_cast<int4*>(ws);
     p.part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(ws) + round256(16 * (size_t)ctas));

@@ -578,12 +578,8 @@ template <int D>
 static gptq_status tc_launch(kva::Params p, void* ws, cudaStream_t s) {
   using namespace kva;
   using C = tc::Cfg<D>;
-  static bool attr_done = false;
-  if (!attr_done) {
-    if (cudaFuncSetAttribute(tc::kv_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
-      return set_error(GPTQ_ERR_CUDA, "cudaFuncSetAttribute(kv_tc_kernel) failed");
-    attr_done = true;
-  }
+  static PerDevice done;
+  if (gptq_status st = allow_smem(done, tc::kv_tc_kernel<D>, C::SMEM, "kv_tc_kernel")) return st;
   const unsigned ctas = (unsigned)sm_count();
   p.cut = reinterpret_cast<int4*>(ws);
   p.part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(ws) + round256(16 * (size_t)ctas));

@@ -405,14 +405,10 @@ gptq_status syrk_accumulate(const uint16_t* X, long long n, long long d, long lo
   g.npairs = 0;
   const int sms = sm_count();
 
-  static bool attr_set[2] = {false, false};
+  static PerDevice done[2];
   for (int k = 0; k < 2; ++k)
-    if (!attr_set[k]) {
-      if (cudaFuncSetAttribute(k ? syrk_kernel<true> : syrk_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               SMEM_BYTES) != cudaSuccess)
-        return set_error(GPTQ_ERR_CUDA, "cudaFuncSetAttribute(syrk_kernel) failed");
-      attr_set[k] = true;
-    }
+    if (gptq_status st = allow_smem(done[k], k ? syrk_kernel<true> : syrk_kernel<false>, SMEM_BYTES, "syrk_kernel"))
+      return st;
 
   // Paired mode when every 128-row tile has its partner: d a multiple of 256.
   int clusters = 0;

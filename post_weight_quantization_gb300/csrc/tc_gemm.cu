@@ -559,12 +559,8 @@ gptq_status tc_gemm(const simt::GemmArgs& g, int batches, bool a_kmaj, bool b_km
   const int grid = std::min(ntiles, g.max_ctas > 0 ? std::min(g.max_ctas, sm_count()) : sm_count());
 
   auto launch = [&](auto kern, int key) -> gptq_status {
-    static bool attr_done[2] = {false, false};
-    if (!attr_done[key]) {
-      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) != cudaSuccess)
-        return set_error(GPTQ_ERR_CUDA, "cudaFuncSetAttribute(tc_gemm_kernel) failed");
-      attr_done[key] = true;
-    }
+    static PerDevice done[2];
+    if (gptq_status st = allow_smem(done[key], kern, SMEM_BYTES, "tc_gemm_kernel")) return st;
     if (launch_pdl(kern, dim3(grid), dim3(key ? threads<true>() : threads<false>()), SMEM_BYTES, s, ma, mb, malo,
                    mblo, p, device_error_word()) != cudaSuccess)
       return check_launch("tc_gemm_kernel");
