@@ -44,10 +44,16 @@ def _sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
 
 
+def _cxx() -> str:
+    return os.environ.get("CXX") or "g++"
+
+
 def _calls_flags():
+    """serving_calls.so is compiled against this torch's C++ headers and says for which: the binding
+    does not use it with another."""
     import torch
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
-    return ["-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+    return ["-O2", "-std=c++17", "-fPIC", f'-DBUILT_FOR="{torch.__version__}"', f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
             "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
             "-isystem", sysconfig.get_paths()["include"],
             "-isystem", os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include")]
@@ -67,12 +73,13 @@ def _fingerprint() -> str:
         h.update(f.encode())
         with open(f, "rb") as fh:
             h.update(fh.read())
-    h.update(" ".join(ARCH_FLAGS + NVCC_FLAGS + _calls_flags()).encode())
+    h.update(" ".join(ARCH_FLAGS + NVCC_FLAGS + [_cxx(), sys.version] + _calls_flags()).encode())
     return h.hexdigest()
 
 
 def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -> str:
-    """Compile and link libgptq.so and serving_calls.so if sources changed; return the library's path."""
+    """Compile and link libgptq.so and serving_calls.so if sources, compilers, torch or Python changed;
+    return the library's path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     stamp = os.path.join(BUILD_DIR, "fingerprint")
     fp = _fingerprint()
@@ -96,17 +103,17 @@ def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -
         return obj
 
     calls_obj = os.path.join(BUILD_DIR, "serving_calls.o")
-    cxx = os.environ.get("CXX") or "g++"
+    cxx = _cxx()
     with ThreadPoolExecutor(jobs or min(8, len(srcs) + 1)) as ex:
         calls = ex.submit(_run, [cxx, *_calls_flags(), "-c", CALLS_SRC, "-o", calls_obj], "serving_calls.cpp")
         objs = list(ex.map(compile_one, srcs))
-        calls.result()
     tmp = LIB_PATH + ".tmp"
     cmd = [nvcc, *ARCH_FLAGS, "-shared", "-o", tmp, *objs]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB_PATH)
+    calls.result()                               # the library is there even if the module cannot be built
     import torch
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = CALLS_PATH + ".tmp"

@@ -332,4 +332,8 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "serving_calls", nullptr, -1, metho
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit_serving_calls() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit_serving_calls() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "built_for", BUILT_FOR) != 0) Py_CLEAR(m);
+  return m;
+}

@@ -7,7 +7,9 @@ allocate outputs and workspaces with torch when the caller passes none, and rais
 ``GPTQError`` on a non-OK status.
 
 If the library has not been built, importing this module fails with an ImportError
-that says how to build it; there is no fallback.
+that says how to build it; there is no fallback. The serving calls also need
+``serving_calls.so``, built beside it for one version of torch, and raise that error
+without it.
 """
 from __future__ import annotations
 
@@ -95,11 +97,31 @@ def _load() -> ctypes.CDLL:
 
 
 _lib = _load()
-try:
-    from . import serving_calls as _calls
-except ImportError as e:
-    raise ImportError("serving_calls.so is missing or does not fit this torch: build it with "
-                      "`python -m post_weight_quantization_gb300.build`") from e
+
+
+class _NoCalls:
+    """Stands for the module of the serving calls where it cannot be used: those calls say why, and
+    quantizing, which needs the library alone, goes on."""
+
+    def __init__(self, why: str):
+        self.why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"serving_calls.so {self.why}: build it with "
+                          "`python -m post_weight_quantization_gb300.build --force`")
+
+
+def _load_calls():
+    try:
+        from . import serving_calls
+    except ImportError as e:
+        return _NoCalls(f"is missing or does not load ({e})")
+    if serving_calls.built_for != torch.__version__:
+        return _NoCalls(f"was built for torch {serving_calls.built_for}, this is {torch.__version__}")
+    return serving_calls
+
+
+_calls = _load_calls()
 
 
 def library() -> ctypes.CDLL:
