@@ -334,6 +334,7 @@ class QuantizedLayer:
     bits: int
     group_size: int
     d: int
+    act_order: bool = False    # columns were quantized, and grouped, in the act-order permutation
 
 
 def gptq_quantize_layer(W: torch.Tensor, Hinv1: torch.Tensor, perm: Optional[torch.Tensor] = None, bits: int = 4,
@@ -365,6 +366,7 @@ def gptq_quantize_layer(W: torch.Tensor, Hinv1: torch.Tensor, perm: Optional[tor
     _need_buffer(out.scales, "out.scales", (m, G), (torch.float32,))
     _need_buffer(out.zeros, "out.zeros", (m, G), (torch.float32,))
     _need_buffer(out.col_losses, "out.col_losses", (d,), (torch.float32,))
+    out.act_order = perm is not None
     need = gptq_workspace_size(GPTQ_WS_QUANTIZE, m, d, bits, group_size, blocksize)
     if ws is None:
         ws = _workspace(need, dev, stream)
@@ -517,7 +519,10 @@ def gptq_adapter_linear(q: "QuantizedLayer", X: torch.Tensor, m: int, A: Optiona
     """Y[t] = X[t] W_hat^T + alpha[a] (X[t] A[a]^T) B[a]^T with a = ids[t] (negative: no
     adapter), from the packed layer q and bf16 tokens X (T x d). A: (n, rank, d), B: (n, m,
     rank) bf16, ids: (T,) int32, alpha: (n,) float32 or None for 1. fp32 output, or bf16 with
-    out_bf16. Without A, B and ids it is the packed layer alone."""
+    out_bf16. Without A, B and ids it is the packed layer alone. Groups are natural ones: an
+    act-order layer of several groups is refused (gptq_dequant_gemv takes its g_idx)."""
+    if q.act_order and q.group_size not in (-1, q.d):
+        raise ValueError("q is an act-order layer with several groups; gptq_adapter_linear reads natural groups")
     if stream is None:
         got = _calls.adapter_linear(q.qweight, q.scales, q.zeros, q.d, q.bits, q.group_size, X, m, A, B, ids, alpha, Y,
                                     out_bf16, ws)
@@ -833,7 +838,7 @@ class HostPipeline:
         self.host_out = QuantizedLayer(
             qweight=_host_empty((m, (d * bits + 31) // 32), torch.int32), scales=_host_empty((m, G), torch.float32),
             zeros=_host_empty((m, G), torch.float32), col_losses=_host_empty((d,), torch.float32),
-            bits=bits, group_size=group_size, d=d)
+            bits=bits, group_size=group_size, d=d, act_order=bool(act_order))
         self.perm = _host_empty((d,), torch.int32) if act_order else None
 
     def __del__(self):

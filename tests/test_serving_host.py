@@ -285,3 +285,30 @@ def test_oracle_norm_rope_turns():
     y = rng.standard_normal((3, 2, 16))
     a = rng.random((5, 8))
     assert np.allclose((so.norm_rope(y, [0, 2, 4], np.cos(a), np.sin(a)) ** 2).sum(-1), (y ** 2).sum(-1))
+
+
+def test_act_order_layers_of_several_groups_are_refused(g):
+    """The adapter projection reads natural groups; a layer that was quantized in the act-order
+    permutation says so."""
+    q = lambda gs, act: g.QuantizedLayer(torch.zeros((8, 8), dtype=torch.int32), torch.zeros((8, 1 if gs == -1 else 64 // gs)),
+                                         torch.zeros((8, 1 if gs == -1 else 64 // gs)), None, 4, gs, 64, act_order=act)
+    X = torch.zeros((2, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="act-order"):
+        g.gptq_adapter_linear(q(32, True), X, 8)
+    for gs, act in ((32, False), (-1, True), (64, True)):          # on to the next check: not a CUDA tensor
+        with pytest.raises(TypeError):
+            g.gptq_adapter_linear(q(gs, act), X, 8)
+
+
+@pytest.mark.gpu
+def test_layers_say_whether_they_are_act_order(g):
+    W, X = torch.randn((64, 256), device="cuda"), torch.randn((300, 256), device="cuda").bfloat16()
+    plain, act = (g.quantize_layer(W, [X], act_order=a)[0] for a in (False, True))
+    assert (plain.act_order, act.act_order) == (False, True)
+    g.gptq_adapter_linear(plain, X[:3], 64)
+    with pytest.raises(ValueError, match="act-order"):
+        g.gptq_adapter_linear(act, X[:3], 64)
+    one = g.quantize_layer(W, [X], group_size=-1, act_order=True)[0]
+    assert torch.allclose(g.gptq_adapter_linear(one, X[:3], 64), g.gptq_dequant_gemv(one, X[:3], 64), rtol=1e-4, atol=1e-4)
+    pipe = g.HostPipeline(64, 256, act_order=True)
+    assert pipe.host_out.act_order and not g.HostPipeline(64, 256).host_out.act_order
