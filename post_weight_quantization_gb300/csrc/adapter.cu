@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(SH_WARPS * 32) adapter_shrink_kernel(ShrinkPar
   __shared__ float red[SH_WARPS][SH_TOK][8 * NT + 1], sums[SH_TOK * 8 * NT];
   grid_dep_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int t0 = blockIdx.y * SH_TOK, part = blockIdx.x, parts = gridDim.x;
+  const int parts = p.splits, t0 = (int)(blockIdx.x / parts) * SH_TOK, part = (int)(blockIdx.x % parts);
   int id = -1;
   if (lane < SH_TOK && t0 + lane < p.T) {
     id = p.ids[t0 + lane];
@@ -1169,7 +1169,9 @@ gptq_status adapter_linear_launch(const uint32_t* qweight, const float* scales, 
     if (pl.N == 256) q.hl = reinterpret_cast<__nv_bfloat16*>(ws);
     else q.part = reinterpret_cast<float*>(ws);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)pl.splits, (unsigned)(T <= SH_FEW ? T * ((rank + SH_ROWS - 1) / SH_ROWS) : (T + SH_TOK - 1) / SH_TOK));
+    // clusters along x where there may be more of them than gridDim.y holds
+    const long long few = T * ((rank + SH_ROWS - 1) / SH_ROWS), many = (T + SH_TOK - 1) / SH_TOK;
+    cfg.gridDim = T <= SH_FEW ? dim3((unsigned)pl.splits, (unsigned)few) : dim3((unsigned)(pl.splits * many));
     cfg.blockDim = dim3(SH_WARPS * 32);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];

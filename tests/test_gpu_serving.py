@@ -728,3 +728,27 @@ def test_attention_counts_past_max_q_are_reported(g, hq, h, D, max_q, n, lens):
         g.gptq_device_check()
     t.check(O, lse, range(len(lens) - 1), (0,))
     assert torch.all(O[total - max_q:] == 5)
+
+
+def test_adapter_linear_a_million_tokens(g):
+    """More groups of 16 tokens than a grid's second dimension holds."""
+    m, d, rank, n, T = 8, 32, 8, 5, 65536 * 16 + 9
+    rng = np.random.default_rng(8)
+    words, sc, ze = _layer(rng, m, d, 4, 32)
+    q = g.QuantizedLayer(torch.from_numpy(words.view(np.int32)).cuda(), torch.from_numpy(sc).cuda(),
+                         torch.from_numpy(ze).cuda(), None, 4, 32, d)
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    rnd = lambda *s: torch.randn(s, device="cuda", generator=gen).bfloat16()
+    X, A, B = rnd(T, d), rnd(n, rank, d), rnd(n, m, rank)
+    ids = (torch.arange(T, device="cuda") // 1000 % (n + 1) - 1).int()
+    Y = g.gptq_adapter_linear(q, X, m, A, B, ids)
+    done(g)
+    W = torch.from_numpy(orc.dequantize_packed(words, sc, ze, 4, d, 32, None)).cuda()
+    x = X.double()
+    ref, bound = x @ W.T, 35 * 2.0 ** -23 * (x.abs() @ W.abs().T)
+    for a in range(n):
+        t = ids == a
+        ref[t] += x[t] @ A[a].double().T @ B[a].double().T
+        bound[t] += ((d + rank) * 2.0 ** -23 + 2.0 ** -16) * (x[t].abs() @ A[a].double().abs().T @ B[a].double().abs().T)
+    bound += HALF_ULP[torch.float32] * ref.abs() + 1e-30
+    assert ((Y.double() - ref).abs() <= bound).all()
