@@ -59,6 +59,10 @@ constexpr int SH_WARPS = 8, SH_TOK = 16;
 // 16 tokens that share it, but a group's adapters one after another. m = d = 8192, 128 tokens, the whole
 // call, in us: 64 adapters in any order 61 / 227, sorted 66 / 170, 4 adapters sorted 59 / 47.
 constexpr int SH_FEW = 256;
+// Tokens above which a call may take tiles of 256 tokens, whose adapters' units need U as two bf16
+// parts: only the other kernel writes those.
+constexpr int TILES_FEW = 256;
+static_assert(SH_FEW <= TILES_FEW, "adapter_shrink_few_kernel writes U in fp32 alone");
 
 struct ShrinkParams {
   const uint16_t* X;
@@ -1071,7 +1075,7 @@ Plan plan_of(long long m, long long d, long long T, int rank) {
   p.mt = (int)((m + BM - 1) / BM);
   p.S = 1;
   p.splits = 1;
-  if (T > 256 && p.mt * ((T + 63) / 64) > sms) {
+  if (T > TILES_FEW && p.mt * ((T + 63) / 64) > sms) {
     p.N = 256;
   } else {
     p.N = T <= 16 ? 16 : (T <= 32 ? 32 : 64);
