@@ -113,7 +113,7 @@ class Attention:
         parts = qkv.split([nq, nk, nk], dim=1)
         for name, Y in zip("qkv", parts):
             self._project(name, X, Y.shape[1], ids, Y)
-        Q, K, V = (Y.view(T, -1, c.head_dim) for Y in parts)
+        Q, K, V = (Y.view(T, Y.shape[1] // c.head_dim, c.head_dim) for Y in parts)
         gptq.gptq_qk_norm_rope(Q, K, step.positions, self.cos, self.sin, self.wq, self.wk, self.eps, Q_out=Q, K_out=K)
         gptq.gptq_kv_append(c, K, V, step.slots)
         O = gptq.gptq_kv_attention(c, Q, step.cu_q, step.kv_lens, step.block_table, step.max_q, window=self.window)

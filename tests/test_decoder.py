@@ -156,3 +156,29 @@ def test_example_runs(dec, capsys):
     dec.main()
     out = capsys.readouterr().out
     assert "us a step" in out and "nan" not in out
+
+
+@pytest.mark.gpu
+def test_empty_step(dec):
+    """A step without new tokens, one without sequences, and the next one as if it had not been."""
+    block = dec.random_block(256, 4, 2, 64, num_pages=8, page_size=16, positions=50, adapters=2, rank=8)
+    gen = torch.Generator().manual_seed(3)
+    X = [torch.randn((n, 256), generator=gen).bfloat16().cuda() for n in (20, 2)]
+    outs = []
+    for empty in (False, True):
+        batch = dec.Batch(8, 16)
+        if empty:
+            assert block.forward(X[0][:0], batch.extend([])).shape == (0, 256)
+        for _ in range(2):
+            batch.add()
+        ids = torch.zeros(20, dtype=torch.int32, device="cuda")
+        outs.append([block.forward(X[0], batch.extend([15, 5]), ids)])
+        if empty:
+            for some in (None, ids[:0]):
+                Y = block.forward(X[0][:0], batch.extend([0, 0]), some)
+                assert Y.shape == (0, 256) and Y.dtype == torch.bfloat16
+        outs[-1].append(block.forward(X[1], batch.extend([1, 1]), ids[:2]))
+    torch.cuda.synchronize()
+    from post_weight_quantization_gb300 import gptq
+    gptq.gptq_device_check()
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
