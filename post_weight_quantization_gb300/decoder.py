@@ -71,7 +71,8 @@ class Step:
 
     def copy_(self, other: "Step") -> "Step":
         """Take over a step of the same shape in place, for a captured graph that reads this one."""
-        if (self.max_q, self.block_table.shape) != (other.max_q, other.block_table.shape):
+        shape = lambda s: (s.max_q, s.slots.shape, s.block_table.shape)
+        if shape(self) != shape(other):
             raise ValueError("the steps have different shapes")
         self.slots.copy_(other.slots)
         self.ints.copy_(other.ints)

@@ -182,3 +182,23 @@ def test_empty_step(dec):
     from post_weight_quantization_gb300 import gptq
     gptq.gptq_device_check()
     assert all(torch.equal(a, b) for a, b in zip(*outs))
+
+
+def test_copy_refuses_steps_of_other_shapes(dec):
+    """... before it writes anything: another number of tokens, sequences, pages or most new tokens."""
+    def step(new, width=3):
+        batch = dec.Batch(20, 4, device="cpu")
+        for _ in new:
+            batch.add()
+        return batch.extend(new, width)
+    at = step([1, 1, 1])
+    slots, ints = at.slots.clone(), at.ints.clone()
+    for other in (step([1, 0, 0]), step([1, 1, 0]), step([1, 1, 1, 1]), step([1, 1, 1], 4), step([2, 1, 0])):
+        with pytest.raises(ValueError):
+            at.copy_(other)
+        assert torch.equal(at.slots, slots) and torch.equal(at.ints, ints)
+    other = step([0, 0, 0])
+    same = dec.Step(slots + 5, ints + 1, 3, 1)
+    with pytest.raises(ValueError):
+        at.copy_(other)
+    assert torch.equal(at.copy_(same).slots, slots + 5) and torch.equal(at.ints, ints + 1)
