@@ -411,7 +411,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
         int e = 14 - ((int)(__float_as_uint(mx) >> 23) - 127);
         e = mx == 0.0f || mx > 3.0e38f ? 0 : max(-126, min(126, e));
         const float f = pow2(e);
-        rowc = p.scale_log2 * pow2(-e);
+        // not 0, which would make a NaN of the -infinity of an unseen key; that low, scores round to 0 anyway
+        rowc = fmaxf(p.scale_log2 * pow2(-e), 1.17549435e-38f);
         const uint32_t dst = smem_u32(smem) + x * C::MAT + r * 128;
 #pragma unroll 4
         for (int c = 0; c < D / 8; ++c) {

@@ -752,3 +752,15 @@ def test_adapter_linear_a_million_tokens(g):
         bound[t] += ((d + rank) * 2.0 ** -23 + 2.0 ** -16) * (x[t].abs() @ A[a].double().abs().T @ B[a].double().abs().T)
     bound += HALF_ULP[torch.float32] * ref.abs() + 1e-30
     assert ((Y.double() - ref).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("new", [1, 3, 70])
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 20), (False, 9)])
+def test_attention_scores_that_vanish(g, new, causal, window):
+    """Scale and queries so small that their product is below every fp32 number: each row is the
+    mean of the keys it sees."""
+    t = Batch([150, 80], [new, new], 4, 2, 128, 16, torch.bfloat16, seed=5, q_scale=1e-35)
+    lse = torch.empty((2 * new, 4), device="cuda")
+    O = g.gptq_kv_attention(*t.gpu(g), new, sm_scale=1e-8, causal=causal, window=window, lse=lse)
+    done(g)
+    t.check(O, lse, sm=1e-8, causal=causal, window=window)
