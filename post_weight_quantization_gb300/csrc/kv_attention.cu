@@ -367,26 +367,29 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, NT>::OCC) kv_split_kernel(Para
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           mx = fmaxf(mx, fabsf(v[k]));
-          sum += v[k];
         }
       }
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      int e = 14 - ((int)(__float_as_uint(mx) >> 23) - 127);
-      e = mx == 0.0f || mx > 3.0e38f ? 0 : max(-126, min(126, e));
+      const int e = row_exponent(mx);
       const float f = pow2(e);
 #pragma unroll
       for (int w = 0; w < KW; ++w) {
         float v[8];
         if (p.q_f16) unpack8<F16>(&raw[w], v); else unpack8<BF16>(&raw[w], v);
-        st.q[n][4 * w] = pack_half2(v[0] * f, v[4] * f);
-        st.q[n][4 * w + 1] = pack_half2(v[1] * f * 0.0625f, v[5] * f * 0.0625f);
-        st.q[n][4 * w + 2] = pack_half2(v[2] * f, v[6] * f);
-        st.q[n][4 * w + 3] = pack_half2(v[3] * f * 0.0625f, v[7] * f * 0.0625f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          v[k] *= f;
+          sum += v[k];                           // of the scaled values: the raw ones' sum can pass fp32
+        }
+        st.q[n][4 * w] = pack_half2(v[0], v[4]);
+        st.q[n][4 * w + 1] = pack_half2(v[1] * 0.0625f, v[5] * 0.0625f);
+        st.q[n][4 * w + 2] = pack_half2(v[2], v[6]);
+        st.q[n][4 * w + 3] = pack_half2(v[3] * 0.0625f, v[7] * 0.0625f);
       }
-      const float rs = sum * f, rc = p.scale_log2 * pow2(-e);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      const float rs = sum, rc = p.scale_log2 * pow2(-e);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {              // rows 2t, 2t + 1 of the n-tile, from the lanes that read them
         st.rq[n][i] = __shfl_sync(0xffffffffu, rs, 4 * (2 * t + i));

@@ -408,8 +408,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
 #pragma unroll
           for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fabsf(v[k]));
         }
-        int e = 14 - ((int)(__float_as_uint(mx) >> 23) - 127);
-        e = mx == 0.0f || mx > 3.0e38f ? 0 : max(-126, min(126, e));
+        const int e = row_exponent(mx);
         const float f = pow2(e);
         // not 0, which would make a NaN of the -infinity of an unseen key; that low, scores round to 0 anyway
         rowc = fmaxf(p.scale_log2 * pow2(-e), 1.17549435e-38f);

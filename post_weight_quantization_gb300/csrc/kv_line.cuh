@@ -55,6 +55,12 @@ __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }   // -126 ... 127
+// The power of two that brings a query row's largest value mx to [2^14, 2^15); 0 for a row of zeros and
+// for one with an infinity, which stays one.
+__device__ __forceinline__ int row_exponent(float mx) {
+  const int e = 14 - ((int)(__float_as_uint(mx) >> 23) - 127);
+  return mx == 0.0f || mx == CUDART_INF_F ? 0 : max(-126, min(126, e));
+}
 // One sequence of the batch, as the line of tiles sees it.
 struct Seq {
   long long tok0;                // its first query token

@@ -545,7 +545,8 @@ def test_attention_piece_with_cold_caches(g, hq, h, D, page):
 class Long:
     """One long sequence's cache, which all sequences of a batch share through their tables (sequence b
     sees its first lens[b] tokens), and attention over it in float64 on the GPU. The cached values
-    are those that gptq_kv_read gives; the bounds are the ones above. Values of V move with their tile of
+    are those that gptq_kv_read gives; the bounds are the ones above, with 2^-11 sm sum |q| |k| more for a
+    score of the kernel for many rows, which rounds k to fp16. Values of V move with their tile of
     128 keys, so that a tile that is lost or counted twice moves the output, and lse moves by the tile's
     share of the softmax."""
 
@@ -576,8 +577,8 @@ class Long:
         ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
         return self.cache, self.Q, ints(self.cu), ints(lens), self.order.int()[None].repeat(len(lens), 1)
 
-    def check(self, O, lse, seqs, heads, causal=True, window=0):
-        sm, G = self.D ** -0.5, self.hq // self.h
+    def check(self, O, lse, seqs, heads, causal=True, window=0, sm=None, many=False):
+        sm, G = self.D ** -0.5 if sm is None else sm, self.hq // self.h
         for b in seqs:
             n, a, z = self.lens[b], self.cu[b], self.cu[b + 1]
             pos = torch.arange(n - (z - a), n, device="cuda")[:, None]
@@ -591,6 +592,8 @@ class Long:
                 p = torch.where(see, torch.exp(s - l[:, None]), 0.0)
                 ref, mag = p @ v, p @ (v.abs() + 2 * num[:, 3:].abs())
                 d_s = (self.D + 8) * 2.0 ** -22 * sm * q.abs().sum(1, keepdim=True) * (15 * num[:, 0] + num[:, 1].abs()).max()
+                if many:
+                    d_s = d_s + 2.0 ** -11 * sm * (q.abs() @ k.abs().T).max(1, keepdim=True).values
                 bound = ((2.0 ** -11 + 2 * d_s + 2.0 ** -18) * mag + HALF_ULP[O.dtype] * ref.abs() * (1 + 2.0 ** -6)
                          + TINY[O.dtype])
                 err = (O[a:z, y].double() - ref).abs()
@@ -764,3 +767,20 @@ def test_attention_scores_that_vanish(g, new, causal, window):
     O = g.gptq_kv_attention(*t.gpu(g), new, sm_scale=1e-8, causal=causal, window=window, lse=lse)
     done(g)
     t.check(O, lse, sm=1e-8, causal=causal, window=window)
+
+
+@pytest.mark.parametrize("new", [1, 3, 70])
+def test_attention_largest_queries(g, new):
+    """bf16 queries up to the largest finite one, whose plain sum over a head is beyond fp32."""
+    t = Long(g, 150, 2, 128, 16, seed=6)
+    args = t.batch([150, 80], [new, new], 4)
+    big = torch.finfo(torch.bfloat16).max
+    t.Q[:, 0::2] = 0.0
+    t.Q[:, 0::2, 5] = big
+    t.Q[:, 0::2, 60] = 3.1e38
+    t.Q[:, 1::2] = (1e38 * t.Q[:, 1::2].float()).clamp(-big, big).bfloat16()
+    t.Q[:, 1::2, 7] = -big
+    lse = torch.empty((2 * new, 4), device="cuda")
+    O = g.gptq_kv_attention(*args, new, sm_scale=2e-38, lse=lse)
+    done(g)
+    t.check(O, lse, (0, 1), range(4), sm=float(np.float32(2e-38)), many=new == 70)
