@@ -40,6 +40,7 @@
 // accumulator leaves tensor memory per 128 columns); 8192 x 8192, 48 tokens 31 us (2.1 TB/s; unpacking:
 // instruction issue 61 % busy).
 #include <cudaTypedefs.h>
+#include <math_constants.h>
 
 #include <algorithm>
 #include <type_traits>
@@ -55,6 +56,7 @@ namespace adp {
 // ---------------------------------------------------------------------------------
 // U = alpha A X
 constexpr int SH_WARPS = 8, SH_TOK = 16;
+constexpr float kBf16Max = 3.3895314e38f;
 // Tokens up to which each reads its adapter by itself: the other kernel reads an adapter once for up to
 // 16 tokens that share it, but a group's adapters one after another. m = d = 8192, 128 tokens, the whole
 // call, in us: 64 adapters in any order 61 / 227, sorted 66 / 170, 4 adapters sorted 59 / 47.
@@ -262,9 +264,10 @@ __global__ void __launch_bounds__(SH_WARPS * 32) adapter_shrink_kernel(ShrinkPar
       if (t0 + i < p.T && p.part) {
         p.part[(long long)(t0 + i) * p.rank + r0 + r] = s;
       } else if (t0 + i < p.T) {
-        const __nv_bfloat16 h = __float2bfloat16_rn(s);
-        p.hl[(long long)(t0 + i) * (2 * p.rank) + r0 + r] = h;
-        p.hl[(long long)(t0 + i) * (2 * p.rank) + p.rank + r0 + r] = __float2bfloat16_rn(s - __bfloat162float(h));
+        // a finite sum has a finite high part; an infinite one is its high part alone (inf - inf is a NaN)
+        const float h = fabsf(s) < CUDART_INF_F ? fminf(fmaxf(__bfloat162float(__float2bfloat16_rn(s)), -kBf16Max), kBf16Max) : s;
+        p.hl[(long long)(t0 + i) * (2 * p.rank) + r0 + r] = __float2bfloat16_rn(h);
+        p.hl[(long long)(t0 + i) * (2 * p.rank) + p.rank + r0 + r] = __float2bfloat16_rn(h == s ? 0.0f : s - h);
       }
     }
     if (parts > 1) cluster_sync();                         // also: nobody leaves while its sums are read

@@ -784,3 +784,36 @@ def test_attention_largest_queries(g, new):
     O = g.gptq_kv_attention(*args, new, sm_scale=2e-38, lse=lse)
     done(g)
     t.check(O, lse, (0, 1), range(4), sm=float(np.float32(2e-38)), many=new == 70)
+
+
+@pytest.mark.parametrize("T", [40, 300, 1300])
+def test_adapter_linear_extreme_inner_products(g, T):
+    """An inner product that is infinite, that is a NaN, and one that is finite in fp32 but rounds to an
+    infinite bf16: the same in every tile size."""
+    m, d, rank = 2500, 64, 8
+    rng = np.random.default_rng(T)
+    words, sc, ze = _layer(rng, m, d, 4, 64)
+    q = g.QuantizedLayer(torch.from_numpy(words.view(np.int32)).cuda(), torch.from_numpy(sc).cuda(),
+                         torch.from_numpy(ze).cuda(), None, 4, 64, d)
+    X = torch.zeros((T, d), dtype=torch.bfloat16)
+    X[:, :3] = torch.tensor([1.0, 1.0, 2.0])
+    A, B = torch.zeros((4, rank, d), dtype=torch.bfloat16), torch.zeros((4, m, rank), dtype=torch.bfloat16)
+    big = torch.finfo(torch.bfloat16).max
+    A[0, 3, 0], A[0, 3, 2] = big, big                              # 3 big: infinite
+    A[1, 3, 0], A[1, 3, 1] = big, 8e35                             # above bf16's largest, below fp32's
+    A[2, 3, 0] = float("nan")
+    A[3] = -A[1]
+    B[0, :, 3] = torch.from_numpy(np.where(np.arange(m) % 2, 2.0, -0.5))
+    B[1:, :, 3] = 2.0 ** -120
+    ids = np.repeat(np.arange(4), -(-T // 4))[:T].astype(np.int32)
+    Y = g.gptq_adapter_linear(q, X.cuda(), m, A.cuda(), B.cuda(), torch.from_numpy(ids).cuda())
+    done(g)
+    W = orc.dequantize_packed(words, sc, ze, 4, d, 64, None)
+    base = f64(X[0]) @ W.T
+    y, inner = f64(Y), float(A[1, 3, 0]) + float(A[1, 3, 1])
+    assert inner < np.finfo(np.float32).max
+    assert np.array_equal(y[ids == 0], np.broadcast_to(np.where(np.arange(m) % 2, np.inf, -np.inf), y[ids == 0].shape))
+    assert np.isnan(y[ids == 2]).all()
+    for a, sign in ((1, 1.0), (3, -1.0)):
+        ref = base + sign * inner * 2.0 ** -120
+        assert (np.abs(y[ids == a] - ref) <= 2.0 ** -15 * (np.abs(ref) + inner * 2.0 ** -120)).all()
