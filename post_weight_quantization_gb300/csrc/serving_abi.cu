@@ -30,6 +30,8 @@ bool tensor_maps_available();
 namespace {
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 int elem_bytes(int dtype) { return dtype == GPTQ_F32 ? 4 : 2; }
+// Keys of a sequence: a tile of keys past them still has 32-bit numbers.
+constexpr int64_t kMaxKeys = 0x7FFFFF00;
 bool any_dtype(int dtype) { return dtype == GPTQ_F32 || dtype == GPTQ_BF16 || dtype == GPTQ_F16; }
 
 // Rows of `width` elements with token stride ld that 16-byte accesses may read.
@@ -160,8 +162,8 @@ gptq_status gptq_kv_attention(const void* Q, int q_dtype, int64_t total_q, int n
     return set_error(GPTQ_ERR_INVALID_ARG, "total_q, batch or max_q out of range");
   if (!(sm_scale > 0.0f) || sm_scale > 1e30f) return set_error(GPTQ_ERR_INVALID_ARG, "sm_scale must be positive and finite");
   if (window < 0) return set_error(GPTQ_ERR_INVALID_ARG, "window must be >= 0");
-  if (table_width < 0 || table_width > 0x7FFFFFFF / page_size || ldt < table_width)
-    return set_error(GPTQ_ERR_INVALID_ARG, "table_width * page_size must fit 31 bits and ldt cover the table");
+  if (table_width < 0 || table_width > kMaxKeys / page_size || ldt < table_width)
+    return set_error(GPTQ_ERR_INVALID_ARG, "table_width * page_size must be at most 2^31 - 256 and ldt cover the table");
   if (total_q == 0 || batch == 0 || max_q == 0) return GPTQ_OK;
   if (!cu_q || !kv_lens || (table_width && !block_table)) return set_error(GPTQ_ERR_INVALID_ARG, "NULL pointer");
   const int64_t width = (int64_t)n_q_heads * head_dim;

@@ -312,3 +312,18 @@ def test_layers_say_whether_they_are_act_order(g):
     assert torch.allclose(g.gptq_adapter_linear(one, X[:3], 64), g.gptq_dequant_gemv(one, X[:3], 64), rtol=1e-4, atol=1e-4)
     pipe = g.HostPipeline(64, 256, act_order=True)
     assert pipe.host_out.act_order and not g.HostPipeline(64, 256).host_out.act_order
+
+
+def test_attention_refuses_lengths_whose_tiles_pass_31_bits(g):
+    lib = g.library()
+
+    def call(width, page):
+        st = lib.gptq_kv_attention(P, 1, 4, 8, 2, 128, 1024, P, P, P, width, width, 4, 1, P, 64, page, 0.1, 1, 0, P, 1024, None,
+                                   P, 0, None)
+        assert st == g.GPTQ_ERR_INVALID_ARG
+        return g.gptq_last_error()
+
+    for page in (16, 48, 256):
+        most = (2 ** 31 - 256) // page
+        assert "workspace" in call(most, page)                     # the next check
+        assert "table_width" in call(most + 1, page) and "table_width" in call((2 ** 31 - 1) // page + 1, page)
