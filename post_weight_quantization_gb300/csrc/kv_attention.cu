@@ -587,7 +587,7 @@ gptq_status kv_attention_launch(const void* Q, int dtype, long long total_q, int
   p.max_q = max_q;
   p.Hq = Hq; p.H = H; p.G = Hq / H; p.batch = (int)batch; p.causal = causal; p.q_f16 = dtype == GPTQ_F16;
   set_pages(p, page);
-  p.window = window;
+  p.window = window > 0x7FFFFFFFLL ? 0 : window;         // every key is nearer than that; sums with it stay in range
   p.scale_log2 = sm_scale * 1.4426950408889634f;
   if (many_rows(D, max_q * p.G)) return kv_attention_tc_launch(p, D, ws, s);
   gptq_status st = GPTQ_OK;

@@ -817,3 +817,16 @@ def test_adapter_linear_extreme_inner_products(g, T):
     for a, sign in ((1, 1.0), (3, -1.0)):
         ref = base + sign * inner * 2.0 ** -120
         assert (np.abs(y[ids == a] - ref) <= 2.0 ** -15 * (np.abs(ref) + inner * 2.0 ** -120)).all()
+
+
+@pytest.mark.parametrize("hq,new", [(2, 5), (8, 40)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attention_windows_of_any_size(g, hq, new, causal):
+    """A window past every position is no window, up to the largest one, for rows before the first key too."""
+    t = Batch([1, 90, 0], [new] * 3, hq, 2, 64, 16, torch.bfloat16, seed=9)
+    want = g.gptq_kv_attention(*t.gpu(g), new, causal=causal)
+    done(g)
+    t.check(want, causal=causal)
+    for window in (200, 2 ** 31 - 1, 2 ** 31, 2 ** 40, 2 ** 63 - 1):
+        assert torch.equal(g.gptq_kv_attention(*t.gpu(g), new, causal=causal, window=window), want), window
+    done(g)
