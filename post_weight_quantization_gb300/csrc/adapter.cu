@@ -606,8 +606,10 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
       }
     }
     if (!ok) { *abort_flag = 1; if (lane == 0) report_device_error(err, DEVERR_TIMEOUT); }
-    // copies still in flight when something gave up: their slots' barriers, with a limit
-    for (uint32_t u = ab > SLOTS ? ab - SLOTS : 0; u < ab; ++u) mbar_wait_bounded(&full[u % SLOTS], (u / SLOTS) & 1u, abort_flag);
+    // copies still in flight when something gave up: their slots' barriers, whose other arrivals may never
+    // come then, so with a limit of 1 ms and whatever the abort flag says
+    for (uint32_t u = ab > SLOTS ? ab - SLOTS : 0; u < ab; ++u)
+      mbar_wait_bounded(&full[u % SLOTS], (u / SLOTS) & 1u, nullptr, 1000000ull);
     } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
     uint32_t ab = 0, unit_no = 0;
