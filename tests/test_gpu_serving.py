@@ -830,3 +830,46 @@ def test_attention_windows_of_any_size(g, hq, new, causal):
     for window in (200, 2 ** 31 - 1, 2 ** 31, 2 ** 40, 2 ** 63 - 1):
         assert torch.equal(g.gptq_kv_attention(*t.gpu(g), new, causal=causal, window=window), want), window
     done(g)
+
+
+MANY_ROWS = [                                    # hq, h, D, page, lens, new, causal, window
+    (6, 2, 128, 64, [9001], [500], True, 0),                     # groups of 3, a partial row tile, more than four parts
+    (24, 8, 128, 64, [9001], [500], True, 0),                    # two to four parts
+    (14, 2, 64, 16, [9001, 3000, 1500], [300, 37, 130], True, 2000),
+    (10, 2, 64, 32, [5000, 1200], [200, 199], False, 0),
+    (16, 1, 128, 48, [131, 4097, 2000], [2, 17, 0], True, 0),
+    (4, 4, 128, 16, [2300], [2300], True, 0),                    # a prompt from an empty cache
+    (4, 2, 64, 256, [3001, 700], [1100, 700], True, 900),
+    (40, 1, 128, 128, [9001] * 3, [1, 1, 1], True, 0),           # wide groups of one token
+    (9, 1, 64, 64, [6000, 6000], [300, 7], False, 1500),
+]
+FEW_ROWS = [
+    (2, 2, 64, 16, [9001], [1], True, 0),                        # one row an item; many parts
+    (32, 2, 64, 32, [9001, 1500], [1, 1], True, 0),              # 16 rows
+    (14, 2, 64, 48, [9001, 8000], [4, 3], True, 0),              # 28 rows, of 32
+    (8, 1, 128, 64, [9001, 40], [1, 1], True, 5000),
+    (12, 1, 128, 128, [9001], [1], True, 0),                     # 12 rows, of 16
+    (10, 2, 128, 16, [9001, 2100, 4000], [3, 1, 2], False, 0),
+    (4, 2, 256, 32, [9001], [1], True, 0),
+    (6, 1, 256, 64, [9001, 3300], [50, 33], True, 0),            # many items of 16 rows
+    (16, 2, 256, 16, [9001] * 8, [3] * 8, True, 3000),
+    (24, 8, 128, 64, [2500 - 61 * i for i in range(40)], [1] * 40, True, 0),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("case", MANY_ROWS + FEW_ROWS, ids=lambda c: "-".join(map(str, (c[0], c[1], c[2], sum(c[5])))))
+def test_attention_of_items_that_are_cut(g, case, dtype):
+    """More than 1024 keys, so that the line of tiles cuts items between CTAs: output and log-sum-exp of
+    every part's join, and the same bits again."""
+    hq, h, D, page, lens, new, causal, window = case
+    t = Long(g, max(lens), h, D, page, seed=hq + D + sum(new))
+    args = t.batch(lens, new, hq, dtype)
+    lse, again = torch.empty((2, sum(new), hq), device="cuda")
+    O = g.gptq_kv_attention(*args, max(new), causal=causal, window=window, lse=lse)
+    O2 = g.gptq_kv_attention(*args, max(new), causal=causal, window=window, lse=again)
+    done(g)
+    assert torch.equal(O, O2) and torch.equal(lse, again)
+    rows = max(new) * (hq // h)
+    t.check(O, lse, range(0, len(lens), 1 + len(lens) // 4), sorted({0, 1, hq // 2, hq - 1}), causal, window,
+            many=D != 256 and rows > (32 if D == 64 else 16))
