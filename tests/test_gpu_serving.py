@@ -873,3 +873,42 @@ def test_attention_of_items_that_are_cut(g, case, dtype):
     rows = max(new) * (hq // h)
     t.check(O, lse, range(0, len(lens), 1 + len(lens) // 4), sorted({0, 1, hq // 2, hq - 1}), causal, window,
             many=D != 256 and rows > (32 if D == 64 else 16))
+
+
+def test_kv_append_every_scale(g):
+    """Every fp16 scale that a row can have (up to twice the largest number over 15), with values on
+    and next to the ties between codes: the bits of a true division."""
+    D, page = 64, 16
+    s = np.arange(1, 0x7C00, dtype=np.uint16).view(np.float16).astype(np.float32)
+    s = s[s <= np.float32(2 * 65504 / 15)]
+    low = np.where(15 * s <= 65504, np.float32(0), np.float32(-65504))
+    low[::2] = np.where(15 * s[::2] <= 65504, -np.minimum(15 * s[::2], 65504).astype(np.float16).astype(np.float32), low[::2])
+    ties = (s[:, None] * (np.arange(15, dtype=np.float32) + np.float32(0.5)) + low[:, None]).astype(np.float32)
+    inf = np.float32(np.inf)
+    x = np.concatenate([low[:, None], (15 * s + low)[:, None], ties, np.nextafter(ties, inf), np.nextafter(ties, -inf),
+                        np.random.default_rng(1).random((len(s), 15), dtype=np.float32) * (15 * s)[:, None] + low[:, None]], axis=1)
+    x = np.concatenate([x, x[:, :D - x.shape[1]]], axis=1).astype(np.float32)
+    T = len(s)
+    for dtype in (torch.float32, torch.bfloat16, torch.float16):
+        K = torch.from_numpy(x).to(dtype)
+        y = np.clip(K.float().numpy(), -65504, 65504)                    # 65504 is 65536 in bf16
+        lo, hi = y.min(1), y.max(1)
+        scale = ((hi - lo) / np.float32(15)).astype(np.float16)
+        low16 = lo.astype(np.float16)
+        if dtype == torch.float32:
+            assert len(set(scale.view(np.uint16).tolist())) > 28000         # nearly every one of them
+        with np.errstate(divide="ignore", invalid="ignore"):
+            q = (y - low16.astype(np.float32)[:, None]) / scale.astype(np.float32)[:, None]
+        codes = np.where(scale[:, None] == 0, 0, np.clip(np.rint(q), 0, 15)).astype(np.uint8)
+        cache = g.KVCache(torch.zeros((-(-T // page), 1, page * (D + 8)), dtype=torch.uint8, device="cuda"), page, 1, D)
+        V = K.flip(0).contiguous()
+        g.gptq_kv_append(cache, K[:, None].cuda(), V[:, None].cuda(), torch.arange(T, device="cuda"))
+        done(g)
+        pool = cache.pool.cpu().numpy()[:, 0]
+        half = page * D // 2
+        num = np.ascontiguousarray(pool[:, 2 * half:]).view(np.float16).reshape(-1, 4)[:T]
+        for kv, order in ((0, slice(None)), (1, slice(None, None, -1))):
+            b = pool[:, kv * half:(kv + 1) * half].reshape(-1, D // 2)[:T]
+            got = np.stack([b & 15, b >> 4], axis=-1).reshape(T, D)
+            assert np.array_equal(got, codes[order]) and np.array_equal(num[:, 2 * kv], scale[order])
+            assert np.array_equal(num[:, 2 * kv + 1], low16[order])
