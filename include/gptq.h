@@ -542,7 +542,8 @@ gptq_status gptq_kv_read(const void* pool, int64_t num_pages, int page_size, int
  *              heads dense, token strides ldq / ldo elements, rows 16-byte aligned.
  *   cu_q       device int32[batch + 1], non-decreasing, within [0, total_q], steps of at most
  *              max_q (a longer sequence gets its first max_q tokens' output, as if it had no
- *              more, and is reported); query tokens outside every sequence get no output.
+ *              more, one whose values are out of range none, and both are reported); query
+ *              tokens outside every sequence get no output.
  *   kv_lens    device int32[batch], in [0, table_width * page_size], which is at most 2^31 - 256.
  *   block_table device int32, batch x table_width, row stride ldt; entries that hold keys
  *              are pages in [0, num_pages), later ones are not read.

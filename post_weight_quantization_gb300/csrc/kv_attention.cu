@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, NT>::OCC) kv_split_kernel(Para
   uint32_t slot = 0, phase = 0;                  // the ring's next tile
   uint32_t use = 0;                              // tiles taken from the ring so far, through all items
   Item it;
-  bool have = line.next(p, it, err);
+  bool have = line.next(p, it);
   int4 cut = make_int4(0, 0, 0, 0);
   if (have && warp < NS - 1 && warp < it.nt) issue(use + warp, cp.source(p, it, warp, D, err));
 
@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, NT>::OCC) kv_split_kernel(Para
 
     // ---- the next item's first tiles are on their way while the warps meet over this one
     Item nx;
-    const bool more = line.next(p, nx, err);
+    const bool more = line.next(p, nx);
     if (more && !dead && warp < NS - 1 && warp < nx.nt) issue(use + warp, cp.source(p, nx, warp, D, err));
 
 #pragma unroll
@@ -583,8 +583,8 @@ gptq_status kv_attention_launch(const void* Q, int dtype, long long total_q, int
   Params p{};
   p.Q = Q; p.O = O; p.lse = lse; p.cu_q = cu_q; p.kv_lens = kv_lens; p.table = table;
   p.pool = reinterpret_cast<const uint8_t*>(pool);
-  p.ldq = ldq; p.ldo = ldo; p.ldt = ldt; p.total_q = total_q; p.table_width = table_width; p.num_pages = num_pages;
-  p.max_q = max_q;
+  p.ldq = ldq; p.ldo = ldo; p.ldt = ldt; p.num_pages = num_pages;
+  p.total_q = (int)total_q; p.max_q = (int)max_q; p.cap = (int)(table_width * page);
   p.Hq = Hq; p.H = H; p.G = Hq / H; p.batch = (int)batch; p.causal = causal; p.q_f16 = dtype == GPTQ_F16;
   set_pages(p, page);
   p.window = window > 0x7FFFFFFFLL ? 0 : window;         // every key is nearer than that; sums with it stay in range
@@ -605,7 +605,7 @@ gptq_status kv_attention_launch(const void* Q, int dtype, long long total_q, int
     // nothing is cut when no item can be longer than kWholeTiles and every CTA gets at most one
     const long long row_items = (max_q * p.G + C::R - 1) / C::R;
     if (table_width * page <= kWholeTiles * TILE && batch * H * row_items <= ctas) return;
-    launch_pdl(kv_join_kernel<DD, C::R>, dim3((unsigned)ctas, NT), dim3(JOIN_WARPS * 32), 0, s, p, device_error_word());
+    launch_pdl(kv_join_kernel<DD, C::R>, dim3((unsigned)ctas, NT), dim3(JOIN_WARPS * 32), 0, s, p);
     count_launch();
     st = check_launch("kv_join_kernel");
   });

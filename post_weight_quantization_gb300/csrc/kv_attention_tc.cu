@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
       Copies cp;
       cp.init(p, lane);
       uint32_t n = 0;
-      while (ok && line.next(p, it, err)) {
+      while (ok && line.next(p, it)) {
         long long src = cp.source(p, it, 0, D, err);
         for (int i = 0; i < it.nt; ++i, ++n) {
           const uint32_t st = n % NC;
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
                       kd + (kk >> 2) * (C::BOX / 16) + 2 * (kk & 3), IDS, kk > 0, leader);
         commit_by(&s_full[2 * x + (j & 1)], leader);
       };
-      while (ok && line.next(p, it, err)) {
+      while (ok && line.next(p, it)) {
         const int groups = it.rows > 128 ? 2 : 1, nh = 2 * it.nt;    // half tiles
         if (nh == 0) continue;
         // the first tile's scores; K is number mat, V number mat + 1 of the ring's matrices
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
     const uint32_t off = blk * p.pb * (D + 8) + at * (D / 2) + half * (D / 4), noff = blk * p.pb * (D + 8) + p.pb * D + at * 8;
     const uint32_t sb = smem_u32(smem), sw = r & 7;
     uint32_t n = 0, mat = 0;
-    while (ok && line.next(p, it, err)) {
+    while (ok && line.next(p, it)) {
       for (int i = 0; i < it.nt; ++i, ++n) {
         const uint32_t st = n % NC, base = sb + C::CODES + st * C::STAGE;
         if (!mbar_wait_bounded(&c_full[st], n / NC & 1u, abort_flag)) { give_up(); break; }
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_tc_kernel(Params p, int* __rest
     const uint32_t st0 = s_tm + 128 * x + lanes, ot = o_tm + D * x + lanes;
     uint32_t ns[2] = {0, 0}, npv = 0, no = 0;                        // waits for S by half tile; half tiles whose P V was asked for; items
     int4 cut = make_int4(0, 0, 0, 0);
-    while (ok && line.next(p, it, err)) {
+    while (ok && line.next(p, it)) {
       if (it.more) cut = make_int4(it.b, it.item, 1 + it.more, 0);
       if (x == 1 && it.rows <= 128) continue;
       const int rr = it.rt * R + 128 * x + r, tk = rr / p.G, hq = it.h * p.G + rr - tk * p.G;
@@ -586,7 +586,7 @@ static gptq_status tc_launch(kva::Params p, void* ws, cudaStream_t s) {
   tc::kv_tc_kernel<D><<<ctas, tc::THREADS, C::SMEM, s>>>(p, device_error_word());
   count_launch();
   if (gptq_status st = check_launch("kv_tc_kernel")) return st;
-  launch_pdl(kv_join_kernel<D, tc::R>, dim3(ctas, 8), dim3(JOIN_WARPS * 32), 0, s, p, device_error_word());
+  launch_pdl(kv_join_kernel<D, tc::R>, dim3(ctas, 8), dim3(JOIN_WARPS * 32), 0, s, p);
   count_launch();
   return check_launch("kv_join_kernel");
 }

@@ -25,7 +25,8 @@ struct Params {
   const int* kv_lens;
   const int* table;
   const uint8_t* pool;
-  long long ldq, ldo, ldt, total_q, table_width, num_pages, max_q;
+  long long ldq, ldo, ldt, num_pages;
+  int total_q, max_q, cap;                      // query tokens, the most of a sequence; keys that a row of the table holds
   int Hq, H, G, page, batch, causal, q_f16;
   int pb, pb_log2;                              // keys of a block: the largest power of two up to TILE that divides page
   uint32_t page_mul;                            // ceil(2^32 / (page / pb)); 0 when page is pb
@@ -69,28 +70,30 @@ struct Seq {
   long long items;               // H * nrt
 };
 
-__device__ __forceinline__ Seq load_seq(const Params& p, int b, int R, int* err) {
+// Its tokens a ... z - 1 are in range (as unsigned numbers: negative ones are large).
+__device__ __forceinline__ bool steps_ok(const Params& p, int a, int z) {
+  return (unsigned)z <= (unsigned)p.total_q && (unsigned)a <= (unsigned)z;
+}
+// Steps out of range count as no tokens, more tokens than max_q, by which the host has chosen the
+// launches, as max_q, and lengths are limited to theirs. find_start, which every CTA begins with, reports all three.
+__device__ __forceinline__ Seq load_seq(const Params& p, int b, int R) {
   Seq s;
-  long long a = p.cu_q[b], z = p.cu_q[b + 1], len = p.kv_lens[b];
-  const long long cap = p.table_width * p.page;
-  // more tokens than max_q count as max_q: the host has chosen the launches by it
-  if (a < 0 || z > p.total_q || z < a || z - a > p.max_q || len < 0 || len > cap) {
-    report_device_error(err, DEVERR_INDEX);
-    a = a < 0 ? 0 : a;
-    z = z > p.total_q ? p.total_q : z;
-    z = z - a > p.max_q ? a + p.max_q : z;
-    len = len < 0 ? 0 : (len > cap ? cap : len);
-  }
+  const int a = p.cu_q[b], z = p.cu_q[b + 1], len = min(max(p.kv_lens[b], 0), p.cap);
   s.tok0 = a;
-  s.nq = z > a ? (int)(z - a) : 0;
-  s.len = (int)len;
-  const long long lo = p.window > 0 ? len - s.nq - p.window + 1 : 0;
+  s.nq = steps_ok(p, a, z) ? min(z - a, p.max_q) : 0;
+  s.len = len;
+  const long long lo = p.window > 0 ? (long long)len - s.nq - p.window + 1 : 0;
   s.t0 = lo > 0 ? (int)(lo / TILE) : 0;
   const int n = (s.len + TILE - 1) / TILE - s.t0;
   s.tiles = n > 0 ? n : 1;
   s.nrt = (int)(((long long)s.nq * p.G + R - 1) / R);
   s.items = (long long)p.H * s.nrt;
   return s;
+}
+
+__device__ __forceinline__ bool seq_ok(const Params& p, int b) {
+  const int a = p.cu_q[b], z = p.cu_q[b + 1];
+  return steps_ok(p, a, z) && z - a <= p.max_q && (unsigned)p.kv_lens[b] <= (unsigned)p.cap;
 }
 
 __device__ __forceinline__ void store_out(const Params& p, long long at, float4 v) {
@@ -121,7 +124,8 @@ __device__ __forceinline__ void find_start(const Params& p, long long* sh, long 
   for (int k = 0; k < nb; ++k) {
     const int b = tid * nb + k;
     if (tid < SCAN && b < p.batch) {
-      const Seq q = load_seq(p, b, R, err);
+      const Seq q = load_seq(p, b, R);
+      if (!seq_ok(p, b)) report_device_error(err, DEVERR_INDEX);
       items += q.items;
       units += q.items * (q.tiles + COST);
       if (q.items) longest = max(longest, q.tiles);
@@ -156,7 +160,7 @@ __device__ __forceinline__ void find_start(const Params& p, long long* sh, long 
   if (tid < SCAN && start >= at && start < at + mine) {              // exactly one thread when start < total
     for (int k = 0; k < nb; ++k) {
       const int b = tid * nb + k;
-      const Seq q = load_seq(p, b, R, err);
+      const Seq q = load_seq(p, b, R);
       const long long u = whole ? q.items : q.items * (q.tiles + COST);
       if (start < at + u) {
         sh[12] = b;
@@ -198,9 +202,9 @@ struct Line {
     left = total - per * blockIdx.x;
     left = left < per ? left : per;
   }
-  __device__ __forceinline__ bool next(const Params& p, Item& it, int* err) {
+  __device__ __forceinline__ bool next(const Params& p, Item& it) {
     while (left > 0 && b < p.batch) {
-      it.sq = load_seq(p, b, R, err);
+      it.sq = load_seq(p, b, R);
       const int cost = one_each ? 1 : it.sq.tiles + COST;
       if (off >= it.sq.items * cost) {
         ++b;
@@ -284,7 +288,7 @@ struct Copies {
 // warps share a row.
 constexpr int JOIN_WARPS = 16;
 template <int D, int R>
-__global__ void __launch_bounds__(JOIN_WARPS * 32) kv_join_kernel(Params p, int* __restrict__ err) {
+__global__ void __launch_bounds__(JOIN_WARPS * 32) kv_join_kernel(Params p) {
   constexpr int VPL = D / 32, PART = R * D + 2 * R;
   using V = typename std::conditional<VPL == 2, float2, float4>::type;       // a lane's values, NV vectors of VW
   constexpr int NV = VPL == 2 ? 1 : VPL / 4, VW = VPL / NV;
@@ -294,7 +298,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) kv_join_kernel(Params p, int*
   const int c = blockIdx.x;
   const int4 cut = p.cut[c];
   if (cut.z == 0) return;
-  const Seq sq = load_seq(p, cut.x, R, err);
+  const Seq sq = load_seq(p, cut.x, R);
   const int h = cut.y / sq.nrt, rt = row_tile(cut.y - h * sq.nrt, sq.nrt), np = cut.z;
   const long long all_rows = (long long)sq.nq * p.G;
   auto part_of = [&](int k) { return p.part + (2LL * (c + k) + (k == 0 ? 1 : 0)) * PART; };

@@ -912,3 +912,30 @@ def test_kv_append_every_scale(g):
             got = np.stack([b & 15, b >> 4], axis=-1).reshape(T, D)
             assert np.array_equal(got, codes[order]) and np.array_equal(num[:, 2 * kv], scale[order])
             assert np.array_equal(num[:, 2 * kv + 1], low16[order])
+
+
+@pytest.mark.parametrize("D,new", [(64, 1), (128, 40), (256, 2)])
+def test_attention_steps_and_lengths_of_any_bits(g, D, new):
+    """cu_q and kv_lens with numbers far out of range: reported, outputs of the other sequences as they
+    are, nothing written outside them."""
+    t = Long(g, 300, 2, D, 16, seed=D)
+    cache, Q, cu, kv, table = t.batch([200, 64, 300], [new] * 3, 4)
+    for at, value in ((1, -2 ** 31), (1, 2 ** 31 - 1), (2, -2 ** 31), (3, 2 ** 31 - 1), (3, -1), (0, -2 ** 31), (0, 2 ** 31 - 1)):
+        bad = cu.clone()
+        bad[at] = value
+        O, lse = torch.full_like(Q, 5.0), torch.full(Q.shape[:2], 5.0, device="cuda")
+        g.gptq_kv_attention(cache, Q, bad, kv, table, new, O=O, lse=lse)
+        torch.cuda.synchronize()
+        with pytest.raises(g.GPTQError):
+            g.gptq_device_check()
+        assert torch.isfinite(O.float()).all()
+        t.check(O, lse, [b for b in range(3) if at not in (b, b + 1)], (0, 3))
+    for b, value in ((1, -1), (1, -2 ** 31), (2, 2 ** 31 - 1)):
+        bad = kv.clone()
+        bad[b] = value
+        O, lse = torch.full_like(Q, 5.0), torch.full(Q.shape[:2], 5.0, device="cuda")
+        g.gptq_kv_attention(cache, Q, cu, bad, table, new, O=O, lse=lse)
+        torch.cuda.synchronize()
+        with pytest.raises(g.GPTQError):
+            g.gptq_device_check()
+        t.check(O, lse, [x for x in range(3) if x != b], (0, 3))
