@@ -535,8 +535,9 @@ gptq_status gptq_kv_read(const void* pool, int64_t num_pages, int page_size, int
  * block_table[b][1], ..., and the query tokens cu_q[b] ... cu_q[b + 1] - 1; its query token i
  * stands at position p = kv_lens[b] - (number of its query tokens) + i. It sees keys j <= p
  * when `causal` (all keys otherwise), and, with window > 0, only j > p - window. A query that
- * sees no key gets zeros (and an lse of -infinity). Query head h reads cache head
- * h / (n_q_heads / n_kv_heads).
+ * sees no key gets zeros (and an lse of -infinity); one that sees a key whose K or V row holds a
+ * NaN gets NaN in every value (its lse is one when K's row holds it, and may be when V's alone
+ * does). Query head h reads cache head h / (n_q_heads / n_kv_heads).
  *
  *   Q, O       device, total_q x n_q_heads x head_dim of q_dtype (GPTQ_BF16 or GPTQ_F16),
  *              heads dense, token strides ldq / ldo elements, rows 16-byte aligned.

@@ -939,3 +939,26 @@ def test_attention_steps_and_lengths_of_any_bits(g, D, new):
         with pytest.raises(g.GPTQError):
             g.gptq_device_check()
         t.check(O, lse, [x for x in range(3) if x != b], (0, 3))
+
+
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("D,hq,new", [(64, 8, 2), (128, 8, 2), (256, 8, 2), (64, 8, 40), (128, 8, 40), (256, 8, 40)])
+def test_attention_nan_in_one_row_of_a_key(g, which, D, hq, new):
+    """A NaN in a key's K row alone or V row alone makes NaN of every value of the rows that see the key,
+    and of no other row's, whatever tile it is in."""
+    for place in (700, 899):
+        t = Batch([900], [new], hq, 1, D, 16, torch.bfloat16, seed=D)
+        lse, lse2 = torch.empty((2, new, hq), device="cuda")
+        clean = g.gptq_kv_attention(*t.gpu(g), new, window=150, lse=lse)
+        slot = int(t.table[0, place // 16]) * 16 + place % 16
+        row = np.full(D, np.nan)
+        k, v = so.read_slot(t.pool, 16, D, slot, 0)
+        so.write_slot(t.pool, 16, D, slot, 0, row if which == "k" else k, row if which == "v" else v)
+        O = g.gptq_kv_attention(*t.gpu(g), new, window=150, lse=lse2)
+        done(g)
+        pos = torch.arange(900 - new, 900)
+        sees = ((pos >= place) & (pos - 150 < place)).cuda()
+        assert sees.any() == (place == 899) and torch.isnan(O[sees]).all()
+        assert torch.equal(O[~sees], clean[~sees]) and torch.equal(lse2[~sees], lse[~sees])
+        if which == "k":
+            assert torch.isnan(lse2[sees]).all()
