@@ -103,7 +103,14 @@ struct Call {
   }
 };
 
-void done(gptq_status st) {
+// The library's call without the interpreter's lock: a launch waits while the stream's queue is full,
+// and other threads go on meanwhile, as they do in the long way. About 0.3 us a call. (`f` touches no Python
+// object; the arguments' tensors are held by the caller.)
+template <typename F>
+void call(F&& f) {
+  PyThreadState* state = PyEval_SaveThread();
+  const gptq_status st = f();
+  PyEval_RestoreThread(state);
   if (st != GPTQ_OK) throw Decline{};                      // the long way reports it
 }
 
@@ -161,10 +168,12 @@ PyObject* adapter_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
     at::Tensor own;
     size_t bytes = 0;
     void* ws = c.workspace(a[14], gptq_adapter_workspace_size(m, d, bits, gs, T, rank), bytes, own);
-    done(gptq_adapter_linear((const uint32_t*)qw, (const float*)sc, (const float*)ze, m, d, bits, gs, (const uint16_t*)X.data_ptr(),
-                             T, T > 1 ? X.stride(0) : d, (const uint16_t*)A, (const uint16_t*)B, (const float*)alpha, na, rank,
-                             (const int32_t*)ids, Y.data_ptr(), yt == at::kBFloat16 ? GPTQ_BF16 : GPTQ_F32,
-                             T > 1 ? Y.stride(0) : m, ws, bytes, c.stream));
+    call([&] {
+      return gptq_adapter_linear((const uint32_t*)qw, (const float*)sc, (const float*)ze, m, d, bits, gs,
+                                 (const uint16_t*)X.data_ptr(), T, T > 1 ? X.stride(0) : d, (const uint16_t*)A, (const uint16_t*)B,
+                                 (const float*)alpha, na, rank, (const int32_t*)ids, Y.data_ptr(),
+                                 yt == at::kBFloat16 ? GPTQ_BF16 : GPTQ_F32, T > 1 ? Y.stride(0) : m, ws, bytes, c.stream);
+    });
     return back(a[12], Y);
   });
 }
@@ -217,10 +226,14 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     void* wq = c.dense_or_null(a[5], at::kFloat, {dim});
     void* wk = c.dense_or_null(a[6], at::kFloat, {dim});
-    done(gptq_qk_norm_rope(Q.data_ptr(), K, code_of(in), T, (int)hq, (int)hk, (int)dim, ldq, ldk, (const float*)wq,
-                           (const float*)wk, real(a[7]), (const float*)cs, (const float*)sn, n_pos, (int)rot, flag(a[8]),
-                           (const int32_t*)pos, Qo.data_ptr(), Ko.defined() ? Ko.data_ptr() : nullptr, code_of(out), ldqo,
-                           ldko, c.stream));
+    const float eps = real(a[7]);
+    const bool interleaved = flag(a[8]);
+    call([&] {
+      return gptq_qk_norm_rope(Q.data_ptr(), K, code_of(in), T, (int)hq, (int)hk, (int)dim, ldq, ldk, (const float*)wq,
+                               (const float*)wk, eps, (const float*)cs, (const float*)sn, n_pos, (int)rot, interleaved,
+                               (const int32_t*)pos, Qo.data_ptr(), Ko.defined() ? Ko.data_ptr() : nullptr, code_of(out),
+                               ldqo, ldko, c.stream);
+    });
     PyObject* q = back(a[9], Qo);
     PyObject* k = Ko.defined() ? back(a[10], Ko) : Py_NewRef(Py_None);
     PyObject* both = q && k ? PyTuple_Pack(2, q, k) : nullptr;
@@ -253,8 +266,10 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (code_of(type) == kBad || V.scalar_type() != type) throw Decline{};
     const int64_t ldk = c.heads(K, -1, p.heads, p.dim), T = K.size(0), ldv = c.heads(V, T, p.heads, p.dim);
     void* slots = c.dense(a[6], at::kLong, {T});
-    done(gptq_kv_append(K.data_ptr(), V.data_ptr(), code_of(type), T, p.heads, p.dim, ldk, ldv, (const int64_t*)slots, p.data,
-                        p.pages, p.page, c.stream));
+    call([&] {
+      return gptq_kv_append(K.data_ptr(), V.data_ptr(), code_of(type), T, p.heads, p.dim, ldk, ldv, (const int64_t*)slots,
+                            p.data, p.pages, p.page, c.stream);
+    });
     Py_RETURN_TRUE;
   });
 }
@@ -278,8 +293,10 @@ PyObject* kv_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (kv[i].scalar_type() != type) throw Decline{};
       ld[i] = c.heads(kv[i], T, p.heads, p.dim);
     }
-    done(gptq_kv_read(p.data, p.pages, p.page, p.heads, p.dim, (const int64_t*)slots, T, kv[0].data_ptr(), kv[1].data_ptr(),
-                      code_of(type), ld[0], ld[1], c.stream));
+    call([&] {
+      return gptq_kv_read(p.data, p.pages, p.page, p.heads, p.dim, (const int64_t*)slots, T, kv[0].data_ptr(), kv[1].data_ptr(),
+                          code_of(type), ld[0], ld[1], c.stream);
+    });
     PyObject *k = back(a[6], kv[0]), *v = back(a[7], kv[1]);
     PyObject* both = k && v ? PyTuple_Pack(2, k, v) : nullptr;
     Py_XDECREF(k);
@@ -311,10 +328,13 @@ PyObject* kv_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     at::Tensor own;
     size_t bytes = 0;
     void* ws = c.workspace(a[14], gptq_kv_attention_workspace_size(total, (int)hq, p.heads, p.dim, batch, max_q), bytes, own);
-    done(gptq_kv_attention(Q.data_ptr(), code_of(type), total, (int)hq, p.heads, p.dim, ldq, (const int32_t*)cu,
-                           (const int32_t*)lens, (const int32_t*)table.data_ptr(), batch > 1 ? table.stride(0) : width, width,
-                           batch, max_q, p.data, p.pages, p.page, scale, flag(a[10]), window, O.data_ptr(), ldo, (float*)lse, ws,
-                           bytes, c.stream));
+    const bool causal = flag(a[10]);
+    call([&] {
+      return gptq_kv_attention(Q.data_ptr(), code_of(type), total, (int)hq, p.heads, p.dim, ldq, (const int32_t*)cu,
+                               (const int32_t*)lens, (const int32_t*)table.data_ptr(), batch > 1 ? table.stride(0) : width,
+                               width, batch, max_q, p.data, p.pages, p.page, scale, causal, window, O.data_ptr(), ldo,
+                               (float*)lse, ws, bytes, c.stream);
+    });
     return back(a[12], O);
   });
 }

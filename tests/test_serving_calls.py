@@ -148,3 +148,37 @@ def test_references_and_memory_are_given_back(g):
         g.gptq_qk_norm_rope(Q, None)
     assert [sys.getrefcount(x) for x in (Q, out)] == refs[:2] and torch.cuda.memory_allocated() == held
     assert abs(sys.getrefcount(None) - refs[2]) < 100
+
+
+@pytest.mark.gpu
+def test_other_threads_go_on_while_a_launch_waits(g):
+    """A launch waits while the stream's queue is full; other Python threads run meanwhile."""
+    import threading
+    import time
+    Q = torch.randn((3, 2, 64), device="cuda").bfloat16()
+    out = torch.empty_like(Q)
+    for _ in range(3):
+        g.gptq_qk_norm_rope(Q, None, Q_out=out)
+    torch.cuda._sleep(1000)
+    torch.cuda.synchronize()
+    gaps, stop = [], threading.Event()
+
+    def tick():
+        at = time.perf_counter()
+        while not stop.is_set():
+            time.sleep(0.001)
+            now = time.perf_counter()
+            gaps.append(now - at)
+            at = now
+    thread = threading.Thread(target=tick)
+    thread.start()
+    start = time.perf_counter()
+    torch.cuda._sleep(2_000_000_000)                               # about a second
+    for _ in range(6000):                                          # more than a queue holds
+        g.gptq_qk_norm_rope(Q, None, Q_out=out)
+    waited = time.perf_counter() - start
+    stop.set()
+    thread.join()
+    torch.cuda.synchronize()
+    assert waited > 0.4, waited                                    # the launches did wait
+    assert max(gaps) < waited / 2, (max(gaps), waited)
