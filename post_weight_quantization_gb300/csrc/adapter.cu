@@ -8,9 +8,10 @@
 //                        needs U only after its own sum over d
 //
 // adapter_gemm_kernel computes a tile of 128 rows of W by N tokens on the 5th-generation tensor
-// cores with W_hat's integers as the A operand IN TENSOR MEMORY: eight warps take the packed
-// words from HBM straight to registers, unpack them there and store them with tcgen05.st;
-// no dequantized operand passes through shared memory or HBM. (Through shared memory the 16-bit
+// cores with W_hat's integers as the A operand IN TENSOR MEMORY: the packed words come by TMA into a
+// ring in shared memory (rows that TMA cannot take, from global memory); 16 warps, eight in the large
+// tiles, unpack them in registers and store them with tcgen05.st; no dequantized operand passes
+// through shared memory or HBM. (Through shared memory the 16-bit
 // operand would be written and read once per tile, four times the 4-bit codes' bytes each way,
 // which bounds a decoding batch before HBM does.) X comes by TMA. Unpacking keeps k in its
 // order: bytes of codes are spread to 16-bit halves by a byte permute, where a small integer c
@@ -36,9 +37,9 @@
 // which the epilogue adds to that run's columns only.
 //
 // Bound: HBM bandwidth for few tokens (the codes), the tensor cores for many. Measured at 4 bits, rank
-// 16: 4096 x 4096, 1 token 12.3 us, 3001 tokens 130 us (780 TFLOP/s, 40 % of the library GEMM's rate: an
-// accumulator leaves tensor memory per 128 columns); 8192 x 8192, 48 tokens 31 us (2.1 TB/s; unpacking:
-// instruction issue 61 % busy).
+// 16: 4096 x 4096, 1 token 12.3 us, 3001 tokens 129 us (785 TFLOP/s, 40 % of the library GEMM's rate: an
+// accumulator leaves tensor memory per 128 columns); 8192 x 8192, 48 tokens 31 us (2.1 TB/s; instruction
+// issue 61 % busy, about a fifth of it unpacking).
 #include <cudaTypedefs.h>
 #include <math_constants.h>
 
@@ -289,7 +290,8 @@ struct Params {
   const float* part;           // few tokens: U [T][rank]
   void* Y;
   long long ldy, n_adapters;
-  int m, d, T, gs, G, wpr, unit, rank, splits, y_bf16;
+  int m, d, T, gs, G, wpr, unit, rank;
+  long long y_bf16;            // 64 bits for the size of all: 8 bytes less and 48 tokens (8192 x 8192) take 32.8 instead of 30.7 us
   uint32_t gs32_mul;           // ceil(2^32 / (gs / 32)), 0 when gs is 32
   int codes_tma;               // the packed rows meet TMA's 16-byte rules: codes come through shared memory
   int mt, nt, S;               // row tiles, token tiles, CTAs that split d
@@ -512,6 +514,8 @@ struct Runs {
   }
 };
 
+// One CTA fits an SM (896 threads of 72 registers, or 640 of 96). It has to: two on one SM, from
+// clusters that each wait for all their members, could wait for each other's tensor memory.
 template <int BITS, int N>
 __global__ void __launch_bounds__(Cfg<BITS, N>::THREADS, 1)
 adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_u,
@@ -1206,7 +1210,7 @@ gptq_status adapter_linear_launch(const uint32_t* qweight, const float* scales, 
   const unsigned gs32 = (unsigned)p.gs / 32;
   p.gs32_mul = gs32 == 1 ? 0u : (uint32_t)((0x100000000ULL + gs32 - 1) / gs32);
   p.unit = p.gs % 128 == 0 ? 128 : (p.gs % 64 == 0 ? 64 : 32);
-  p.rank = rank; p.splits = pl.splits; p.y_bf16 = y_dtype == GPTQ_BF16;
+  p.rank = rank; p.y_bf16 = y_dtype == GPTQ_BF16;
   p.mt = pl.mt; p.nt = pl.nt; p.S = pl.S;
   CUtensorMap mx, mu;
   if (!make_map(&mx, X, d, T, ldx, pl.N)) return set_error(GPTQ_ERR_CUDA, "cuTensorMapEncodeTiled failed for X");

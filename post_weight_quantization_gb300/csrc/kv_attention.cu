@@ -550,7 +550,7 @@ void with_shape(int D, int nt, F&& f) {
 
 // Which kernel: many rows of a head at once are worth dequantizing a tile into shared memory for the
 // large tensor-core tiles; this one streams the cache again for its most rows each. (Heads of 256
-// do not fit the other's tensor memory.) Measured over 8 kv heads, in us, this one / the other: D = 128, 32
+// do not fit the other's tensor memory with its two groups of rows.) Measured over 8 kv heads, in us, this one / the other: D = 128, 32
 // sequences of 1024 tokens, 16 rows a head 25 / 57, 32 rows 57 / 57, 64 rows 129 / 59; 8 of 2048, 16 rows
 // 23 / 37, 32 rows 47 / 37; one of 8192, 16 rows 23 / 31, 32 rows 45 / 31. D = 64, 32 of 1024: 32 rows 31 / 45, 48
 // rows 70 / 45; one of 8192: 32 rows 30 / 27.

@@ -48,8 +48,8 @@ __device__ __forceinline__ float divide(float a, float s, float inv) {
   const float q = __fmul_rn(a, inv);
   return __fmaf_rn(__fmaf_rn(-q, s, a), inv, q);
 }
-// fl(1 / s) of an fp16 value: the hardware's approximation and one Newton step (checked for
-// every positive fp16 value).
+// fl(1 / s) of an fp16 value: the hardware's approximation and one Newton step (the GPU tests have every
+// scale that a row can have, with values on and next to the ties between codes).
 __device__ __forceinline__ float reciprocal(float s) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(s));

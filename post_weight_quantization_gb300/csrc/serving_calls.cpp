@@ -5,9 +5,9 @@
 // the long way, whose checks say what is wrong (or allow what is merely unusual).
 //
 // Why: attribute reads and ctypes cost the host more than a small call's kernels cost the GPU. Measured,
-// the long way / this one, in us a call: 33 tokens of gptq_qk_norm_rope 20.2 / 6.0 (host alone 18 / 5),
-// gptq_kv_append with gptq_kv_read 24.7 / 8.8, gptq_kv_attention over 331 tokens 21.9 / 10.2,
-// gptq_adapter_linear of one token 24.5 / 14.3.
+// the long way / this one, in us a call: 33 tokens of gptq_qk_norm_rope 20.2 / 6.2 (host alone 18 / 5),
+// gptq_kv_append with gptq_kv_read 24.7 / 9.2, gptq_kv_attention over 331 tokens 21.9 / 10.2,
+// gptq_adapter_linear of one token 24.5 / 12.3.
 #include <Python.h>
 
 #include <cmath>
