@@ -238,8 +238,9 @@ def _empty(shape, dtype, device, stream=None, keep: bool = True) -> torch.Tensor
     memory is not given out again before the current stream's work at that time is done either."""
     if stream is None or _stream(stream) == _stream(None):
         return torch.empty(shape, dtype=dtype, device=device)
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
-    with torch.cuda.stream(s):
+    if not isinstance(stream, torch.cuda.Stream):       # a handle; 1 is cudaStreamLegacy, the default stream
+        stream = torch.cuda.ExternalStream(int(stream) if int(stream) != 1 else 0)
+    with torch.cuda.stream(stream):
         t = torch.empty(shape, dtype=dtype, device=device)
     if keep:
         t.record_stream(torch.cuda.current_stream())

@@ -962,3 +962,23 @@ def test_attention_nan_in_one_row_of_a_key(g, which, D, hq, new):
         assert torch.equal(O[~sees], clean[~sees]) and torch.equal(lse2[~sees], lse[~sees])
         if which == "k":
             assert torch.isnan(lse2[sees]).all()
+
+
+def test_streams_by_handle(g):
+    """A stream as a handle: torch's own, the default stream's two (0 and 1) and the thread's own (2), with the
+    current stream another one."""
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    X = torch.randn((40, 256), generator=gen, device="cuda").bfloat16()
+    q = g.quantize_layer(torch.randn((64, 256), generator=gen, device="cuda"), [X])[0]
+    calls = (lambda s: g.gptq_adapter_linear(q, X, 64, stream=s), lambda s: g.gptq_dequant_gemm(q, X, 64, stream=s),
+             lambda s: g.gptq_qk_norm_rope(X.view(40, 2, 128), None, stream=s)[0])
+    want = [c(None) for c in calls]
+    torch.cuda.synchronize()
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    for handle in (other.cuda_stream, 0, 1, 2):
+        for current in (torch.cuda.default_stream(), side):
+            with torch.cuda.stream(current):
+                got = [c(handle) for c in calls]
+                torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want)), handle
+    done(g)
