@@ -16,7 +16,10 @@
 //     scores leave with their key on the lane row; one movmatrix per 8 x 8 tile brings
 //     the probabilities to the B layout of O^T = V^T P^T (A = 16 dims x 16 keys of codes).
 //   * The probabilities times the key's V scale are rounded to fp16 for the second product:
-//     2^-11 of each, random in sign, against the output's own 2^-8 or 2^-11. They are
+//     2^-11 of each, random in sign, against the output's own 2^-8 for bf16. For fp16 outputs, which
+//     round to 2^-11 themselves, they are two fp16 parts (22 bits) and two products: with one, the
+//     error against 64 bits was 1.1 to 1.56 times the output's rounding, with two it is 1.00 (and two
+//     sequences of 131000 keys take 74 instead of 69 us, 48 ragged ones 45 instead of 43). They are
 //     brought to the top of fp16's range by a power of two that follows the largest V scale
 //     seen, so small probabilities keep their bits down to 2^-24 of the largest.
 //   Why mma.sync and not tcgen05: the product is bound by HBM bandwidth (one pass over the
@@ -101,7 +104,7 @@ struct State {
   float vlim, vinv;              // V scales below vlim = 2^(x+1) are multiplied by vinv = 2^(kVExp - x)
 };
 
-template <int D, int NT, bool MASK>
+template <int D, int NT, bool FINE, bool MASK>
 __device__ __forceinline__ void chunk(State<D, NT>& st, uint32_t k_0, uint32_t k_1, uint32_t n_0, uint32_t n_1, uint32_t pb,
                                       int key0, int g, int t) {
   constexpr int KW = D / 32;                     // K words of a key per lane, words KW t ...
@@ -240,7 +243,7 @@ __device__ __forceinline__ void chunk(State<D, NT>& st, uint32_t k_0, uint32_t k
   }
 #pragma unroll
   for (int mt = 0; mt < 2; ++mt) {
-    uint32_t b[NT][2];
+    uint32_t b[NT][2], b2[NT][2];                // FINE: what the rounding left over
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const float c = vs[mt][e] * st.vinv;
@@ -259,7 +262,12 @@ __device__ __forceinline__ void chunk(State<D, NT>& st, uint32_t k_0, uint32_t k
             pc[i] = pr * c;
           }
         }
-        b[n][e] = movmatrix(pack_half2(pc[0], pc[1]));
+        const uint32_t h = pack_half2(pc[0], pc[1]);
+        b[n][e] = movmatrix(h);
+        if (FINE) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+          b2[n][e] = movmatrix(pack_half2(pc[0] - f.x, pc[1] - f.y));
+        }
       }
     }
     // V^T fragments: keys of tile rows 2t, 2t + 1 (low) and 2t + 8, 2t + 9 (high)
@@ -278,16 +286,20 @@ __device__ __forceinline__ void chunk(State<D, NT>& st, uint32_t k_0, uint32_t k
         const uint32_t sel = (uint32_t)(by * 0x0011 + (4 + by) * 0x1100);
         const uint32_t l2 = prmt(v0[w], v1[w], sel), h2 = prmt(v2[w], v3[w], sel);
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n) {
           mma_f16(st.o[4 * w + by][n], l2 & 0x000F000Fu, l2 & 0x00F000F0u, h2 & 0x000F000Fu, h2 & 0x00F000F0u, b[n][0],
                   b[n][1]);
+          if (FINE)
+            mma_f16(st.o[4 * w + by][n], l2 & 0x000F000Fu, l2 & 0x00F000F0u, h2 & 0x000F000Fu, h2 & 0x00F000F0u, b2[n][0],
+                    b2[n][1]);
+        }
       }
   }
 }
 
 
 
-template <int D, int NT>
+template <int D, int NT, bool FINE>
 __global__ void __launch_bounds__(THREADS, Cfg<D, NT>::OCC) kv_split_kernel(Params p, int* __restrict__ err) {
   using C = Cfg<D, NT>;
   constexpr int R = C::R, NS = C::NS, KW = D / 32, VW = D / 64;
@@ -431,9 +443,9 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, NT>::OCC) kv_split_kernel(Para
       const uint32_t base = ring + slot * C::STAGE;
       const int key0 = (it.tl + i) * TILE + warp * KC;
       if (i >= plain_lo && i <= plain_hi)
-        chunk<D, NT, false>(st, base + koff[0], base + koff[1], base + noff[0], base + noff[1], p.pb, key0, g, t);
+        chunk<D, NT, FINE, false>(st, base + koff[0], base + koff[1], base + noff[0], base + noff[1], p.pb, key0, g, t);
       else if (key0 < it.hi_all && key0 + KC > it.lo_all)
-        chunk<D, NT, true>(st, base + koff[0], base + koff[1], base + noff[0], base + noff[1], p.pb, key0, g, t);
+        chunk<D, NT, FINE, true>(st, base + koff[0], base + koff[1], base + noff[0], base + noff[1], p.pb, key0, g, t);
       // the stage's words have been read: without the fence nothing keeps the next copy, which is
       // another proxy's write, behind loads that are still on their way to the MMAs
       fence_proxy_async_smem();
@@ -594,12 +606,13 @@ gptq_status kv_attention_launch(const void* Q, int dtype, long long total_q, int
   with_shape(D, row_tiles(D, max_q * p.G), [&](auto d, auto n) {
     constexpr int DD = decltype(d)::value, NT = decltype(n)::value;
     using C = Cfg<DD, NT>;
-    static PerDevice done;
-    if ((st = allow_smem(done, kv_split_kernel<DD, NT>, C::SMEM, "kv_split_kernel"))) return;
+    static PerDevice done[2];
+    const auto kernel = p.q_f16 ? kv_split_kernel<DD, NT, true> : kv_split_kernel<DD, NT, false>;
+    if ((st = allow_smem(done[p.q_f16], kernel, C::SMEM, "kv_split_kernel"))) return;
     const long long ctas = (long long)sm_count() * C::OCC;
     p.cut = reinterpret_cast<int4*>(ws);
     p.part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(ws) + round256(16 * (size_t)ctas));
-    kv_split_kernel<DD, NT><<<(unsigned)ctas, THREADS, C::SMEM, s>>>(p, device_error_word());
+    kernel<<<(unsigned)ctas, THREADS, C::SMEM, s>>>(p, device_error_word());
     count_launch();
     if ((st = check_launch("kv_split_kernel"))) return;
     // nothing is cut when no item can be longer than kWholeTiles and every CTA gets at most one

@@ -982,3 +982,39 @@ def test_streams_by_handle(g):
                 torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(got, want)), handle
     done(g)
+
+
+def _fp16_error(g, D, hq, h, n, new, window):
+    """The error of fp16 outputs over values without a mean, where no rounding is averaged away, in the
+    2-norm and in units of the rounding of the exact output."""
+    gen = torch.Generator(device="cuda").manual_seed(n + D)
+    page, batch = 16, 4
+    pages = -(-n // page)
+    cache = g.KVCache.empty(batch * pages, page, h, D)
+    at = torch.arange(n, device="cuda")
+    table = torch.arange(batch * pages, device="cuda").view(batch, pages)
+    Q = (1.5 * torch.randn((batch * new, hq, D), device="cuda", generator=gen)).half()
+    want = []
+    for b in range(batch):
+        slots = table[b, at // page] * page + at % page
+        g.gptq_kv_append(cache, *(torch.randn((n, h, D), device="cuda", generator=gen) for _ in range(2)), slots)
+        k, v = (x.double() for x in g.gptq_kv_read(cache, slots, dtype=torch.float32))
+        pos = torch.arange(n - new, n, device="cuda")[:, None]
+        see = (at <= pos) & ((at > pos - window) if window else (at >= 0))
+        q = Q[b * new:(b + 1) * new].double()
+        s = torch.einsum("ihd,khd->ihk", q, k.repeat_interleave(hq // h, 1)) * D ** -0.5
+        p = torch.softmax(s.masked_fill(~see[:, None], -float("inf")), -1)
+        want.append(torch.einsum("ihk,khd->ihd", p, v.repeat_interleave(hq // h, 1)))
+    want = torch.cat(want)
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    O = g.gptq_kv_attention(cache, Q, ints([new * i for i in range(batch + 1)]), ints([n] * batch), table.int(), new, window=window)
+    done(g)
+    return float((O.double() - want).norm() / (want.half().double() - want).norm())
+
+
+# One more rounding as large as the output's would make it sqrt(2); with 6 % for the scatter 1.5.
+@pytest.mark.parametrize("D,hq,h,new", [(64, 4, 1, 2), (64, 16, 1, 1), (64, 28, 1, 1), (128, 8, 8, 1), (128, 16, 1, 1), (256, 8, 1, 1),
+                                        (256, 16, 2, 3), (256, 16, 2, 100)])
+@pytest.mark.parametrize("n,window", [(3, 0), (100, 11), (128, 0), (600, 0)])
+def test_attention_fp16_output_of_few_rows(g, D, hq, h, n, new, window):
+    assert _fp16_error(g, D, hq, h, n, min(new, n), window) <= 1.5
