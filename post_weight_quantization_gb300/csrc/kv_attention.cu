@@ -567,6 +567,15 @@ void with_shape(int D, int nt, F&& f) {
 // 23 / 37, 32 rows 47 / 37; one of 8192, 16 rows 23 / 31, 32 rows 45 / 31. D = 64, 32 of 1024: 32 rows 31 / 45, 48
 // rows 70 / 45; one of 8192: 32 rows 30 / 27.
 static bool many_rows(int D, long long rows) { return D != 256 && rows > (D == 64 ? 32 : 16); }
+// fp16 outputs over few keys stay with this kernel for any number of rows. The other one rounds k, v and the
+// probabilities to fp16, each as coarsely as the output itself is rounded, and over few keys nothing averages
+// that. Error against 64 bits, in units of the output's rounding, this one / the other: up to 128 keys (whole
+// caches or windows) 1.0 / 1.2 to 1.68, at 200 to 400 1.0 / 1.2 to 1.45, at 1000 1.0 / 1.1 to 1.27. In us, 4 sequences of 100 tokens, D = 128: 16 rows a
+// token 23 / 23, 7 rows 30 / 25, 8 heads of 8 54 / 25; of 40 tokens 12 / 23, 13 / 25, 29 / 25. (bf16 rounds to 2^-8: 1.02 in either.)
+constexpr int kFewKeys = 128;
+static bool few_keys_f16(int dtype, long long keys, int causal, long long window) {
+  return dtype == GPTQ_F16 && (keys <= kFewKeys || (causal && window > 0 && window <= kFewKeys));
+}
 
 size_t kv_attention_tc_workspace_bytes(int D);
 gptq_status kv_attention_tc_launch(const kva::Params& p, int D, void* ws, cudaStream_t s);
@@ -576,14 +585,13 @@ size_t kv_attention_workspace_bytes(long long total_q, int Hq, int H, int D, lon
   using namespace kva;
   (void)total_q;
   (void)batch;
-  if (many_rows(D, max_q * (Hq / H))) return kv_attention_tc_workspace_bytes(D);
-  size_t bytes = 0;
+  size_t bytes = 0;                              // of this kernel, and of the other where a call can take either
   with_shape(D, row_tiles(D, max_q * (Hq / H)), [&](auto d, auto n) {
     using C = Cfg<decltype(d)::value, decltype(n)::value>;
     const size_t ctas = (size_t)sm_count() * C::OCC;
     bytes = round256(16 * ctas) + ctas * 2 * C::PART * 4;
   });
-  return bytes;
+  return many_rows(D, max_q * (Hq / H)) ? std::max(bytes, kv_attention_tc_workspace_bytes(D)) : bytes;
 }
 
 gptq_status kv_attention_launch(const void* Q, int dtype, long long total_q, int Hq, int H, int D, long long ldq,
@@ -601,7 +609,8 @@ gptq_status kv_attention_launch(const void* Q, int dtype, long long total_q, int
   set_pages(p, page);
   p.window = window > 0x7FFFFFFFLL ? 0 : window;         // every key is nearer than that; sums with it stay in range
   p.scale_log2 = sm_scale * 1.4426950408889634f;
-  if (many_rows(D, max_q * p.G)) return kv_attention_tc_launch(p, D, ws, s);
+  if (many_rows(D, max_q * p.G) && !few_keys_f16(dtype, table_width * page, causal, window))
+    return kv_attention_tc_launch(p, D, ws, s);
   gptq_status st = GPTQ_OK;
   with_shape(D, row_tiles(D, max_q * p.G), [&](auto d, auto n) {
     constexpr int DD = decltype(d)::value, NT = decltype(n)::value;

@@ -9,7 +9,9 @@
 //   O += P V     P from tensor memory (fp16, over S's own columns), V in shared memory as it was
 //                dequantized (keys as rows: the MN-major B operand), O in tensor memory
 // Roundings to fp16 (11 bits): k and v as code * scale + low, once (half of 2^-11, random, where the
-// output type itself rounds to 2^-8 or 2^-11); the probabilities, 2^8 times too large, so that
+// output type itself rounds to 2^-8 or 2^-11; measured in units of that rounding, the error against 64 bits is
+// at most 1.04 for bf16 outputs; for fp16 ones 1.1 to 1.45 over values with a mean, which errors average
+// out against, and 2.0 to 2.4 over values without one; up to 128 keys the other kernel takes those, with 1.0); the probabilities, 2^8 times too large, so that
 // those down to 2^-22 of a row's largest keep all bits (a maximum that lags leaves them more). Queries are scaled by a power of two per
 // row as in the other kernel, so bf16 ones are exact. Scores, maxima and sums are fp32.
 // Keys past the end are zero, keys with a NaN among their numbers get a NaN k and a zero v, so a

@@ -1018,3 +1018,9 @@ def _fp16_error(g, D, hq, h, n, new, window):
 @pytest.mark.parametrize("n,window", [(3, 0), (100, 11), (128, 0), (600, 0)])
 def test_attention_fp16_output_of_few_rows(g, D, hq, h, n, new, window):
     assert _fp16_error(g, D, hq, h, n, min(new, n), window) <= 1.5
+
+
+@pytest.mark.parametrize("D,hq,h", [(64, 16, 1), (128, 16, 1), (64, 28, 4), (128, 8, 8)])
+@pytest.mark.parametrize("n,new,window", [(3, 3, 0), (8, 5, 4), (24, 20, 11), (128, 64, 0), (400, 100, 30), (600, 100, 128)])
+def test_attention_fp16_output_of_many_rows_over_few_keys(g, D, hq, h, n, new, window):
+    assert _fp16_error(g, D, hq, h, n, new, window) <= 1.5
