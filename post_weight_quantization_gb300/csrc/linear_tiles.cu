@@ -23,13 +23,14 @@
 // share the schedulers with the unpacking (about 11 instructions per 8 codes). Sixteen epilogue warps of 64 sums a
 // thread hide the loads from tensor memory; eight of 128 would take the registers of twice as many.
 //
-// Measured: 8192 x 8192, 4096 tokens 340 us in bf16 (1.62 PFLOP/s, 93 % of the library's sustained rate), 307 in e4m3 (1.79); 28672 x
-// 8192, 2500 tokens in e4m3 646 us (1.82 PFLOP/s). Bound: the issue slots that unpacking and epilogue share (e4m3 without
+// Measured: 8192 x 8192, 4096 tokens 349 us in bf16 (1.58 PFLOP/s, 91 % of the library's sustained rate), 317 in e4m3 (1.74); 28672 x
+// 8192, 2500 tokens in e4m3 661 us (1.78 PFLOP/s). Bound: the issue slots that unpacking and epilogue share (e4m3 without
 // the unpacking: 225 us), power beyond that.
 #include <algorithm>
 #include <type_traits>
 
 #include "packed.cuh"
+#include "ring.h"
 
 namespace gptq {
 namespace ltl {
@@ -56,11 +57,13 @@ struct Params {
   long long ldy, ldm, ldr;
   int m, d, T, gs, G, wpr, unit, act, y_bf16, codes_tma;
   uint32_t gs32_mul;           // ceil(2^32 / (gs / 32)), 0 when gs is 32
+  int d_pad;                   // d in whole blocks
   int mt, nt, group;           // row tiles, token tiles, token tiles that are walked together
 };
 
 // The unpacking warps form sets that take slabs in turn, so that one set's waits pass beside another's work: four, where
-// shared memory has room for as many slabs and their codes (8192 x 8192, 4096 tokens in bf16: 347 us, with two 375).
+// shared memory has room for as many slabs and their codes (8192 x 8192, 4096 tokens in bf16: 349 us, with two 375; at 4 bits
+// in e4m3, where it has room for three blocks of codes: 320, with two 317).
 template <int BITS, bool BYTES>
 struct Cfg {
   static constexpr int KC = BYTES ? 128 : 64;              // columns of a slab
@@ -71,9 +74,12 @@ struct Cfg {
   static constexpr int S_BYTES = S_STAGES * SCALES * BM * 4;                   // scales, and zeros as many
   static constexpr int SMEM = STAGES * (A_SLAB + X_SLAB) + CODE_STAGES * C_BYTES + 2 * S_BYTES + 1024 + 256;
   static_assert(SMEM <= 232448, "more than an SM has");
-  // A set skips the others' slabs: the use before of a slab's or a block's place must be one that it has seen, or a
-  // parity would tell it of another use. (Batches of zeros it waits for one by one.)
-  static_assert(SETS <= STAGES && SETS * KC <= CODE_STAGES * KB, "more sets than places");
+  // Barriers of the slabs that are free again and of the blocks that have landed, for sets that skip the others' (ring.h). A
+  // row's last block counts as whole, so that a set's step is the same from tile to tile.
+  static constexpr int BLOCK_STEP = SETS * KC > KB ? SETS * KC / KB : 1;
+  static constexpr int EMPTIES = barriers_for(STAGES, SETS), C_FULLS = barriers_for(CODE_STAGES, BLOCK_STEP);
+  static constexpr int BARRIERS = STAGES + EMPTIES + C_FULLS + CODE_STAGES + 2 * ND + 4 * S_STAGES + 1;
+  static_assert(8 * BARRIERS + 8 <= 256, "more barriers than have room");
 };
 
 __device__ __forceinline__ void umma(bool bytes, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate,
@@ -278,8 +284,8 @@ linear_tiles_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
   uint32_t* zeros = reinterpret_cast<uint32_t*>(scales + C::S_BYTES / 4);      // in the form that the unpacking takes
   uint64_t* full = reinterpret_cast<uint64_t*>(zeros + C::S_BYTES / 4);
   uint64_t* empty = full + STAGES;
-  uint64_t* c_full = empty + STAGES;
-  uint64_t* c_empty = c_full + CODE_STAGES;
+  uint64_t* c_full = empty + C::EMPTIES;
+  uint64_t* c_empty = c_full + C::C_FULLS;
   uint64_t* d_full = c_empty + CODE_STAGES;
   uint64_t* d_empty = d_full + ND;
   uint64_t* s_full = d_empty + ND;
@@ -292,14 +298,10 @@ linear_tiles_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int b = 0; b < STAGES; ++b) {
-      mbar_init(&full[b], SET + 1);
-      mbar_init(&empty[b], 1);
-    }
-    for (int b = 0; b < CODE_STAGES; ++b) {
-      mbar_init(&c_full[b], 1);
-      mbar_init(&c_empty[b], SET * (KB / KC));
-    }
+    for (int b = 0; b < STAGES; ++b) mbar_init(&full[b], SET + 1);
+    for (int b = 0; b < C::EMPTIES; ++b) mbar_init(&empty[b], 1);
+    for (int b = 0; b < C::C_FULLS; ++b) mbar_init(&c_full[b], 1);
+    for (int b = 0; b < CODE_STAGES; ++b) mbar_init(&c_empty[b], SET * (KB / KC));
     for (int b = 0; b < ND; ++b) {
       mbar_init(&d_full[b], 1);
       mbar_init(&d_empty[b], NEPI);
@@ -322,6 +324,11 @@ linear_tiles_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int ntiles = p.mt * p.nt, step = (int)gridDim.x;
+  // slab n's place is free: the MMAs on slab n - STAGES are done
+  auto slab_free = [&](uint32_t n) -> bool {
+    const uint32_t u = n - STAGES;
+    return n < STAGES || mbar_wait_bounded(&empty[u % C::EMPTIES], (u / C::EMPTIES) & 1u, abort_flag);
+  };
 
   if (warp < UNPACK0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_ISSUE));
@@ -332,10 +339,12 @@ linear_tiles_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
       for (int tile = (int)blockIdx.x; ok && tile < ntiles; tile += step) {
         int rt, tt;
         tile_of(p, tile, rt, tt);
-        for (int k = 0; k < p.d; k += KC, ++n) {
+        for (int k = 0; k < p.d_pad; k += KC, ++n) {
           const uint32_t i = n % STAGES;
-          if (!mbar_wait_bounded(&empty[i], ((n / STAGES) & 1u) ^ 1u, abort_flag)) { ok = false; break; }
-          if (lane == 0) {
+          if (!slab_free(n)) { ok = false; break; }
+          if (k >= p.d) {                                  // the empty half of the last block
+            if (lane == 0) mbar_arrive(&full[i]);
+          } else if (lane == 0) {
             mbar_arrive_expect_tx(&full[i], X_SLAB);
             tma_load_2d(xs + i * X_SLAB, &map_x, &full[i], k, tt * NTOK);
           }
@@ -363,11 +372,15 @@ linear_tiles_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
         if (p.unit >= KC) {
           const int per = p.unit / KC;                     // slabs of a unit
           int in = 0;                                      // slabs of the present one so far
-          for (int k0 = 0; k0 < p.d; k0 += KC, ++n) {
+          for (int k0 = 0; k0 < p.d_pad; k0 += KC, ++n) {
             const uint32_t i = n % STAGES, dt = tmem + (unit_no % ND) * NTOK;
             const uint64_t ad = a0 + (uint64_t)(i * (A_SLAB / 16)), bd = b0 + (uint64_t)(i * (X_SLAB / 16));
-            if (in == 0 && !accumulator()) { ok = false; break; }
+            if (in == 0 && k0 < p.d && !accumulator()) { ok = false; break; }
             if (!mbar_wait_poll(&full[i], (n / STAGES) & 1u, abort_flag)) { ok = false; break; }
+            if (k0 >= p.d) {
+              umma_commit_by(&empty[n % C::EMPTIES], leader);
+              continue;
+            }
             umma(BYTES, dt, ad, bd, IDESC, in != 0, leader);
             if (k0 + KC <= p.d) {
 #pragma unroll
@@ -375,7 +388,7 @@ linear_tiles_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
             } else {
               for (int kk = 1; k0 + kk * KSTEP < p.d; ++kk) umma(BYTES, dt, ad + 2 * kk, bd + 2 * kk, IDESC, 1, leader);
             }
-            umma_commit_by(&empty[i], leader);
+            umma_commit_by(&empty[n % C::EMPTIES], leader);
             if (++in == per || k0 + KC >= p.d) {
               umma_commit_by(&d_full[unit_no % ND], leader);
               ++unit_no;
@@ -383,7 +396,7 @@ linear_tiles_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
             }
           }
         } else {                                           // several units in a slab
-          for (int k0 = 0; ok && k0 < p.d; k0 += KC, ++n) {
+          for (int k0 = 0; ok && k0 < p.d_pad; k0 += KC, ++n) {
             const uint32_t i = n % STAGES;
             const uint64_t ad = a0 + (uint64_t)(i * (A_SLAB / 16)), bd = b0 + (uint64_t)(i * (X_SLAB / 16));
             if (!mbar_wait_poll(&full[i], (n / STAGES) & 1u, abort_flag)) { ok = false; break; }
@@ -396,7 +409,7 @@ linear_tiles_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
                 ++unit_no;
               }
             }
-            if (ok) umma_commit_by(&empty[i], leader);
+            if (ok) umma_commit_by(&empty[n % C::EMPTIES], leader);
           }
         }
       }
@@ -416,15 +429,15 @@ linear_tiles_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
           if (!p.codes_tma) {
             copy_codes<BITS>(p, smem_u32(codes) + i * C::C_BYTES, rt * BM, k / 32 * BITS, lane);
             __syncwarp();
-            if (lane == 0) mbar_arrive(&c_full[i]);
+            if (lane == 0) mbar_arrive(&c_full[n % C::C_FULLS]);
           } else if (lane == 0) {
-            mbar_arrive_expect_tx(&c_full[i], BM * C::ROW_BYTES);
-            tma_load_2d(codes + i * C::C_BYTES, &map_c, &c_full[i], k / KB * C::ROW_BYTES, rt * BM);
+            mbar_arrive_expect_tx(&c_full[n % C::C_FULLS], BM * C::ROW_BYTES);
+            tma_load_2d(codes + i * C::C_BYTES, &map_c, &c_full[n % C::C_FULLS], k / KB * C::ROW_BYTES, rt * BM);
           }
         }
       }
       if (!ok) { *abort_flag = 1; if (lane == 0) report_device_error(err, DEVERR_TIMEOUT); }
-      for (uint32_t u = n > CODE_STAGES ? n - CODE_STAGES : 0; u < n; ++u) mbar_wait_bounded(&c_full[u % CODE_STAGES], (u / CODE_STAGES) & 1u, nullptr);
+      for (uint32_t u = n > CODE_STAGES ? n - CODE_STAGES : 0; u < n; ++u) mbar_wait_bounded(&c_full[u % C::C_FULLS], (u / C::C_FULLS) & 1u, nullptr);
     } else if (warp == 3) {
       // ---------------- the scales and zeros of the next units, by row ----------------
       uint32_t n = 0;
@@ -511,16 +524,17 @@ linear_tiles_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
     for (int tile = (int)blockIdx.x; ok && tile < ntiles; tile += step) {
       const uint32_t n0 = n;
       // this set's slabs: first, first + SETS, ...
-      for (int k = (int)((uint32_t)(set - n0) % SETS) * KC; k < p.d; k += SETS * KC) {
+      for (int k = (int)((uint32_t)(set - n0) % SETS) * KC; k < p.d_pad; k += SETS * KC) {
         const uint32_t at = n0 + (uint32_t)(k / KC), i = at % STAGES, cb = cn + (uint32_t)(k / KB), st = cb % CODE_STAGES;
         const uint32_t zb = zn + (uint32_t)(k >> (ush + 2)), zi = zb % S_STAGES;
         release_to(zb);
         if (!ok || !mbar_wait_bounded(&z_full[zi], (zb / S_STAGES) & 1u, abort_flag)) { fail(); break; }
-        if (!mbar_wait_bounded(&c_full[st], (cb / CODE_STAGES) & 1u, abort_flag)) { fail(); break; }
-        if (!mbar_wait_bounded(&empty[i], ((at / STAGES) & 1u) ^ 1u, abort_flag)) { fail(); break; }
+        if (!mbar_wait_bounded(&c_full[cb % C::C_FULLS], (cb / C::C_FULLS) & 1u, abort_flag)) { fail(); break; }
+        if (!slab_free(at)) { fail(); break; }
         const uint32_t sc = smem_u32(codes) + st * C::C_BYTES;
 #pragma unroll
         for (int j = 0; j < ROWS; ++j) {
+          if (k >= p.d) break;                             // the empty half of the last block
           const int r = 32 * (ROWS * sub + j) + lane;
           const uint32_t* zr = zeros + (zi * SCALES) * BM + r;
           const uint32_t to = smem_u32(smem) + i * A_SLAB + r * 128, sw = (uint32_t)(r & 7);
@@ -554,19 +568,10 @@ linear_tiles_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
           mbar_arrive(&c_empty[st]);
         }
       }
-      n = n0 + (uint32_t)((p.d + KC - 1) / KC);
-      cn += (uint32_t)((p.d + KB - 1) / KB);
+      n = n0 + (uint32_t)(p.d_pad / KC);
+      cn += (uint32_t)(p.d_pad / KB);
       zn += (uint32_t)((p.d + (SCALES << ush) - 1) >> (ush + 2));
       release_to(zn);
-      if (!BYTES && (p.d + KB - 1) / KB * 2 > (p.d + KC - 1) / KC && ok) {
-        // the last block ends in its first slab: the set that would have taken the second one releases the codes
-        if ((int)(n % SETS) == set) {
-          const uint32_t cb = cn - 1, st = cb % CODE_STAGES;
-          if (!mbar_wait_bounded(&c_full[st], (cb / CODE_STAGES) & 1u, abort_flag)) fail();
-          __syncwarp();
-          if (lane == 0 && ok) mbar_arrive(&c_empty[st]);
-        }
-      }
     }
   } else {
     // ---------------- epilogue ----------------
@@ -673,6 +678,7 @@ gptq_status linear_tiles_launch(const uint32_t* qweight, const float* scales, co
   p.gs = group_size < 0 ? (int)d : group_size;
   p.G = (int)(d / p.gs);
   p.wpr = (int)(d / 32 * bits);
+  p.d_pad = (int)((d + KB - 1) / KB * KB);
   p.unit = p.gs % 128 == 0 ? 128 : (p.gs % 64 == 0 ? 64 : 32);
   p.act = act; p.y_bf16 = y_dtype == GPTQ_BF16;
   const unsigned gs32 = (unsigned)p.gs / 32;
