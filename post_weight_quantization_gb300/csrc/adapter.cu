@@ -37,7 +37,7 @@
 // which the epilogue adds to that run's columns only.
 //
 // Bound: HBM bandwidth for few tokens (the codes), the tensor cores for many. Measured at 4 bits, rank
-// 16: 4096 x 4096, 1 token 12.3 us, 3001 tokens 129 us (785 TFLOP/s, 40 % of the library GEMM's rate: an
+// 16: 4096 x 4096, 1 token 12.3 us, 3001 tokens 123 us (817 TFLOP/s, 42 % of the library GEMM's rate: an
 // accumulator leaves tensor memory per 128 columns); 8192 x 8192, 48 tokens 31 us (2.1 TB/s; instruction
 // issue 61 % busy, about a fifth of it unpacking).
 #include <math_constants.h>
@@ -47,6 +47,7 @@
 
 #include "elem.cuh"
 #include "packed.cuh"
+#include "ring.h"
 
 namespace gptq {
 
@@ -322,6 +323,10 @@ struct Cfg {
   static constexpr int SETS = MANY ? 2 : 4, EPI0 = UNPACK0 + 4 * SETS, THREADS = (EPI0 + NEPI) * 32;
   static constexpr int REG_ISSUE = 32, REG_UNPACK = 56, REG_EPI = 168;
   static constexpr int SLOTS = !MANY ? 4 : (BITS == 8 ? 2 : 3);     // blocks in the ring: an A buffer, X, packed codes
+  // barriers of the slots that are free again and of the codes that have landed: a set of unpacking warps waits on its own
+  // (ring.h). The blocks of a tile's adapters are filled up to a multiple of the sets, so that a set's step stays the same for both.
+  static constexpr int BARRIERS = barriers_for(SLOTS, SETS);
+  static_assert(8 * (2 * SLOTS + 2 * BARRIERS + 2 * ND + 1) + 8 <= 256, "more barriers than have room");
   static constexpr int ROW_BYTES = 16 * BITS;              // packed codes of a row in one block
   static constexpr int C_BYTES = (BM * ROW_BYTES + 1023) / 1024 * 1024;
   static constexpr int X_BOX = N * XK * 2, X_BYTES = 2 * X_BOX;
@@ -414,11 +419,11 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   uint8_t* codes = smem + SLOTS * C::X_BYTES;
   // full[i]: slot i's A block is in tensor memory (four warps arrive) and its X in shared memory
-  // (the producer arrives, TMA completes); empty[i]: its MMAs are done. c_*: the packed codes.
+  // (the producer arrives, TMA completes); empty[n % BARRIERS]: block n's MMAs are done. c_*: the packed codes.
   uint64_t* full = reinterpret_cast<uint64_t*>(codes + SLOTS * C::C_BYTES);
   uint64_t* empty = full + SLOTS;
-  uint64_t* c_full = empty + SLOTS;
-  uint64_t* c_empty = c_full + SLOTS;
+  uint64_t* c_full = empty + C::BARRIERS;
+  uint64_t* c_empty = c_full + C::BARRIERS;
   uint64_t* d_full = c_empty + SLOTS;
   uint64_t* d_empty = d_full + ND;
   uint64_t* drain = d_empty + ND;
@@ -431,9 +436,11 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
   if (threadIdx.x == 0) {
     for (int b = 0; b < SLOTS; ++b) {
       mbar_init(&full[b], 5);
+      mbar_init(&c_empty[b], 4);
+    }
+    for (int b = 0; b < C::BARRIERS; ++b) {
       mbar_init(&empty[b], 1);
       mbar_init(&c_full[b], 1);
-      mbar_init(&c_empty[b], 4);
     }
     for (int b = 0; b < ND; ++b) {
       mbar_init(&d_full[b], 1);
@@ -463,6 +470,11 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
   const int k_lo = blk0 * KB, k_hi = min(p.d, blk1 * KB);
   const int ad_units = (2 * p.rank + KB - 1) / KB;         // A blocks of one adapter
   constexpr uint32_t IDESC = umma_idesc(/*bf16*/ 1, false, false, BM, NP);
+  // block n's slot is free: the MMAs on block n - SLOTS are done
+  auto slot_free = [&](uint32_t n) -> bool {
+    const uint32_t u = n - SLOTS;
+    return n < SLOTS || mbar_wait_bounded(&empty[u % C::BARRIERS], (u / C::BARRIERS) & 1u, abort_flag);
+  };
 
   if (warp < UNPACK0) {
     if (MANY) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REG_ISSUE));
@@ -473,11 +485,13 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
     if constexpr (EPI) {
       if (p.wait_x) grid_dep_wait();
     }
-    // a block of `cols` columns from k on: one box, or two
+    // a block of `cols` columns from k on: one box, or two, or none
     auto push = [&](const CUtensorMap* map, int k, int cols, int t) {
       const uint32_t i = ab % SLOTS;
-      if (!mbar_wait_bounded(&empty[i], ((ab / SLOTS) & 1u) ^ 1u, abort_flag)) { ok = false; return; }
-      if (lane == 0) {
+      if (!slot_free(ab)) { ok = false; return; }
+      if (cols <= 0) {
+        if (lane == 0) mbar_arrive(&full[i]);
+      } else if (lane == 0) {
         mbar_arrive_expect_tx(&full[i], cols > XK ? C::X_BYTES : C::X_BOX);
         tma_load_2d(smem + i * C::X_BYTES, map, &full[i], k, t);
         if (cols > XK) tma_load_2d(smem + i * C::X_BYTES + C::X_BOX, map, &full[i], k + XK, t);
@@ -492,8 +506,10 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
         Runs runs;
         runs.init(p, t0, lane);
         int c0, c1, id;
+        const uint32_t ab0 = ab;
         while (ok && runs.next(c0, c1, id))
           for (int k = 0; ok && k < 2 * p.rank; k += KB) push(&map_u, k, 2 * p.rank - k, t0);
+        while (ok && (ab - ab0) % SETS) push(&map_u, 0, 0, t0);
       }
     }
     if (!ok) { *abort_flag = 1; if (lane == 0) report_device_error(err, DEVERR_TIMEOUT); }
@@ -543,7 +559,7 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
           }
         }
         if (!ok) break;
-        umma_commit_by(&empty[i], leader);
+        umma_commit_by(&empty[ab % C::BARRIERS], leader);
       }
     };
     for (int tile = tile0; ok && tile < ntiles; tile += step) {
@@ -552,7 +568,12 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
         Runs runs;
         runs.init(p, (tile / p.mt) * N, lane);
         int c0, c1, id;
+        const uint32_t ab0 = ab;
         while (ok && runs.next(c0, c1, id)) stream(2 * p.rank, KB);
+        for (; ok && (ab - ab0) % SETS; ++ab) {
+          if (!mbar_wait_poll(&full[ab % SLOTS], (ab / SLOTS) & 1u, abort_flag)) { ok = false; break; }
+          umma_commit_by(&empty[ab % C::BARRIERS], leader);
+        }
       }
     }
     if (!ok) { *abort_flag = 1; if (lane == 0) report_device_error(err, DEVERR_TIMEOUT); }
@@ -568,13 +589,13 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
         const uint32_t i = cn % SLOTS;
         if (!mbar_wait_bounded(&c_empty[i], ((cn / SLOTS) & 1u) ^ 1u, abort_flag)) { ok = false; break; }
         if (lane == 0) {
-          mbar_arrive_expect_tx(&c_full[i], BM * C::ROW_BYTES);
-          tma_load_2d(codes + i * C::C_BYTES, &map_c, &c_full[i], b * C::ROW_BYTES, r0);
+          mbar_arrive_expect_tx(&c_full[cn % C::BARRIERS], BM * C::ROW_BYTES);
+          tma_load_2d(codes + i * C::C_BYTES, &map_c, &c_full[cn % C::BARRIERS], b * C::ROW_BYTES, r0);
         }
       }
     }
     if (!ok) { *abort_flag = 1; if (lane == 0) report_device_error(err, DEVERR_TIMEOUT); }
-    for (uint32_t u = cn > SLOTS ? cn - SLOTS : 0; u < cn; ++u) mbar_wait_bounded(&c_full[u % SLOTS], (u / SLOTS) & 1u, nullptr);
+    for (uint32_t u = cn > SLOTS ? cn - SLOTS : 0; u < cn; ++u) mbar_wait_bounded(&c_full[u % C::BARRIERS], (u / C::BARRIERS) & 1u, nullptr);
     } else if (warp == 3 && !MANY && p.ids) {
     // ---------------- U, while the others work ----------------
     grid_dep_wait();
@@ -598,7 +619,7 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
     uint32_t ta = 0;
     auto ready = [&]() -> bool {                           // the block's buffer is free
       ta = ta0 + (ab % SLOTS) * (KB / 2);
-      if (!mbar_wait_bounded(&empty[ab % SLOTS], ((ab / SLOTS) & 1u) ^ 1u, abort_flag)) {
+      if (!slot_free(ab)) {
         *abort_flag = 1;
         if (lane == 0) report_device_error(err, DEVERR_TIMEOUT);
         return false;
@@ -627,7 +648,7 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
         uint32_t w[WB];
         if (p.codes_tma) {
           const uint32_t cn = cb0 + (uint32_t)(b - blk0), st = cn % SLOTS;
-          if (!mbar_wait_bounded(&c_full[st], (cn / SLOTS) & 1u, abort_flag)) {
+          if (!mbar_wait_bounded(&c_full[cn % C::BARRIERS], (cn / C::BARRIERS) & 1u, abort_flag)) {
             *abort_flag = 1;
             if (lane == 0) report_device_error(err, DEVERR_TIMEOUT);
             ok = false;
@@ -667,6 +688,7 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
         Runs runs;
         runs.init(p, (tile / p.mt) * N, lane);
         int c0, c1, id;
+        const uint32_t first_ad = ab;
         while (ok && runs.next(c0, c1, id)) {
           const uint32_t* br = reinterpret_cast<const uint32_t*>(p.B + ((long long)id * p.m + (live ? row : 0)) * p.rank);
           for (int u = 0; u < ad_units; ++u, ++ab) {
@@ -688,6 +710,11 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
             }
             publish();
           }
+        }
+        for (; ok && (ab - first_ad) % SETS; ++ab) {
+          if ((int)(ab % SETS) != set) continue;
+          if (!ready()) { ok = false; break; }
+          if (lane == 0) mbar_arrive(&full[ab % SLOTS]);
         }
       }
     }

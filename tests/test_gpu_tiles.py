@@ -130,3 +130,41 @@ def test_long_rows_repeat_themselves(g, eight):
         call(b)
         assert torch.equal(call(a), want)
     g.gptq_device_check()
+
+
+# 20 x 20 tiles of 256 tokens with adapters: runs of one adapter's tokens in every number, so that a tile has an odd or an even
+# number of blocks more; ranks of one block and of two, rows of an odd number of blocks. U = alpha A x has d products of fp32 sums,
+# then enters as two bf16 parts (2^-16), with `rank` products more.
+@pytest.mark.parametrize("call", ["adapter_linear", "linear"])
+@pytest.mark.parametrize("d,bits,group,rank", [(640, 4, 128, 16), (512, 4, 64, 72), (384, 8, 128, 8), (416, 8, 32, 128), (640, 3, 128, 16), (320, 2, 64, 64)])
+def test_three_tiles_of_a_cta_with_adapters(g, d, bits, group, rank, call):
+    rng = np.random.default_rng(d + bits + rank)
+    T, m, n = 5003, 2500, 7
+    q, W = layer(g, rng, m, d, bits, group)
+    x, _, X = tokens(rng, T, d, False)
+    A = (torch.from_numpy(rng.standard_normal((n, rank, d))).cuda() * d ** -0.5).bfloat16()
+    B = (torch.from_numpy(rng.standard_normal((n, m, rank))).cuda() * rank ** -0.5).bfloat16()
+    alpha = torch.from_numpy((0.5 + rng.random(n)).astype(np.float32)).cuda()
+    runs = rng.choice([1, 17, 90, 200, 256, 700], 400)
+    ids = torch.from_numpy(np.repeat(rng.integers(-1, n, 400), runs)[:T].astype(np.int32)).cuda()
+    z, mag = X @ W.T, X.abs() @ W.abs().T
+    unit = 128 if group % 128 == 0 else 64 if group % 64 == 0 else 32
+    err = (unit + -(-d // unit) + 2) * 2.0 ** -23 * mag
+    for a in range(n):
+        at = (ids == a).nonzero()[:, 0]
+        z[at] += alpha[a].double() * ((X[at] @ A[a].double().T) @ B[a].double().T)
+        err[at] += ((d + rank) * 2.0 ** -23 + 2.0 ** -16) * alpha[a].double() * ((X[at].abs() @ A[a].double().abs().T) @ B[a].double().abs().T)
+    y = z
+    if call == "linear":
+        res = torch.randn((T, m), device="cuda")
+        Y = g.gptq_linear(q, x, m, A=A, B=B, ids=ids, alpha=alpha, act="silu", residual=res)
+        y = z * torch.sigmoid(z)
+        err = 1.1 * err + (16 + 4 * z.abs()) * 2.0 ** -23 * y.abs()
+        y = y + res.double()
+        err += 2.0 ** -23 * y.abs()
+    else:
+        Y = g.gptq_adapter_linear(q, x, m, A, B, ids, alpha)
+    torch.cuda.synchronize()
+    g.gptq_device_check()
+    off = (Y.double() - y).abs() / (err + 2.0 ** -24 * y.abs() + 1e-37)
+    assert bool((off <= 1).all()), (float(off.max()), (off > 1).nonzero()[:5].tolist(), int((off > 1).sum()))
