@@ -132,7 +132,7 @@ __device__ __forceinline__ unsigned long long weight(const uint32_t* roots, floa
   return ((unsigned long long)m << (FRAC - 31)) >> (-(j >> 11));
 }
 
-// Every CTA's 32 words of `part` to every CTA. Two buffers: one is written again only after all have read it and
+// Every CTA's 32 words of `part` to every CTA (all of which are known to run). Two buffers: one is written again only after all have read it and
 // met once more.
 struct Exchange {
   Common& s;
@@ -186,6 +186,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (E8 > 3 ? 2 : 4) : (E8 > 2 ? 1
   asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n_cta));
   const int rank = (int)cluster_ctarank();
   const long long row = blockIdx.x / n_cta;
+  cluster_arrive();                                        // waited for before anything is written to another CTA
   Exchange exchange{sm, rank, n_cta, warp, lane};
   // the row's settings, checked by every thread alike
   const float u = p.u[row], T = p.temperature ? p.temperature[row] : 1.0f;
@@ -193,6 +194,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (E8 > 3 ? 2 : 4) : (E8 > 2 ? 1
   const float top_p = CUT && p.top_p ? p.top_p[row] : 1.0f, min_p = CUT && p.min_p ? p.min_p[row] : 0.0f;
   const bool first = rank == 0 && threadIdx.x == 0;
   if (!(u >= 0.0f && u < 1.0f) || !(T == 0.0f || (T >= T_MIN && T <= T_MAX)) || top_p != top_p || min_p != min_p) {
+    cluster_wait();
     if (first) {
       p.tokens[row] = -1;
       if (p.logprob) p.logprob[row] = CUDART_NAN_F;
@@ -233,6 +235,8 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (E8 > 3 ? 2 : 4) : (E8 > 2 ? 1
   if (threadIdx.x < 32) sm.part[threadIdx.x] = 0;
   __syncthreads();
   if (lane == 0) sm.part[warp] = top;
+  __syncwarp();
+  cluster_wait();                                          // every CTA of the cluster runs
   {
     const uint32_t (*all)[32] = exchange();
     uint32_t m = 0;
