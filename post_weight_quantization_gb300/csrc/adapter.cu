@@ -146,12 +146,14 @@ __global__ void __launch_bounds__(SH_WARPS * 32) adapter_shrink_few_kernel(Shrin
     for (int r = threadIdx.x; r < nr; r += SH_WARPS * 32) sums[r] = 0.0f;
   }
   __syncthreads();
+  __syncwarp();
   cluster_sync();
   if (blockIdx.x == 0 && threadIdx.x < nr) {
     float s = 0.0f;
     for (int k = 0; k < p.splits; ++k) s += ld_cluster(smem_u32(&sums[threadIdx.x]), (uint32_t)k);
     p.part[(long long)t * p.rank + r0 + threadIdx.x] = s;
   }
+  __syncwarp();
   cluster_sync();
 }
 
@@ -254,6 +256,7 @@ __global__ void __launch_bounds__(SH_WARPS * 32) adapter_shrink_kernel(ShrinkPar
       for (int w = 0; w < SH_WARPS; ++w) s += red[w][i][r];
       sums[x] = s;
     }
+    __syncwarp();
     if (parts > 1) cluster_sync();
     for (int x = SH_WARPS * 32 * part + threadIdx.x; x < SH_TOK * nr; x += SH_WARPS * 32 * parts) {
       const int i = x / nr, r = x - i * nr;
@@ -270,6 +273,7 @@ __global__ void __launch_bounds__(SH_WARPS * 32) adapter_shrink_kernel(ShrinkPar
         p.hl[(long long)(t0 + i) * (2 * p.rank) + p.rank + r0 + r] = __float2bfloat16_rn(h == s ? 0.0f : s - h);
       }
     }
+    __syncwarp();
     if (parts > 1) cluster_sync();                         // also: nobody leaves while its sums are read
     else __syncthreads();
   }

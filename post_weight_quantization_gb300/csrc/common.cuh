@@ -194,7 +194,8 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
   return r;
 }
 
-// Every thread of every CTA in the cluster arrives, then waits for all of them.
+// Every thread of every CTA in the cluster arrives, then waits for all of them. The warp is converged: behind a branch or a loop
+// that its lanes leave apart, __syncwarp() comes first.
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }

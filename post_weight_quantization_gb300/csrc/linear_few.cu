@@ -178,8 +178,12 @@ __global__ void __launch_bounds__(WARPS * 32, 2) linear_few_kernel(Params p) {
     for (int k = 0; k < WARPS; ++k) v += red[k][at];
     part[at] = v;
   }
-  if (p.S > 1) cluster_sync();
-  else __syncthreads();
+  if (p.S > 1) {
+    __syncwarp();                                          // the loop's passes differ within a warp
+    cluster_sync();
+  } else {
+    __syncthreads();
+  }
   for (int o = rank * WARPS * 32 + (int)threadIdx.x; o < total; o += p.S * WARPS * 32) {
     const int r = o % ROWS, tok = o / ROWS, row = r0 + r;
     if (row >= p.m) continue;
