@@ -634,8 +634,8 @@ gptq_status gptq_linear(const uint32_t* qweight, const float* scales, const floa
  *         counts as the larger. The largest logit is always kept.
  *   token: the first kept i, by index, with (the kept w up to and with i) > u * (all kept w)
  *
- * Weights are accurate to 2^-32 and summed as integers, so the draw from given kept ones does not depend on how a row is
- * split. The masses that top_p compares are fp32 sums: a border of top_p within 2^-17 of the mass may fall either way.
+ * Weights are accurate to 2^-31 of themselves and 2^-44 of the largest, and summed as integers, those that top_p compares
+ * too: a row's token does not depend on the rows beside it or on how it is split.
  *
  *   logits     device, rows x vocab of dtype (GPTQ_F32, _BF16 or _F16), row stride ld >= vocab elements, aligned
  *              as their type. -infinity: never drawn. Several +infinity share the row's weight.

@@ -17,14 +17,17 @@
 // 2^-44, which no order of summation changes. FP64 would do it too, at 2 lanes an SM.
 //
 // Where few are kept (top_k up to 512, or little mass) they are listed, sorted and drawn from by one CTA. Otherwise
-// top_k and top_p look for the logit where a count, or a mass, is reached: the bits of an order-preserving
-// integer of the logit are fixed five at a time, from the top. Each thread adds its values to a column of 32
-// bins of its own in shared memory (no atomics, no conflicts); the columns' sums meet in the
-// cluster through shared memory, and every warp finds the bin in which the sum is reached.
+// top_k and top_p look for the logit where a count, or a mass, is reached. For a count the bits of an order-preserving integer of
+// the logit are fixed five at a time, from the top: each thread adds its values to a column of 32 bins of its own in shared memory
+// (no atomics, no conflicts); the columns' sums meet in the cluster through shared memory, and every warp finds the bin
+// in which the sum is reached. Masses are the draw's integers, so that a border of top_p is the same however a row is split. A weight
+// costs as much as seven comparisons, so fewer rounds weigh many values: the first bits are those of the distance to the
+// largest logit, which part a row more evenly than the integer's, whose bits only part the values that share those. (256 rows of
+// 151665 with top_p alone 894 us, with the integer's bits throughout 1078.)
 //
 // Bound: latency (a load, two or three exchanges of a cluster, a sort), and for large batches the phases of a CTA one after
-// another. Measured: one row of 32000 16 us, 48 rows of 128256 with top_k, top_p and min_p 33 us, 256 rows of 151665 drawn
-// whole 175 us (0.9 TB/s).
+// another. Measured: one row of 32000 12 us, 48 rows of 128256 with top_k, top_p and min_p 35 us, 256 rows of 151665 drawn
+// whole 176 us (0.9 TB/s).
 #pragma once
 
 #include <math_constants.h>
@@ -41,6 +44,7 @@ namespace smp {
 constexpr int MOST = 8, WHOLE = 3, CUTS = 8;             // CTAs of a cluster at most; vectors a thread before a row gets more CTAs
 constexpr int ROOTS = 2048, FRAC = 44;
 constexpr int LIST = 2048, GUESS = 256;                  // candidates at most; how many where top_k does not say
+constexpr int WIDE = 96, MASSES = 16;                    // words of a wide exchange, the first one of 32 masses in it
 constexpr float T_MIN = 1e-30f, T_MAX = 1e30f;
 
 // 2^(i / 2048) in units of 2^-31, from square roots by Newton's iteration.
@@ -90,13 +94,14 @@ struct Few {
 };
 struct Common {
   uint32_t roots[ROOTS];
-  uint32_t part[32];
-  uint32_t all[2][MOST][32];   // the cluster's parts, two exchanges in turn
+  uint32_t part[WIDE];         // 32 words, or 16 and 32 masses
+  uint32_t all[2][MOST][WIDE]; // the cluster's parts, two exchanges in turn
 };
 template <int NT, bool CUT>
 struct Smem : Common {
   union {
-    float bins[32][NT];
+    float bins[32][NT];        // a thread's column of counts
+    uint32_t halves[2][32][NT / 2];    // two threads' column of masses, in two words
     Few<NT> few;
   };
 };
@@ -108,12 +113,6 @@ __device__ __forceinline__ uint32_t key_of(float x) {      // grows with x; a Na
   return x != x ? 0xFFFFFFFFu : b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float of_key(uint32_t k) { return __uint_as_float(k ^ (k >> 31 ? 0x80000000u : 0xFFFFFFFFu)); }
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // w of logit x in units of 2^-44: 2^(n + j / 2048) * 2^f with a root from the table and a polynomial.
 __device__ __forceinline__ unsigned long long weight(const uint32_t* roots, float x, float big, float ch, float cl) {
@@ -132,19 +131,21 @@ __device__ __forceinline__ unsigned long long weight(const uint32_t* roots, floa
   return ((unsigned long long)m << (FRAC - 31)) >> (-(j >> 11));
 }
 
-// Every CTA's 32 words of `part` to every CTA (all of which are known to run). Two buffers: one is written again only after all have read it and
+// Every CTA's 32 words (wide: all) of `part` to every CTA (all of which are known to run). Two buffers: one is written again only after all have read it and
 // met once more.
 struct Exchange {
   Common& s;
   int rank, n, warp, lane;
   uint32_t turn = 0;
-  __device__ __forceinline__ const uint32_t (*operator()())[32] {
+  __device__ __forceinline__ const uint32_t (*operator()(bool wide = false))[WIDE] {
     __syncthreads();                                       // part is written
     const uint32_t b = turn++ & 1u;
     if (warp < n) {
       uint32_t to;
       asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_u32(&s.all[b][rank][lane])), "r"(warp));
       asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to), "r"(s.part[lane]) : "memory");
+      for (int i = 32; wide && i < WIDE; i += 32)
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to + 4 * i), "r"(s.part[i + lane]) : "memory");
     }
     __syncwarp();
     cluster_sync();
@@ -165,8 +166,21 @@ __device__ __forceinline__ float log_share(float x, float big, float T, unsigned
 }
 
 struct Found {
-  uint32_t key;                // the key (its leading bits) in which the sum is reached
-  float above, at;             // the sum over larger keys, and over this one
+  uint32_t key;                // the key (its leading bits) in which the count is reached
+  float above, at;             // the count of larger keys, and of this one
+};
+
+// Masses are whole units. A share of one, rounded down, and whether that left a rest: what lies before a place is less than the
+// share where it is less than `units`, or as much and there is a rest.
+struct Share {
+  unsigned long long units;
+  bool rest;
+  __device__ __forceinline__ Share(unsigned long long mass, float share) {
+    const unsigned long long p64 = share > 0.0f ? __float2ull_rz(share * 18446744073709551616.0f) : 0ull;
+    units = __umul64hi(mass, p64);
+    rest = mass * p64 != 0;
+  }
+  __device__ __forceinline__ bool above(unsigned long long sum) const { return sum < units || (sum == units && rest); }
 };
 
 template <typename EI> constexpr int key_shift() {         // bits of the key that a logit of this type leaves alone
@@ -238,7 +252,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (E8 > 3 ? 2 : 4) : (E8 > 2 ? 1
   __syncwarp();
   cluster_wait();                                          // every CTA of the cluster runs
   {
-    const uint32_t (*all)[32] = exchange();
+    const uint32_t (*all)[WIDE] = exchange();
     uint32_t m = 0;
     for (int r = 0; r < n_cta; ++r) m = max(m, all[r][lane]);
     top = __reduce_max_sync(0xffffffffu, m);
@@ -264,7 +278,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (E8 > 3 ? 2 : 4) : (E8 > 2 ? 1
     if (threadIdx.x < 32) sm.part[threadIdx.x] = 0xFFFFFFFFu;
     __syncthreads();
     if (lane == 0) sm.part[warp] = at;
-    const uint32_t (*all)[32] = exchange();
+    const uint32_t (*all)[WIDE] = exchange();
     if (rank == 0 && warp == 0) {
       for (int r = 0; r < n_cta; ++r) at = min(at, all[r][lane]);
       at = __reduce_min_sync(0xffffffffu, at);
@@ -281,9 +295,64 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (E8 > 3 ? 2 : 4) : (E8 > 2 ? 1
   const bool by_k = top_k > 0 && top_k < p.V, by_p = top_p < 1.0f;
   const unsigned long long floor_w = min_p > 0.0f ? (unsigned long long)(fminf(min_p, 1.0f) * 17592186044416.0f) : 0ull;
 
+  // The next vector of the thread's comes first: code for one of them that goes around them all.
+  auto around = [&]() {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float first_x = x[0][k];
+#pragma unroll
+      for (int i = 0; i + 1 < E8; ++i) x[i][k] = x[i + 1][k];
+      x[E8 - 1][k] = first_x;
+    }
+  };
   uint32_t least = 0;                                      // kept: keys above it, and the first `ties` of those equal to it
   uint32_t ties = 0xFFFFFFFFu;
   if constexpr (CUT) {
+  unsigned long long mass = 0, hist = 0;                   // of the row, and of this lane's part of it
+  // A value's place: how far it lies below the largest, 2^32 steps of it down to where weights end; counted from the far end, so
+  // that larger logits have larger places. Equal logits have the same one, and a few neighbours may.
+  const float per = ch * (32.0f / 45.0f * 134217728.0f);
+  auto place_of = [&](float v) -> uint32_t { return v == big ? 0xFFFFFFFFu : ~__float2uint_rz((big - v) * per); };
+  // The CTA's mass of the values in each of 32 bins, into `part`. A weight is two words of 22 bits, so that the sums of two
+  // threads' values are plain words, in any order.
+  auto tally = [&](auto bin_of) {
+    const int half = (int)threadIdx.x / (NT / 2), col = (int)threadIdx.x % (NT / 2);
+    __syncthreads();
+#pragma unroll
+    for (int b = 0; b < 32; ++b) sm.halves[half][b][col] = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (int i = 0; i < E8; ++i, around())
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t bin = bin_of(x[0][k]);
+        if (bin < 32u) {
+          const unsigned long long w = weight(sm.roots, x[0][k], big, ch, cl);
+          atomicAdd(&sm.halves[0][bin][col], (uint32_t)w & 0x3FFFFFu);
+          atomicAdd(&sm.halves[1][bin][col], (uint32_t)(w >> 22));
+        }
+      }
+    __syncthreads();
+#pragma unroll
+    for (int b = warp; b < 32; b += WARPS) {
+      unsigned long long s = 0;
+#pragma unroll
+      for (int c = 0; c < NT / 2; c += 32) s += sm.halves[0][b][c + lane] + ((unsigned long long)sm.halves[1][b][c + lane] << 22);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (lane == 0) *reinterpret_cast<unsigned long long*>(&sm.part[MASSES + 2 * b]) = s;
+    }
+  };
+  auto collect = [&](const uint32_t (*all)[WIDE]) -> unsigned long long {      // a bin a lane
+    unsigned long long s = 0;
+    for (int r = 0; r < n_cta; ++r) s += *reinterpret_cast<const unsigned long long*>(&all[r][MASSES + 2 * lane]);
+    return s;
+  };
+  auto over_lanes = [](unsigned long long s) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+  };
   // ---- few kept: the `most` largest logits are sought, sorted and drawn from. Where the threads' own largest
   // are sorted, at least `most` values are not below the one at place `most`, and the CTA's `most` largest are
   // among them: a CTA lists all such values, and the first `most` of the sorted list of all CTAs are the row's.
@@ -313,38 +382,32 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (E8 > 3 ? 2 : 4) : (E8 > 2 ? 1
     __syncthreads();
     const uint32_t least = max(few.keys[most - 1], key_of(-CUDART_INF_F) + 1u);
     uint32_t count = 0;
-    float mass = 0.0f;
 #pragma unroll
     for (int i = 0; i < E8; ++i)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        count += key_of(x[i][k]) >= least;
-        if (by_p && !by_k) mass += x[i][k] == big ? 1.0f : ex2((x[i][k] - big) * ch);
-      }
+      for (int k = 0; k < 8; ++k) count += key_of(x[i][k]) >= least;
     uint32_t upto = count;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += y;
-      mass += __shfl_xor_sync(0xffffffffu, mass, o);
     }
-    if (lane == 31) {
-      sm.part[warp] = upto;
-      sm.part[WARPS + warp] = __float_as_uint(mass);
-    }
-    const uint32_t (*all)[32] = exchange();
+    if (lane == 31) sm.part[warp] = upto;
+    const bool by_mass = by_p && !by_k;
+    if (by_mass) tally([&](float v) { return place_of(v) >> 27; });
+    const uint32_t (*all)[WIDE] = exchange(by_mass);
     uint32_t n = 0, at = 0;                                // candidates, and those before this warp's
-    mass = 0.0f;
     for (int r = 0; r < n_cta; ++r) {
       const uint32_t c = lane < WARPS ? all[r][lane] : 0u;
       n += c;
       if (r < rank || (r == rank && lane < warp)) at += c;
-      if (lane >= WARPS) mass += __uint_as_float(all[r][lane]);
     }
     n = __reduce_add_sync(0xffffffffu, n);
     at = __reduce_add_sync(0xffffffffu, at) + upto - count;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
+    if (by_mass) {
+      hist = collect(all);
+      mass = over_lanes(hist);
+    }
     if (n <= LIST) {
       uint32_t list;                                       // the first CTA's
       asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(list) : "r"(smem_u32(few.list)));
@@ -407,15 +470,10 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (E8 > 3 ? 2 : 4) : (E8 > 2 ? 1
         };
         unsigned long long total;
         scan(sum, total);
-        const unsigned long long all_w = by_k ? total : (unsigned long long)(mass * 17592186044416.0f);
-        // p * all_w: whole units, and whether there is a rest
-        const unsigned long long p64 = by_p ? (top_p > 0.0f ? __float2ull_rz(top_p * 18446744073709551616.0f) : 0ull) : 0ull;
-        const unsigned long long goal = by_p ? __umul64hi(all_w, p64) : 0ull, rest = by_p ? all_w * p64 : 0ull;
-        const unsigned long long before = sum - w;
-        const bool keep = i < m && w >= floor_w && (i == 0 || !by_p || before < goal || (before == goal && rest));
+        const Share goal(by_k ? total : mass, by_p ? top_p : 0.0f);
+        const bool keep = i < m && w >= floor_w && (i == 0 || !by_p || goal.above(sum - w));
         // whether what may be kept lies among the sorted ones, where their number was a guess
-        done = by_k || (int)n < most || (by_p && (total > goal || (total == goal && !rest))) ||
-               (floor_w && __syncthreads_or(i == m - 1 && w < floor_w));
+        done = by_k || (int)n < most || (by_p && !goal.above(total)) || (floor_w && __syncthreads_or(i == m - 1 && w < floor_w));
         if (!keep) w = 0;
         if (done) {
           const int kept = __syncthreads_count(keep);      // the first ones
@@ -443,10 +501,8 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (E8 > 3 ? 2 : 4) : (E8 > 2 ? 1
     }
   }
 
-  // ---- where a count (MASS false) or a mass reaches `target` (+ `rest`, what its rounding left), by falling logit,
-  // among keys from `least` on
-  auto find = [&](auto mass, uint32_t least, float target, float rest) -> Found {
-    constexpr bool MASS = decltype(mass)::value;
+  // ---- where the count of values, by falling logit, reaches `target`
+  auto find = [&](float target) -> Found {
     uint32_t prefix = 0;
     float above = 0.0f, at = 0.0f;
 #pragma unroll 1
@@ -459,11 +515,8 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (E8 > 3 ? 2 : 4) : (E8 > 2 ? 1
       for (int i = 0; i < E8; ++i)
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const uint32_t key = key_of(x[i][k]) >> SH, bin = (key >> left) - (prefix << nb);
-          if (key >= least && bin < (1u << nb)) {
-            const float w = !MASS ? 1.0f : x[i][k] == big ? 1.0f : ex2((x[i][k] - big) * ch);
-            sm.bins[bin][threadIdx.x] += w;
-          }
+          const uint32_t bin = (key_of(x[i][k]) >> SH >> left) - (prefix << nb);
+          if (bin < (1u << nb)) sm.bins[bin][threadIdx.x] += 1.0f;
         }
       __syncthreads();
 #pragma unroll
@@ -475,7 +528,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (E8 > 3 ? 2 : 4) : (E8 > 2 ? 1
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         if (lane == 0) sm.part[b] = __float_as_uint(s);
       }
-      const uint32_t (*all)[32] = exchange();
+      const uint32_t (*all)[WIDE] = exchange();
       float own = 0.0f;
       for (int r = 0; r < n_cta; ++r) own += __uint_as_float(all[r][lane]);
       float sum = own;                                     // over this bin and the larger ones
@@ -484,10 +537,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (E8 > 3 ? 2 : 4) : (E8 > 2 ? 1
         const float v = __shfl_down_sync(0xffffffffu, sum, o);
         if (lane + o < 32) sum += v;
       }
-      const uint32_t reached = __ballot_sync(0xffffffffu, own > 0.0f && (above + sum) - target >= rest);
-      const uint32_t any = __ballot_sync(0xffffffffu, own > 0.0f);
-      // where rounding leaves the whole sum below the target, the last bin with something in it
-      const int b = reached ? 31 - __clz(reached) : __ffs(any) - 1;
+      const int b = 31 - __clz(__ballot_sync(0xffffffffu, own > 0.0f && above + sum >= target));
       const float over = __shfl_sync(0xffffffffu, sum, min(b + 1, 31));
       above += b < 31 ? over : 0.0f;
       at = __shfl_sync(0xffffffffu, own, b);
@@ -495,45 +545,86 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (E8 > 3 ? 2 : 4) : (E8 > 2 ? 1
     }
     return Found{prefix, above, at};
   };
-
-  float mass = 0.0f;                                       // of the kept ones at the border of top_k
+  unsigned long long beyond = 0;                           // the mass of equal ones that top_k leaves out
   if (by_k) {
-    const Found f = find(std::false_type{}, 0u, (float)top_k, 0.0f);
+    const Found f = find((float)top_k);
     least = f.key;
     ties = (uint32_t)max(1, top_k - (int)f.above);
     if ((float)ties >= f.at) ties = 0xFFFFFFFFu;
+    else beyond = weight(sm.roots, of_lead<SH>(least), big, ch, cl) * ((uint32_t)f.at - ties);
   }
   if (by_p) {
-    // the kept mass, in the order that find() sums it
-    float own = 0.0f;
-    const float xl = of_lead<SH>(least), wl = xl == big ? 1.0f : ex2((xl - big) * ch);
-#pragma unroll
-    for (int i = 0; i < E8; ++i)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t key = key_of(x[i][k]) >> SH;
-        if (key > least || (key == least && ties == 0xFFFFFFFFu)) own += x[i][k] == big ? 1.0f : ex2((x[i][k] - big) * ch);
+    // ---- the border's key: the bits of its place are fixed five at a time, until few values are left, then those of the key
+    constexpr int LEVELS = SH ? 2 : 4;
+    uint32_t prefix = 0, place = 0, key = 0;               // of the key, or before of the place; the place when it is fixed
+    int left = 32, place_left = 0, nb = 5;
+    bool keys = false, have = !by_k;
+    unsigned long long above = 0;                          // the mass of larger ones
+    Share goal(mass, top_p);
+#pragma unroll 1
+    for (;;) {
+      left -= nb;
+      if (!have) {
+        tally([&](float v) -> uint32_t {
+          const uint32_t k = key_of(v) >> SH, at = place_of(v);
+          const bool in = k >= least && (!keys || at >> place_left == place);
+          const uint32_t bin = ((keys ? k : at) >> left) - (prefix << nb);
+          return in && bin < (1u << nb) ? bin : 32u;
+        });
+        hist = collect(exchange(true));
+        if (by_k && !keys && left == 27) goal = Share(mass = over_lanes(hist) - beyond, top_p);
       }
+      have = false;
+      unsigned long long sum = hist;                       // over this bin and the larger ones
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) own += __shfl_xor_sync(0xffffffffu, own, o);
-    __syncthreads();
-    if (threadIdx.x < 32) sm.part[threadIdx.x] = 0;
-    __syncthreads();
-    if (lane == 0) sm.part[warp] = __float_as_uint(own);
-    const uint32_t (*all)[32] = exchange();
-    for (int r = 0; r < n_cta; ++r) mass += __uint_as_float(all[r][lane]);
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long v = __shfl_down_sync(0xffffffffu, sum, o);
+        if (lane + o < 32) sum += v;
+      }
+      const int b = 31 - __clz(__ballot_sync(0xffffffffu, hist && !goal.above(above + sum)));
+      const unsigned long long over = __shfl_sync(0xffffffffu, sum, min(b + 1, 31));
+      above += b < 31 ? over : 0ull;
+      prefix = (prefix << nb) + (uint32_t)b;
+      if (!keys && left > 32 - 5 * LEVELS) continue;
+      if (!keys) {
+        // the keys that are left
+        place = prefix;
+        place_left = left;
+        uint32_t lo = 0xFFFFFFFFu, hi = 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
-    if (ties != 0xFFFFFFFFu) mass += wl * (float)ties;
-    const float target = __fmul_rn(top_p, mass), rest = fmaf(top_p, mass, -target);
-    const Found f = find(std::true_type{}, least, target, rest);
-    // of the equal ones as many as begin below the target: exactly, where the weights are whole (all logits equal)
-    const float xt = of_lead<SH>(f.key), wt = xt == big ? 1.0f : ex2((xt - big) * ch), gap = target - f.above;
-    float n_eq = wt > 0.0f ? floorf(__fdiv_rn(gap, wt)) : 0.0f;
-    if (fmaf(-n_eq, wt, gap) + rest > 0.0f) n_eq += 1.0f;
-    const uint32_t n = n_eq >= 1.0f ? (n_eq < 1e9f ? (uint32_t)n_eq : 1000000000u) : 1u;
-    ties = f.key == least ? min(ties, n) : n;
-    least = f.key;
+        for (int i = 0; i < E8; ++i)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t v = key_of(x[i][k]) >> SH;
+            if (v >= least && place_of(x[i][k]) >> left == place) {
+              lo = min(lo, v);
+              hi = max(hi, v);
+            }
+          }
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        hi = __reduce_max_sync(0xffffffffu, hi);
+        if (lane == 0) {
+          sm.part[warp] = hi;
+          sm.part[WARPS + warp] = ~lo;
+        }
+        const uint32_t (*all)[WIDE] = exchange();
+        uint32_t most_of = 0;                              // the upper half of the lanes: inverted smallest
+        for (int r = 0; r < n_cta; ++r) most_of = max(most_of, all[r][lane]);
+        hi = __reduce_max_sync(0xffffffffu, lane < WARPS ? most_of : 0u);
+        lo = ~__reduce_max_sync(0xffffffffu, lane < WARPS ? 0u : most_of);
+        keys = true;
+        left = lo == hi ? 0 : 32 - __clz(lo ^ hi);
+        prefix = left < 32 ? hi >> left : 0u;
+      }
+      if (left == 0) break;
+      nb = min(5, left);
+    }
+    key = prefix;
+    // of the equal ones as many as begin below the goal
+    const unsigned long long w = weight(sm.roots, of_lead<SH>(key), big, ch, cl), gap = goal.units - above, whole = gap / w;
+    const uint32_t n = (uint32_t)max(1ull, whole + (goal.rest || whole * w < gap));
+    ties = key == least ? min(ties, n) : n;
+    least = key;
   }
   }
   // ---- how many values equal to the border lie before this warp's
@@ -550,7 +641,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (E8 > 3 ? 2 : 4) : (E8 > 2 ? 1
     if (threadIdx.x < 32) sm.part[threadIdx.x] = 0;
     __syncthreads();
     if (lane == 0) sm.part[warp] = eq;
-    const uint32_t (*all)[32] = exchange();
+    const uint32_t (*all)[WIDE] = exchange();
     for (int r = 0; r <= rank; ++r)
       if (r < rank || lane < warp) before += all[r][lane];
     before = __reduce_add_sync(0xffffffffu, before);
@@ -589,25 +680,11 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (E8 > 3 ? 2 : 4) : (E8 > 2 ? 1
       }
     }
   };
-  // f on every vector in turn. In rows that are not cut they go around and the first is worked on: unrolled, the code
-  // of all weights would be read from memory, once (256 rows of 151665: 264 us). Cut rows work on few.
-  auto around = [&]() {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float first_x = x[0][k];
-#pragma unroll
-      for (int i = 0; i + 1 < E8; ++i) x[i][k] = x[i + 1][k];
-      x[E8 - 1][k] = first_x;
-    }
-  };
+  // f on every vector in turn: they go around and the first is worked on. Unrolled, the code of all weights would be read
+  // from memory, once (256 rows of 151665, in us, so / unrolled: whole 177 / 264, with top_p alone 894 / 934).
   auto in_turn = [&](auto&& f) {
-    if constexpr (CUT) {
-#pragma unroll
-      for (int i = 0; i < E8; ++i) f(i, x[i]);
-    } else {
 #pragma unroll 1
-      for (int i = 0; i < E8; ++i, around()) f(i, x[0]);
-    }
+    for (int i = 0; i < E8; ++i, around()) f(i, x[0]);
   };
   unsigned long long own = 0;
   uint32_t eq = before;
@@ -624,7 +701,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (E8 > 3 ? 2 : 4) : (E8 > 2 ? 1
     sm.part[2 * warp] = (uint32_t)own;
     sm.part[2 * warp + 1] = (uint32_t)(own >> 32);
   }
-  const uint32_t (*all)[32] = exchange();
+  const uint32_t (*all)[WIDE] = exchange();
   unsigned long long total = 0, less = 0;                  // the kept mass, and what lies before this warp
   if (lane < WARPS) {
     for (int r = 0; r < n_cta; ++r) {
