@@ -603,7 +603,9 @@ enum { GPTQ_ACT_NONE = 0, GPTQ_ACT_RELU = 1, GPTQ_ACT_SILU = 2, GPTQ_ACT_GELU = 
  * with W_hat and the adapters, a = ids[t], as in gptq_adapter_linear (zeros in [0, 2^bits - 1], as
  * gptq_quantize_layer writes them). act(z) is z, max(z, 0), z / (1 + e^-z),
  * z Phi(z) (Phi the normal distribution's), or z / (1 + e^(-2 sqrt(2 / pi) (z + 0.044715 z^3))), the
- * tanh form of it. Sums are fp32; Y is rounded once.
+ * tanh form of it. Sums are fp32; Y is rounded once. act's own arithmetic errs by at most 5 * 2^-23 of |act(z)| for positive z;
+ * for negative z by (5 + 1.2 |z|) (silu), (5 + z^2 + |z|) (gelu) or (5 + 4.2 y) with y = 1.6 |z| (1 + 0.045 z^2) (gelu_tanh) times
+ * 2^-23 of it, and by 2^-126 |z|.
  *
  *   qweight, scales, zeros, m, d, bits, group_size, A, B, alpha, n_adapters, rank, ids
  *              as in gptq_adapter_linear. No adapters: n_adapters and rank 0.
@@ -634,7 +636,7 @@ gptq_status gptq_linear(const uint32_t* qweight, const float* scales, const floa
  *         counts as the larger. The largest logit is always kept.
  *   token: the first kept i, by index, with (the kept w up to and with i) > u * (all kept w)
  *
- * Weights are accurate to 2^-31 of themselves and 2^-44 of the largest, and summed as integers, those that top_p compares
+ * Weights are accurate to 2^-30 of themselves and 2^-44 of the largest, and summed as integers, those that top_p compares
  * too: a row's token does not depend on the rows beside it or on how it is split.
  *
  *   logits     device, rows x vocab of dtype (GPTQ_F32, _BF16 or _F16), row stride ld >= vocab elements, aligned

@@ -141,8 +141,11 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t* r) {
   }
 }
 
-// A value for each of many a thread, so by the fast exponential and quotient: their errors (2 + 1.2 |z| and 2 units of
-// fp32's last place) lie far below a bf16 output's rounding.
+// A value for each of many a thread, so by the fast exponential and quotient, which err by 2 + 1.2 y and 2 units of fp32's last
+// place, y the exponent's size. Counted in 2^-23 of |act(z)|: silu 5 + 1.2 |z|; gelu_tanh 5 + 4.2 y, y = 1.6 |z| (1 + 0.045 z^2), whose
+// exponent is itself off by 3 y; gelu (erfcf by 4, its argument's rounding by z^2 + |z|) 5 + z^2 + |z|; for positive z all of them 5
+// at most, as the exponential is the smaller part of 1 + e there. silu and gelu_tanh are 0 where their divisor passes 2^126.
+// bf16 outputs are rounded by 2^15 of these units; in fp32 outputs of large negative z, themselves next to 0, the errors are seen.
 __device__ __forceinline__ float activate(float z, int act) {
   switch (act) {
     case GPTQ_ACT_RELU: return z < 0.0f ? 0.0f : z;
