@@ -665,7 +665,8 @@ def gptq_add_rms_norm(X: torch.Tensor, R: Optional[torch.Tensor] = None, w: Opti
     d) float32, bfloat16 or float16, R may be None; w: (d,) float32 or None for ones. Returns (Y, R_out,
     scale): Y of out_dtype (default: X's type); R_out, s rounded to R's type (None without R; may be X or R
     itself); scale, None unless out_dtype is torch.float8_e4m3fn: then a row's values are Y * scale,
-    the 8-bit tokens of gptq_linear, with scale (T,) float32 the largest |value| / 448."""
+    the 8-bit tokens of gptq_linear, with scale (T,) float32 the largest |value| / 448. Squares and their sum
+    are float32: a row with values above 1.8e19, or whose squares' sum passes 3.4e38, gives zeros."""
     if stream is None:
         got = _calls.add_rms_norm(X, R, w, eps, R_out, Y, out_dtype, scale)
         if got is not None:
