@@ -165,8 +165,11 @@ class Decoder:
 
     def logits(self, tokens: torch.Tensor, step: Step, ids: Optional[torch.Tensor] = None) -> torch.Tensor:
         """tokens (T,) int32 or int64, the new tokens of all sequences one after another; returns (batch, vocab)
-        float32, the logits behind each sequence's last new token (of no meaning for a sequence without one)."""
-        X = self.embedding[tokens]
+        float32, the logits behind each sequence's last new token (of no meaning for a sequence without one). A
+        token outside the vocabulary, such as the -1 of a row that could not be drawn from, has NaN for its
+        embedding: the logits of its sequence are NaN, its next token is -1, and no other sequence is touched."""
+        inside = tokens.clamp(0, self.embedding.shape[0] - 1)
+        X = self.embedding[inside].masked_fill_((tokens != inside)[:, None], float("nan"))
         for layer in self.layers:
             X = layer.forward(X, step, ids)
         N, _, _ = gptq.gptq_add_rms_norm(X[(step.cu_q[1:] - 1).clamp(min=0)], None, self.w, eps=self.eps)
