@@ -172,7 +172,8 @@ class Decoder:
         X = self.embedding[inside].masked_fill_((tokens != inside)[:, None], float("nan"))
         for layer in self.layers:
             X = layer.forward(X, step, ids)
-        N, _, _ = gptq.gptq_add_rms_norm(X[(step.cu_q[1:] - 1).clamp(min=0)], None, self.w, eps=self.eps)
+        last = X[(step.cu_q[1:] - 1).clamp(min=0)] if X.shape[0] else X.new_zeros((step.kv_lens.shape[0], X.shape[1]))
+        N, _, _ = gptq.gptq_add_rms_norm(last, None, self.w, eps=self.eps)
         return gptq.gptq_linear(self.head, N, self.embedding.shape[0])
 
     def forward(self, tokens: torch.Tensor, step: Step, u: torch.Tensor, ids: Optional[torch.Tensor] = None,

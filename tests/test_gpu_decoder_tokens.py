@@ -50,3 +50,21 @@ def test_tokens_outside_the_vocabulary(dec, bad, eight_bit):
         for i in (0, 2):
             assert torch.equal(l0[i], l1[i]) and t0[i] == t1[i] and p0[i] == p1[i]
         assert torch.isnan(l1[1]).all() and int(t1[1]) == -1 and torch.isnan(p1[1])
+
+
+def test_a_step_without_tokens(dec):
+    model = model_of(dec, False)
+    batch = dec.Batch(40, 16)
+    for _ in range(2):
+        batch.add()
+    prompt = torch.arange(30, dtype=torch.int32, device="cuda")
+    before = model.logits(prompt, batch.extend([20, 10], 4))
+    pools = [layer.attention.cache.pool.clone() for layer in model.layers]
+    u = torch.zeros(2, device="cuda")
+    token, _ = model.forward(prompt[:0], batch.extend([0, 0], 4), u)
+    assert token.shape == (2,) and model.logits(prompt[:0], batch.extend([0, 0], 4)).shape == before.shape
+    assert all(torch.equal(layer.attention.cache.pool, p) for layer, p in zip(model.layers, pools))
+    one = model.logits(prompt[:1], batch.extend([0, 1], 4))
+    assert torch.isfinite(one).all()
+    torch.cuda.synchronize()
+    dec.gptq.gptq_device_check()
