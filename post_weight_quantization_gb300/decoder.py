@@ -169,10 +169,11 @@ class Decoder:
         token outside the vocabulary, such as the -1 of a row that could not be drawn from, has NaN for its
         embedding: the logits of its sequence are NaN, its next token is -1, and no other sequence is touched."""
         inside = tokens.clamp(0, self.embedding.shape[0] - 1)
-        X = self.embedding[inside].masked_fill_((tokens != inside)[:, None], float("nan"))
+        X = self.embedding.index_select(0, inside).masked_fill_((tokens != inside)[:, None], float("nan"))
         for layer in self.layers:
             X = layer.forward(X, step, ids)
-        last = X[(step.cu_q[1:] - 1).clamp(min=0)] if X.shape[0] else X.new_zeros((step.kv_lens.shape[0], X.shape[1]))
+        last = (step.cu_q[1:] - 1).clamp(min=0)
+        last = X.index_select(0, last) if X.shape[0] else X.new_zeros((last.shape[0], X.shape[1]))
         N, _, _ = gptq.gptq_add_rms_norm(last, None, self.w, eps=self.eps)
         return gptq.gptq_linear(self.head, N, self.embedding.shape[0])
 
