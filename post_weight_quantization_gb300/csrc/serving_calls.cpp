@@ -336,7 +336,7 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void *A = nullptr, *B = nullptr, *ids = nullptr, *alpha = nullptr;
     if (a[13] != Py_None) {
       const at::Tensor& t = c.on(a[13]);
-      if (t.dim() != 3) throw Decline{};
+      if (t.dim() != 3 || bytes) throw Decline{};
       na = t.size(0);
       rank = (int)t.size(1);
       A = c.dense(a[13], at::kBFloat16, {na, rank, d});
@@ -345,6 +345,10 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
       alpha = c.dense_or_null(a[16], at::kFloat, {na});
     } else if (a[14] != Py_None || a[15] != Py_None || a[16] != Py_None) {
       throw Decline{};
+    }
+    if (na == 0) {                                         // none to choose from: none
+      rank = 0;
+      A = B = ids = alpha = nullptr;
     }
     const at::Tensor Y = a[17] == Py_None ? c.make({T, m}, yt) : c.on(a[17]);
     const int64_t ldy = Call::rows(Y, yt, T, m);

@@ -765,6 +765,9 @@ def gptq_linear(q: "QuantizedLayer", X: torch.Tensor, m: int, x_scale: Optional[
     if Y is None:
         Y = _empty((T, m), ydt, dev, stream)
     ldy = _rows2(Y, "Y", (ydt,), T, m)
+    if n == 0:                                              # none to choose from: none
+        A = B = ids = alpha = None
+        rank = 0
     need = _lib.gptq_linear_workspace_size(m, d, bits, gs, T, 3 if bytes8 else 1, rank)
     if ws is None:
         ws = _workspace(need, dev, stream)
