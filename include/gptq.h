@@ -576,7 +576,7 @@ gptq_status gptq_kv_attention(const void* Q, int q_dtype, int64_t total_q, int n
  * in fp32; the norm is that of s before its rounding. With out_dtype GPTQ_E4M3 the row's scale is
  * max|y| / 448 and its codes are y / scale in e4m3, to nearest even: the 8-bit tokens of
  * gptq_linear. There a row of zeros (or one whose largest |s w| is below 2^-119) has a scale and codes of 0, one
- * with a NaN or an infinity a scale and codes of NaN. The squares are fp32 too: where their sum passes its range, as with
+ * with a NaN or an infinity among s or s w a scale and codes of NaN. The squares are fp32 too: where their sum passes its range, as with
  * a value above 1.8e19, y is 0 (the scale and the codes as well, r_out is not), and where mean(s^2) + eps lies below 2^-126, as with eps 0
  * and values below 1e-19, y loses bits, down to an infinite one.
  *

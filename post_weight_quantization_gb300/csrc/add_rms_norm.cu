@@ -149,8 +149,9 @@ __global__ void __launch_bounds__(MOST ? MOST : 32 * ROWS) add_rms_norm_kernel(P
   TO* y = reinterpret_cast<TO*>(p.y) + t * p.ldy;
   if constexpr (BYTES) {
     // a row of zeros (or of values whose reciprocal fp32 does not hold) has codes and a scale of 0, whatever n is there;
-    // a NaN, or an infinity times 0, is the row's maximum, and an infinity's n is 0: a scale and codes of NaN
-    const float top = big < 0x1p-119f ? 0.0f : big, scale = top == 0.0f ? 0.0f : __fdiv_rn(top * n, 448.0f);
+    // a NaN, or an infinity times 0, is the row's maximum, and an infinity's n is 0, or its difference from itself (of a product
+    // with a weight) no number: a scale and codes of NaN
+    const float top = big < 0x1p-119f ? 0.0f : big, scale = top == 0.0f ? 0.0f : __fdiv_rn(top * n, 448.0f) + (top - top);
     // v * 448 / top, with the quotient's remainder put back (Markstein): correctly rounded, so a quotient halfway
     // between two codes stays there. A power of two keeps the steps in fp32's range.
     const float f = top > 0x1p64f ? 0x1p-64f : top < 0x1p-40f ? 0x1p64f : 1.0f, f448 = 448.0f * f, tf = top * f;
