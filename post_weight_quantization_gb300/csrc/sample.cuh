@@ -348,6 +348,16 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (E8 > 3 ? 2 : 4) : (E8 > 2 ? 1
     for (int r = 0; r < n_cta; ++r) s += *reinterpret_cast<const unsigned long long*>(&all[r][MASSES + 2 * lane]);
     return s;
   };
+  // the bin in which the goal is reached, with `above` in larger ones of an earlier round; `sum`: over a lane's bin and the larger ones
+  auto bin_of_goal = [&](const Share& goal, unsigned long long above, unsigned long long& sum) -> int {
+    sum = hist;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long v = __shfl_down_sync(0xffffffffu, sum, o);
+      if (lane + o < 32) sum += v;
+    }
+    return 31 - __clz(__ballot_sync(0xffffffffu, hist && !goal.above(above + sum)));
+  };
   auto over_lanes = [](unsigned long long s) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -394,7 +404,10 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (E8 > 3 ? 2 : 4) : (E8 > 2 ? 1
     }
     if (lane == 31) sm.part[warp] = upto;
     const bool by_mass = by_p && !by_k;
-    if (by_mass) tally([&](float v) { return place_of(v) >> 27; });
+    if (by_mass) {
+      tally([&](float v) { return place_of(v) >> 27; });
+      if (threadIdx.x == 0) sm.part[MASSES + 64] = place_of(of_key(least)) >> 27;
+    }
     const uint32_t (*all)[WIDE] = exchange(by_mass);
     uint32_t n = 0, at = 0;                                // candidates, and those before this warp's
     for (int r = 0; r < n_cta; ++r) {
@@ -404,11 +417,17 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (E8 > 3 ? 2 : 4) : (E8 > 2 ? 1
     }
     n = __reduce_add_sync(0xffffffffu, n);
     at = __reduce_add_sync(0xffffffffu, at) + upto - count;
+    bool listed = n <= LIST;
     if (by_mass) {
       hist = collect(all);
       mass = over_lanes(hist);
+      // the border lies below every CTA's listed ones, and with it below the `most` largest: what would be listed is not enough
+      uint32_t bin = 0;
+      for (int r = 0; r < n_cta; ++r) bin = max(bin, all[r][MASSES + 64]);
+      unsigned long long sum;
+      listed = listed && (floor_w || bin_of_goal(Share(mass, top_p), 0ull, sum) >= (int)bin);
     }
-    if (n <= LIST) {
+    if (listed) {
       uint32_t list;                                       // the first CTA's
       asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(list) : "r"(smem_u32(few.list)));
       if (count) {
@@ -575,13 +594,8 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (E8 > 3 ? 2 : 4) : (E8 > 2 ? 1
         if (by_k && !keys && left == 27) goal = Share(mass = over_lanes(hist) - beyond, top_p);
       }
       have = false;
-      unsigned long long sum = hist;                       // over this bin and the larger ones
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long v = __shfl_down_sync(0xffffffffu, sum, o);
-        if (lane + o < 32) sum += v;
-      }
-      const int b = 31 - __clz(__ballot_sync(0xffffffffu, hist && !goal.above(above + sum)));
+      unsigned long long sum;
+      const int b = bin_of_goal(goal, above, sum);
       const unsigned long long over = __shfl_sync(0xffffffffu, sum, min(b + 1, 31));
       above += b < 31 ? over : 0ull;
       prefix = (prefix << nb) + (uint32_t)b;
@@ -591,12 +605,12 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (E8 > 3 ? 2 : 4) : (E8 > 2 ? 1
         place = prefix;
         place_left = left;
         uint32_t lo = 0xFFFFFFFFu, hi = 0;
-#pragma unroll
-        for (int i = 0; i < E8; ++i)
+#pragma unroll 1
+        for (int i = 0; i < E8; ++i, around())
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const uint32_t v = key_of(x[i][k]) >> SH;
-            if (v >= least && place_of(x[i][k]) >> left == place) {
+            const uint32_t v = key_of(x[0][k]) >> SH;
+            if (v >= least && place_of(x[0][k]) >> left == place) {
               lo = min(lo, v);
               hi = max(hi, v);
             }
