@@ -23,8 +23,8 @@
 // share the schedulers with the unpacking (about 11 instructions per 8 codes). Sixteen epilogue warps of 64 sums a
 // thread hide the loads from tensor memory; eight of 128 would take the registers of twice as many.
 //
-// Measured: 8192 x 8192, 4096 tokens 349 us in bf16 (1.58 PFLOP/s, 91 % of the library's sustained rate), 317 in e4m3 (1.74); 28672 x
-// 8192, 2500 tokens in e4m3 661 us (1.78 PFLOP/s). Bound: the issue slots that unpacking and epilogue share (e4m3 without
+// Measured: 8192 x 8192, 4096 tokens 345 us in bf16 (1.59 PFLOP/s, 92 % of the library's sustained rate), 320 in e4m3 (1.72); 28672 x
+// 8192, 2500 tokens in e4m3 663 us (1.77 PFLOP/s). Bound: the issue slots that unpacking and epilogue share (e4m3 without
 // the unpacking: 225 us), power beyond that.
 #include <algorithm>
 #include <type_traits>
@@ -62,8 +62,8 @@ struct Params {
 };
 
 // The unpacking warps form sets that take slabs in turn, so that one set's waits pass beside another's work: four, where
-// shared memory has room for as many slabs and their codes (8192 x 8192, 4096 tokens in bf16: 349 us, with two 375; at 4 bits
-// in e4m3, where it has room for three blocks of codes: 320, with two 317).
+// shared memory has room for as many slabs and their codes (8192 x 8192, 4096 tokens in bf16: 345 us, with two 375; at 4 bits
+// in e4m3, where it has room for three blocks of codes, two: 317 to 324, with four 320).
 template <int BITS, bool BYTES>
 struct Cfg {
   static constexpr int KC = BYTES ? 128 : 64;              // columns of a slab
@@ -324,11 +324,13 @@ linear_tiles_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int ntiles = p.mt * p.nt, step = (int)gridDim.x;
-  // slab n's place is free: the MMAs on slab n - STAGES are done
+  // Slab n's place is free: the MMAs on slab n - STAGES are done, the use of its barrier before u (none, and a new barrier's
+  // parity, for the first slabs).
   auto slab_free = [&](uint32_t n) -> bool {
-    const uint32_t u = n - STAGES;
-    return n < STAGES || mbar_wait_bounded(&empty[u % C::EMPTIES], (u / C::EMPTIES) & 1u, abort_flag);
+    const uint32_t u = n + (C::EMPTIES - STAGES);
+    return mbar_wait_bounded(&empty[u % C::EMPTIES], ((u / C::EMPTIES) & 1u) ^ 1u, abort_flag);
   };
+  const bool half = p.d_pad - p.d >= KC;                   // a row's last block has an empty half, a slab of nothing
 
   if (warp < UNPACK0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_ISSUE));
@@ -339,15 +341,18 @@ linear_tiles_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
       for (int tile = (int)blockIdx.x; ok && tile < ntiles; tile += step) {
         int rt, tt;
         tile_of(p, tile, rt, tt);
-        for (int k = 0; k < p.d_pad; k += KC, ++n) {
+        for (int k = 0; k < p.d; k += KC, ++n) {
           const uint32_t i = n % STAGES;
           if (!slab_free(n)) { ok = false; break; }
-          if (k >= p.d) {                                  // the empty half of the last block
-            if (lane == 0) mbar_arrive(&full[i]);
-          } else if (lane == 0) {
+          if (lane == 0) {
             mbar_arrive_expect_tx(&full[i], X_SLAB);
             tma_load_2d(xs + i * X_SLAB, &map_x, &full[i], k, tt * NTOK);
           }
+        }
+        if (half && ok) {
+          if (!slab_free(n)) { ok = false; break; }
+          if (lane == 0) mbar_arrive(&full[n % STAGES]);
+          ++n;
         }
       }
       if (!ok) { *abort_flag = 1; if (lane == 0) report_device_error(err, DEVERR_TIMEOUT); }
@@ -372,15 +377,11 @@ linear_tiles_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
         if (p.unit >= KC) {
           const int per = p.unit / KC;                     // slabs of a unit
           int in = 0;                                      // slabs of the present one so far
-          for (int k0 = 0; k0 < p.d_pad; k0 += KC, ++n) {
+          for (int k0 = 0; k0 < p.d; k0 += KC, ++n) {
             const uint32_t i = n % STAGES, dt = tmem + (unit_no % ND) * NTOK;
             const uint64_t ad = a0 + (uint64_t)(i * (A_SLAB / 16)), bd = b0 + (uint64_t)(i * (X_SLAB / 16));
-            if (in == 0 && k0 < p.d && !accumulator()) { ok = false; break; }
+            if (in == 0 && !accumulator()) { ok = false; break; }
             if (!mbar_wait_poll(&full[i], (n / STAGES) & 1u, abort_flag)) { ok = false; break; }
-            if (k0 >= p.d) {
-              umma_commit_by(&empty[n % C::EMPTIES], leader);
-              continue;
-            }
             umma(BYTES, dt, ad, bd, IDESC, in != 0, leader);
             if (k0 + KC <= p.d) {
 #pragma unroll
@@ -396,7 +397,7 @@ linear_tiles_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
             }
           }
         } else {                                           // several units in a slab
-          for (int k0 = 0; ok && k0 < p.d_pad; k0 += KC, ++n) {
+          for (int k0 = 0; ok && k0 < p.d; k0 += KC, ++n) {
             const uint32_t i = n % STAGES;
             const uint64_t ad = a0 + (uint64_t)(i * (A_SLAB / 16)), bd = b0 + (uint64_t)(i * (X_SLAB / 16));
             if (!mbar_wait_poll(&full[i], (n / STAGES) & 1u, abort_flag)) { ok = false; break; }
@@ -411,6 +412,11 @@ linear_tiles_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
             }
             if (ok) umma_commit_by(&empty[n % C::EMPTIES], leader);
           }
+        }
+        if (half && ok) {
+          if (!mbar_wait_poll(&full[n % STAGES], (n / STAGES) & 1u, abort_flag)) { ok = false; break; }
+          umma_commit_by(&empty[n % C::EMPTIES], leader);
+          ++n;
         }
       }
       if (!ok) { *abort_flag = 1; if (lane == 0) report_device_error(err, DEVERR_TIMEOUT); }
@@ -532,30 +538,31 @@ linear_tiles_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
         if (!mbar_wait_bounded(&c_full[cb % C::C_FULLS], (cb / C::C_FULLS) & 1u, abort_flag)) { fail(); break; }
         if (!slab_free(at)) { fail(); break; }
         const uint32_t sc = smem_u32(codes) + st * C::C_BYTES;
+        if (k < p.d) {                                     // else an empty half
 #pragma unroll
-        for (int j = 0; j < ROWS; ++j) {
-          if (k >= p.d) break;                             // the empty half of the last block
-          const int r = 32 * (ROWS * sub + j) + lane;
-          const uint32_t* zr = zeros + (zi * SCALES) * BM + r;
-          const uint32_t to = smem_u32(smem) + i * A_SLAB + r * 128, sw = (uint32_t)(r & 7);
+          for (int j = 0; j < ROWS; ++j) {
+            const int r = 32 * (ROWS * sub + j) + lane;
+            const uint32_t* zr = zeros + (zi * SCALES) * BM + r;
+            const uint32_t to = smem_u32(smem) + i * A_SLAB + r * 128, sw = (uint32_t)(r & 7);
 #pragma unroll
-          for (int q = 0; q < QS; ++q) {
-            uint32_t w[BITS];
-            const uint32_t z = zr[(((k + 32 * q) >> ush) & (SCALES - 1)) * BM];
-            lds_quarter<BITS>(sc, r, (k % KB) / 32 + q, w);
-            if constexpr (BYTES) {
-              uint32_t o[8];
-              spread32<BITS>(w, o);
+            for (int q = 0; q < QS; ++q) {
+              uint32_t w[BITS];
+              const uint32_t z = zr[(((k + 32 * q) >> ush) & (SCALES - 1)) * BM];
+              lds_quarter<BITS>(sc, r, (k % KB) / 32 + q, w);
+              if constexpr (BYTES) {
+                uint32_t o[8];
+                spread32<BITS>(w, o);
 #pragma unroll
-              for (int c = 0; c < 8; ++c) o[c] = minus_zero(o[c], z);
-              sts16(to + (((uint32_t)(2 * q) ^ sw) << 4), o[0], o[1], o[2], o[3]);
-              sts16(to + (((uint32_t)(2 * q + 1) ^ sw) << 4), o[4], o[5], o[6], o[7]);
-            } else {
-              uint32_t o[16];
-              unpack32<BITS>(w, z, o);
+                for (int c = 0; c < 8; ++c) o[c] = minus_zero(o[c], z);
+                sts16(to + (((uint32_t)(2 * q) ^ sw) << 4), o[0], o[1], o[2], o[3]);
+                sts16(to + (((uint32_t)(2 * q + 1) ^ sw) << 4), o[4], o[5], o[6], o[7]);
+              } else {
+                uint32_t o[16];
+                unpack32<BITS>(w, z, o);
 #pragma unroll
-              for (int c = 0; c < 4; ++c)
-                sts16(to + (((uint32_t)(4 * q + c) ^ sw) << 4), o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+                for (int c = 0; c < 4; ++c)
+                  sts16(to + (((uint32_t)(4 * q + c) ^ sw) << 4), o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+              }
             }
           }
         }
