@@ -1206,8 +1206,8 @@ static bool by_few(long long d, int group_size, long long T) {
 
 // Without adapters, more than 64 tokens may go by linear_tiles.cu, in 8 bits as they are where (code - zero) fits e4m3. A
 // block of 128 columns takes either kernel about 0.75 us a tile (of 256 tokens there, of 64 here, in up to eight slices of
-// d), so the one with fewer blocks one after another. 11008 x 4096, in us, here / there: 128 tokens 47 / 28, 256 tokens
-// 70 / 28.
+// d), so the one with fewer blocks one after another. 11008 x 4096, in us, here / there: 64 tokens 23 / 25, 128 tokens
+// 44 / 30, 256 tokens 64 / 31.
 static bool by_tiles(long long m, long long d, long long T) {
   if (T <= 64) return false;
   const adp::Plan pl = adp::plan_of(m, d, T, 8);

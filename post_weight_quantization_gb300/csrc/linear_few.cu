@@ -10,8 +10,9 @@
 // the block's columns on both sides. A block's sums, times the row's scale, are added in fp32; the warps' and then the
 // cluster's sums meet in shared memory in a fixed order.
 //
-// Bound: L1's lookups, a line a row for every 64 bytes of codes (a lane's fragment rows lie in eight lines), and latency;
-// 3.2 TB/s at 28672 x 8192 (one token, 41.0 us). Copies through shared memory (cp.async) took twice as long.
+// Bound: too little in flight. 28672 x 8192, one token: 41.0 us (3.2 TB/s), at 3.8 of 16 warps a scheduler, a third of whose time
+// is spent on loads; issue slots 46 %, L1 58 % of its peak (a line a row for every 64 bytes of codes: a lane's fragment rows lie
+// in eight lines), HBM 28 %. Copies through shared memory (cp.async) took twice as long.
 #include <algorithm>
 #include <type_traits>
 
