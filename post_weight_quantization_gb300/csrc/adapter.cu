@@ -474,10 +474,11 @@ adapter_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
   const int k_lo = blk0 * KB, k_hi = min(p.d, blk1 * KB);
   const int ad_units = (2 * p.rank + KB - 1) / KB;         // A blocks of one adapter
   constexpr uint32_t IDESC = umma_idesc(/*bf16*/ 1, false, false, BM, NP);
-  // block n's slot is free: the MMAs on block n - SLOTS are done
+  // Block n's slot is free: the MMAs on block n - SLOTS are done, the use of its barrier before u (none, and a new barrier's
+  // parity, for the first blocks).
   auto slot_free = [&](uint32_t n) -> bool {
-    const uint32_t u = n - SLOTS;
-    return n < SLOTS || mbar_wait_bounded(&empty[u % C::BARRIERS], (u / C::BARRIERS) & 1u, abort_flag);
+    const uint32_t u = n + (C::BARRIERS - SLOTS);
+    return mbar_wait_bounded(&empty[u % C::BARRIERS], ((u / C::BARRIERS) & 1u) ^ 1u, abort_flag);
   };
 
   if (warp < UNPACK0) {
