@@ -45,6 +45,7 @@ constexpr int MOST = 8, WHOLE = 3, CUTS = 8;             // CTAs of a cluster at
 constexpr int ROOTS = 2048, FRAC = 44;
 constexpr int LIST = 2048, GUESS = 256;                  // candidates at most; how many where top_k does not say
 constexpr int WIDE = 96, MASSES = 16;                    // words of a wide exchange, the first one of 32 masses in it
+static_assert(MASSES + 64 < WIDE && MASSES % 2 == 0, "a wide exchange holds 32 masses and a word");
 constexpr float T_MIN = 1e-30f, T_MAX = 1e30f;
 
 // 2^(i / 2048) in units of 2^-31, from square roots by Newton's iteration.
@@ -94,7 +95,7 @@ struct Few {
 };
 struct Common {
   uint32_t roots[ROOTS];
-  uint32_t part[WIDE];         // 32 words, or 16 and 32 masses
+  uint32_t part[WIDE];         // 32 words, or 16, 32 masses and one word
   uint32_t all[2][MOST][WIDE]; // the cluster's parts, two exchanges in turn
 };
 template <int NT, bool CUT>
@@ -348,7 +349,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (E8 > 3 ? 2 : 4) : (E8 > 2 ? 1
     for (int r = 0; r < n_cta; ++r) s += *reinterpret_cast<const unsigned long long*>(&all[r][MASSES + 2 * lane]);
     return s;
   };
-  // the bin in which the goal is reached, with `above` in larger ones of an earlier round; `sum`: over a lane's bin and the larger ones
+  // the bin in which the goal is reached, with `above` in larger ones of an earlier pass; `sum`: over a lane's bin and the larger ones
   auto bin_of_goal = [&](const Share& goal, unsigned long long above, unsigned long long& sum) -> int {
     sum = hist;
 #pragma unroll
@@ -575,7 +576,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (E8 > 3 ? 2 : 4) : (E8 > 2 ? 1
   if (by_p) {
     // ---- the border's key: the bits of its place are fixed five at a time, until few values are left, then those of the key
     constexpr int LEVELS = SH ? 2 : 4;
-    uint32_t prefix = 0, place = 0, key = 0;               // of the key, or before of the place; the place when it is fixed
+    uint32_t prefix = 0, place = 0;                        // leading bits of the key, at first of the place; the place's, once fixed
     int left = 32, place_left = 0, nb = 5;
     bool keys = false, have = !by_k;
     unsigned long long above = 0;                          // the mass of larger ones
@@ -633,7 +634,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (E8 > 3 ? 2 : 4) : (E8 > 2 ? 1
       if (left == 0) break;
       nb = min(5, left);
     }
-    key = prefix;
+    const uint32_t key = prefix;
     // of the equal ones as many as begin below the goal
     const unsigned long long w = weight(sm.roots, of_lead<SH>(key), big, ch, cl), gap = goal.units - above, whole = gap / w;
     const uint32_t n = (uint32_t)max(1ull, whole + (goal.rest || whole * w < gap));

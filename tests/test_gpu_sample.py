@@ -86,8 +86,8 @@ def kept_of(x, p, T, k=0):
 @pytest.mark.parametrize("k", [0, 100000])
 @pytest.mark.parametrize("v", [150000, 262144])
 def test_the_border_of_top_p_in_flat_rows(g, v, k):
-    """Each row's u draws the last kept token by index: its place says how much is kept. The sums are exact to 2^-32 of
-    a token's share; rows whose border is nearer than 2^-30 of the mass to a token's end are left out (none is expected)."""
+    """Each row's u draws the last kept token by index, and the border's token is the last one there is: drawn if it is kept. Weights
+    are exact to 2^-30, so a border may fall either way within that share of the mass from a token's end; here none is so near."""
     rng = np.random.default_rng(v + k)
     n = 12
     x = flat(rng, n, v)
